@@ -90,6 +90,9 @@ extern "C" {
 #define PULSE_OP_CAST_DIFF_LZ4 9 /* n = element count, aux = block_bytes           */
 #define PULSE_OP_APPLY_QUANT 10 /* n = element count of the view (segment index)   */
 
+#define PULSE_OP_GRAD_NORM 11  /* n = tile count (any: the size is fixed)          */
+#define PULSE_OP_ADAMW 12      /* n = tile count (pulse_segment_tiles)             */
+
 /* Bytes of workspace the op needs for the given size (0 if it needs none).
  * A workspace serves any number of calls of the op it was sized for, of any
  * size up to the one it was sized for; it must not be shared between
@@ -581,6 +584,91 @@ int pulse_cast_diff_segments(const pulse_segment *segs, int32_t nseg, const uint
 int pulse_apply_patch_segments(const pulse_view *views, int32_t nseg, const int32_t *patch_idx,
                                const uint16_t *patch_val, const int64_t *seg_offsets, int64_t max_count,
                                uint32_t *d_status, hipStream_t stream);
+
+/* ---- the trainer's step: gradient norm and AdamW over a list of tensors -----
+ * The masters that the codec casts and compares come from an Adam step whose
+ * size is about the learning rate ([Jiang talk] 07:17-10:37; [PULSE summary]
+ * "Osservazione Centrale").  These calls run that step over a whole list of
+ * tensors in one launch, with the tiling metadata of pulse_segment_tiles, and
+ * write the served BF16 view and the sparse patch in the same pass.
+ *
+ * One gradient of the list (device table of nseg entries, 24 bytes each). */
+typedef struct pulse_grad_segment {
+    const void *g;  /* [n] float32 or BF16 gradient (read), 16-byte aligned */
+    int64_t n;      /* elements, 1 .. 2^31 - 1                              */
+    int64_t tile0;  /* first tile of the tensor: pulse_segment_tiles        */
+} pulse_grad_segment;
+
+/* The norm of the whole list and the factor that clips it:
+ *   norm  = grad_mul * sqrt(sum of squares of all elements)   (float64 sums)
+ *   scale = grad_mul * min(1, max_norm / (norm + 1e-6)), or NaN when the norm
+ *           is not finite (pulse_adamw_step then skips the step).
+ *   segs, tile_seg, ntiles  as for pulse_cast_diff_segments.
+ *   grad_bf16  0: float32 gradients, 1: BF16.
+ *   grad_mul   a positive factor on every gradient (1 / the loss scale or the
+ *              number of micro-batches); max_norm > 0, infinity for no clip.
+ *   d_out      (device) float32[2]: scale, norm (written).
+ *   ws         pulse_workspace_bytes(PULSE_OP_GRAD_NORM, ntiles, 0), zeroed
+ *              before its first use (pulse_workspace_init).
+ * The result does not depend on the order in which workgroups run. */
+int pulse_grad_norm(const pulse_grad_segment *segs, int32_t nseg, const uint32_t *tile_seg, int64_t ntiles,
+                    int32_t grad_bf16, double grad_mul, double max_norm, float *d_out, void *ws, size_t ws_bytes,
+                    hipStream_t stream);
+
+/* One tensor of an AdamW step (device table of nseg entries, 80 bytes each);
+ * every pointer but the scales 16-byte aligned. */
+typedef struct pulse_adamw_segment {
+    float *p;            /* [n] float32 masters (updated)                       */
+    const void *g;       /* [n] float32 or BF16 gradient (read)                 */
+    void *m;             /* [n] first moment: float32, or E4M3 codes (updated)  */
+    void *v;             /* [n] second moment: float32, or E4M3 codes of its
+                            square root (updated)                               */
+    float *m_scale;      /* [ceil(n/256)] 8-bit states: a block's code 1.0 (updated) */
+    float *v_scale;      /* [ceil(n/256)]                                       */
+    uint16_t *b;         /* [n] served BF16 view (written; read for a patch), or
+                            NULL when no patch is asked for                     */
+    int64_t n;           /* elements, 1 .. 2^31 - 1                             */
+    int64_t tile0;       /* first tile of the tensor: pulse_segment_tiles       */
+    float lr_mult;       /* this tensor's factor on the learning rate           */
+    float weight_decay;  /* decoupled weight decay                              */
+} pulse_adamw_segment;
+
+typedef struct pulse_adamw_params {
+    double lr, beta1, beta2, eps; /* lr >= 0, 0 <= beta < 1, eps > 0            */
+    int64_t step;                 /* t >= 1, for the bias corrections           */
+    uint32_t seed;                /* 8-bit states: seed of the random rounding,
+                                     another one every step                     */
+    int32_t grad_bf16;            /* 0: float32 gradients, 1: BF16              */
+    int32_t state_bits;           /* 32 or 8                                    */
+    int32_t reserved;             /* 0                                          */
+} pulse_adamw_params;
+
+/* One AdamW step.  Per element, in float32 with each operation rounded once:
+ *   g  = grad * scale                       (scale = *d_scale, or 1)
+ *   m' = b1 m + (1 - b1) g;  v' = b2 v + (1 - b2) (g g)
+ *   p' = p (1 - lr' wd) - (lr' / (1 - b1^t)) (m' / (sqrt(v') / sqrt(1 - b2^t) + eps))
+ * with lr' = lr lr_mult and the constants (1 - b1, 1 / (1 - b1^t) and the like)
+ * computed in float64 and rounded; then b' = bf16(p') as pulse_cast_diff casts.
+ * 8-bit states: per block of 256 elements of a tensor, code = E4M3(x 448 / amax)
+ * rounded up or down at random by 20 bits of a mix of (element, tensor, seed),
+ * scale = amax / 448 (a block whose amax is below 2^-96 is stored as zero); v
+ * holds sqrt(v'), and a value above zero gets at least the smallest code.  The
+ * update itself uses m' and v' before they are rounded.  A block with Inf or
+ * NaN in it has unspecified codes and scales (the call still completes).
+ *   params     (host) read during the call only: a captured graph keeps them.
+ *   d_scale    (device float32) factor on the gradients, as pulse_grad_norm
+ *              writes it, or NULL; when it is not finite the step is skipped:
+ *              nothing changes and the patch is empty.
+ *   patch_idx, patch_val, patch_cap, seg_offsets  the patch of the view's
+ *              changed elements as pulse_cast_diff_segments writes it (b is
+ *              both the old and the new view), or all NULL.
+ *   d_status   PULSE_DS_CAPACITY, PULSE_DS_BADSEGMENT, PULSE_DS_WORKSPACE.
+ *   ws         pulse_workspace_bytes(PULSE_OP_ADAMW, ntiles, 0) when a patch is
+ *              asked for; ignored otherwise. */
+int pulse_adamw_step(const pulse_adamw_segment *segs, int32_t nseg, const uint32_t *tile_seg, int64_t ntiles,
+                     const pulse_adamw_params *params, const float *d_scale, int32_t *patch_idx,
+                     uint16_t *patch_val, int64_t patch_cap, int64_t *seg_offsets, uint32_t *d_status, void *ws,
+                     size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

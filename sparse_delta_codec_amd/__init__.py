@@ -24,6 +24,8 @@ __all__ = [
     "pulse_apply_patch_tiled", "patch_tile_count", "pulse_segment_tiles", "SegmentTable", "ViewTable",
     "pulse_cast_diff_segments", "pulse_apply_patch_segments", "lz4_decode_parse", "lz4_decode_apply",
     "pulse_cast_diff_lz4_noalloc", "PULSE_NOALLOC_SCRATCH_BYTES",
+    "PULSE_OP_GRAD_NORM", "PULSE_OP_ADAMW", "PULSE_ADAMW_BLOCK", "GradTable", "AdamWTable", "pulse_grad_norm",
+    "pulse_adamw_step",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -48,6 +50,8 @@ PULSE_OP_PATCH_UNPACK = 7
 PULSE_OP_CAST_DIFF_SEGMENTS = 8
 PULSE_OP_CAST_DIFF_LZ4 = 9
 PULSE_OP_APPLY_QUANT = 10
+PULSE_OP_GRAD_NORM = 11
+PULSE_OP_ADAMW = 12
 PULSE_DS_BADSEGMENT = 0x10
 PULSE_NOALLOC_SCRATCH_BYTES = 256 + 2 * 262144 * 8
 
@@ -90,7 +94,9 @@ _lib.pulse_apply_quant_plan_bytes.argtypes = [_I32]
 _lib.pulse_apply_quant_plan_bytes.restype = _I64
 _lib.pulse_apply_quant_plan.argtypes = [_P, _I32, _I64, _P, _I64, _P]
 _lib.pulse_apply_quant.argtypes = [_P, _I64, _P, _P, _P, _I64, _P, _I64, _P, _P, _SZ, _P]
-for _f in ("pulse_cast_diff_segments", "pulse_apply_patch_segments", "patch_pack", "patch_unpack",
+_lib.pulse_grad_norm.argtypes = [_P, _I32, _P, _I64, _I32, ctypes.c_double, ctypes.c_double, _P, _P, _SZ, _P]
+_lib.pulse_adamw_step.argtypes = [_P, _I32, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _P, _SZ, _P]
+for _f in ("pulse_grad_norm", "pulse_adamw_step", "pulse_cast_diff_segments", "pulse_apply_patch_segments", "patch_pack", "patch_unpack",
            "pulse_workspace_init", "pulse_cast_diff", "pulse_compact", "pulse_apply_patch",
            "xor_mask_apply", "lz4_encode_blocks", "lz4_decode_blocks", "fp8_block_quant",
            "fp8_view_delta", "fp8_view_apply", "pulse_loco_gate", "pulse_loco_accumulate",
@@ -659,3 +665,121 @@ def pulse_apply_patch_segments(views, patch_idx, patch_val, seg_offsets, d_statu
         _dev(patch_val, "patch_val", _U16), _dev(seg_offsets, "seg_offsets", torch.int64), max_count,
         _dev(d_status, "d_status", torch.int32), _stream(stream)), "pulse_apply_patch_segments")
 
+
+PULSE_ADAMW_BLOCK = 256  # elements that share one scale of an 8-bit state
+
+
+def _aligned(t, name):
+    if t is not None and t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned")
+
+
+class GradTable:
+    """Device tables of pulse_grad_norm for a list of gradients (GPU tensors, all
+    float32 or all bfloat16), prepared once and reused every step."""
+
+    def __init__(self, g, device="cuda"):
+        import numpy as np
+
+        if not g:
+            raise ValueError("g must be a list of at least one tensor")
+        self.grad_bf16 = int(g[0].dtype == torch.bfloat16)
+        for i, t in enumerate(g):
+            _dev(t, f"g[{i}]", torch.bfloat16 if self.grad_bf16 else torch.float32)
+            _aligned(t, f"g[{i}]")
+        self.ntiles, tile0, tile_seg = pulse_segment_tiles([t.numel() for t in g])
+        tab = np.array([[t.data_ptr(), t.numel(), t0] for t, t0 in zip(g, tile0)], np.int64)
+        self.nseg = len(g)
+        self.segs = torch.from_numpy(tab).to(device)
+        self.tile_seg = torch.from_numpy(tile_seg.view(np.int32)).to(device)
+        self._keep = list(g)
+
+
+def pulse_grad_norm(table, out, ws, max_norm=float("inf"), grad_mul=1.0, stream=None):
+    """out (float32[2]) = the clip factor and the norm of the table's gradients."""
+    _need(out, 8, "out")
+    wsp, wsb = _ws(ws)
+    _check(_lib.pulse_grad_norm(
+        table.segs.data_ptr(), table.nseg, table.tile_seg.data_ptr(), table.ntiles, table.grad_bf16, grad_mul,
+        max_norm, _dev(out, "out", torch.float32), wsp, wsb, _stream(stream)), "pulse_grad_norm")
+
+
+class _AdamWParams(ctypes.Structure):
+    """The layout of pulse_adamw_params."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("seed", ctypes.c_uint32),
+                ("grad_bf16", ctypes.c_int32), ("state_bits", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AdamWTable:
+    """Device tables of an AdamW step over a list of tensors, prepared once and
+    reused every step.  Lists of contiguous, 16-byte aligned GPU tensors:
+      p        float32 masters
+      g        gradients, all float32 or all bfloat16
+      m, v     moments: float32, or uint8 codes with m_scale and v_scale, lists of
+               float32 [ceil(n/256)] block scales (zeroed codes and scales are the
+               state before the first step)
+      b        BF16/uint16 served views, or None
+    lr_mult and weight_decay: one number, or one per tensor."""
+
+    def __init__(self, p, g, m, v, b=None, m_scale=None, v_scale=None, lr_mult=1.0, weight_decay=0.0, device="cuda"):
+        import numpy as np
+
+        if not p or any(x is not None and len(x) != len(p) for x in (g, m, v, b, m_scale, v_scale)):
+            raise ValueError("p, g, m, v (and b, m_scale, v_scale) must be lists of the same, non-zero length")
+        if (m_scale is None) != (v_scale is None):
+            raise ValueError("m_scale and v_scale go together")
+        nseg = len(p)
+        eight = m_scale is not None
+        self.state_bits = 8 if eight else 32
+        self.grad_bf16 = int(g[0].dtype == torch.bfloat16)
+        self.has_view = b is not None
+        state = torch.uint8 if eight else torch.float32
+        lr_mult, weight_decay = ([float(x)] * nseg if isinstance(x, (int, float)) else [float(y) for y in x]
+                                 for x in (lr_mult, weight_decay))
+        if len(lr_mult) != nseg or len(weight_decay) != nseg:
+            raise ValueError("lr_mult and weight_decay hold one number per tensor")
+        ns = [t.numel() for t in p]
+        self.ntiles, tile0, tile_seg = pulse_segment_tiles(ns)
+        tab = np.zeros((nseg, 10), np.int64)
+        kinds = (("p", p, torch.float32, 4), ("g", g, torch.bfloat16 if self.grad_bf16 else torch.float32,
+                                              2 if self.grad_bf16 else 4),
+                 ("m", m, state, 1 if eight else 4), ("v", v, state, 1 if eight else 4),
+                 ("m_scale", m_scale, torch.float32, 0), ("v_scale", v_scale, torch.float32, 0), ("b", b, _U16, 2))
+        for c, (name, tensors, dtype, size) in enumerate(kinds):
+            if tensors is None:
+                continue
+            for i, t in enumerate(tensors):
+                tab[i, c] = _dev(t, f"{name}[{i}]", dtype)
+                if size:
+                    _aligned(t, f"{name}[{i}]")
+                    _need(t, size * ns[i], f"{name}[{i}]")
+                else:
+                    _need(t, 4 * ((ns[i] + PULSE_ADAMW_BLOCK - 1) // PULSE_ADAMW_BLOCK), f"{name}[{i}]")
+        tab[:, 7], tab[:, 8] = ns, tile0
+        tab[:, 9] = np.stack([np.array(lr_mult, np.float32), np.array(weight_decay, np.float32)],
+                             1).view(np.int64)[:, 0]
+        self.nseg = nseg
+        self.segs = torch.from_numpy(tab).to(device)
+        self.tile_seg = torch.from_numpy(tile_seg.view(np.int32)).to(device)
+        self._keep = [None if x is None else list(x) for x in (p, g, m, v, b, m_scale, v_scale)]
+
+
+def pulse_adamw_step(table, step, lr, betas=(0.9, 0.999), eps=1e-8, d_scale=None, seed=0, d_status=None, ws=None,
+                     patch_idx=None, patch_val=None, seg_offsets=None, stream=None):
+    """One AdamW step over the table's tensors, with their served views and, when
+    patch_idx, patch_val and seg_offsets are given, the patch of the views'
+    changed elements (as pulse_cast_diff_segments writes it)."""
+    cap = 0 if patch_idx is None else patch_idx.numel()
+    if patch_idx is not None and not table.has_view:
+        raise ValueError("a patch needs the table's views (b)")
+    _need(patch_val, 2 * cap, "patch_val")
+    _need(seg_offsets, 8 * (table.nseg + 1), "seg_offsets")
+    _need(d_scale, 4, "d_scale")
+    params = _AdamWParams(lr, betas[0], betas[1], eps, step, seed & 0xFFFFFFFF, table.grad_bf16, table.state_bits, 0)
+    wsp, wsb = _ws(ws)
+    _check(_lib.pulse_adamw_step(
+        table.segs.data_ptr(), table.nseg, table.tile_seg.data_ptr(), table.ntiles, ctypes.byref(params),
+        _dev(d_scale, "d_scale", torch.float32), _dev(patch_idx, "patch_idx", torch.int32),
+        _dev(patch_val, "patch_val", _U16), cap, _dev(seg_offsets, "seg_offsets", torch.int64),
+        _dev(d_status, "d_status", torch.int32), wsp, wsb, _stream(stream)), "pulse_adamw_step")

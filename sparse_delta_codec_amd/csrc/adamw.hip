@@ -1,0 +1,580 @@
+// adamw.hip -- the trainer's step in front of the codec: the norm of a list of
+// gradients with the factor that clips them, and one AdamW step over a list of
+// tensors that writes the served BF16 view and, where asked, the sparse patch
+// of the view's changed elements.
+//
+// The mathematics, per element, in float32 with every operation rounded once
+// (no fused multiply-add: the library is built with -ffp-contract=off), so a
+// step is bit for bit the same wherever an element lies in a launch:
+//   g  = grad * scale
+//   m' = b1 m + (1 - b1) g          v' = b2 v + (1 - b2) (g g)
+//   u  = sqrt(v')
+//   p' = p (1 - lr wd) - (lr / (1 - b1^t)) (m' / (u / sqrt(1 - b2^t) + eps))
+//   b' = bf16(p')                   patch: the elements where b' != b
+// States in 8 bits: m and u, in blocks of 256 elements of one tensor, as
+// E4M3 codes times amax / 448.  u rather than v is kept because a square root
+// halves the exponents: 18 binades of u are 36 of v.  Codes are rounded up or
+// down at random, with the chance that makes the expectation exact: at
+// b2 = 0.999 a step moves u by at most 0.05%, far below half a code's spacing
+// (3% to 6%), so rounding to nearest would never let a code follow.  The random
+// bits are a mix of the element's place, its tensor's number and the caller's
+// seed.  A u above zero gets at least the smallest code: a zero would divide
+// the next update by eps alone.
+#include <type_traits>
+
+#include "compact.hpp"
+
+namespace pulse {
+
+struct AdamSeg {  // the layout of pulse_adamw_segment
+    float *p;
+    const void *g;
+    void *m;
+    void *v;
+    float *m_scale;
+    float *v_scale;
+    uint16_t *b;
+    int64_t n;
+    int64_t tile0;
+    float lr_mult;
+    float weight_decay;
+};
+
+struct GradSeg {  // the layout of pulse_grad_segment
+    const void *g;
+    int64_t n;
+    int64_t tile0;
+};
+
+struct AdamArgs {
+    const AdamSeg *segs;
+    const uint32_t *tile_seg;
+    const float *d_scale;
+    int32_t nseg;
+    uint32_t npieces;
+    uint32_t seed;
+    float lr, b1, omb1, b2, omb2, eps, inv_bc1, inv_sqrt_bc2;
+    // the patch (PATCH only)
+    int32_t *idx;
+    uint16_t *val;
+    int64_t cap;
+    int64_t *seg_offsets;
+    uint32_t *d_status;
+    WsHeader *hdr;
+    uint64_t *status;
+};
+
+constexpr int AW_BLOCK = 256;  // elements of a state block: one group of a wave
+constexpr float kTinyBlock = 0x1p-96f;  // blocks below are stored as zero (448 / amax would overflow)
+
+// 32 well-mixed bits of x: xor-shifts and products with odd constants (the
+// fractional bits of the square roots of 2 and 3).
+__device__ __forceinline__ uint32_t aw_mix(uint32_t x) {
+    x ^= x >> 16;
+    x *= 0x6A09E667u;
+    x ^= x >> 15;
+    x *= 0xBB67AE85u;
+    return x ^ (x >> 16);
+}
+
+// |x| * inv (at most 448 and a rounding) to an E4M3 code: the bits below the
+// code's last one are added to 20 random bits, the carry rounds up.  Below
+// 2^-6 the codes are evenly spaced, which adding 2^-6 turns into the spacing
+// of the binade above it.
+__device__ __forceinline__ uint32_t aw_code(float x, float inv, uint32_t rnd20) {
+    const float y = __builtin_fabsf(x) * inv;
+    const bool small = y < 0x1p-6f;
+    const float t = y + (small ? 0x1p-6f : 0.0f);
+    const uint32_t c = ((__float_as_uint(t) + rnd20) >> 20) - (small ? 968u : 960u);
+    return c < 126u ? c : 126u;
+}
+
+// wave-wide maximum of the absolute values' bits, in every lane (a NaN, whose
+// bits exceed every number's, wins)
+__device__ __forceinline__ uint32_t aw_wave_max(uint32_t v) {
+    v = wave_incl_max(v);
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+template <bool BF16G>
+struct GradVec;
+template <>
+struct GradVec<false> {
+    typedef u32x4 T;
+};
+template <>
+struct GradVec<true> {
+    typedef u32x2 T;
+};
+
+template <bool BF16G>
+__device__ __forceinline__ float grad_of(const typename GradVec<BF16G>::T &v, int k) {
+    if constexpr (BF16G) return __uint_as_float((k & 1) ? (v[k >> 1] & 0xFFFF0000u) : (v[k >> 1] << 16));
+    else return __uint_as_float(v[k]);
+}
+
+// Four consecutive elements of E bytes each at element e of a tensor of n
+// (FULL: all inside), as 32-bit words; elements past n read as zero.
+template <bool FULL, typename V>
+__device__ __forceinline__ V load4(const void *p, int64_t e, int64_t n) {
+    constexpr int E = sizeof(V) / 4;
+    const char *q = static_cast<const char *>(p) + e * E;
+    if (FULL || e + 3 < n) return __builtin_nontemporal_load(reinterpret_cast<const V *>(q));
+    union {
+        V v;
+        uint8_t c[sizeof(V)];
+    } u = {};
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        if (e + k < n) {
+            if constexpr (E == 4) reinterpret_cast<uint32_t *>(u.c)[k] = reinterpret_cast<const uint32_t *>(q)[k];
+            else if constexpr (E == 2) reinterpret_cast<uint16_t *>(u.c)[k] = reinterpret_cast<const uint16_t *>(q)[k];
+            else u.c[k] = reinterpret_cast<const uint8_t *>(q)[k];
+        }
+    return u.v;
+}
+
+template <bool FULL, typename V>
+__device__ __forceinline__ void store4v(void *p, int64_t e, int64_t n, V v) {
+    constexpr int E = sizeof(V) / 4;
+    char *q = static_cast<char *>(p) + e * E;
+    if (FULL || e + 3 < n) {
+        __builtin_nontemporal_store(v, reinterpret_cast<V *>(q));
+        return;
+    }
+    union {
+        V v;
+        uint8_t c[sizeof(V)];
+    } u;
+    u.v = v;
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        if (e + k < n) {
+            if constexpr (E == 4) reinterpret_cast<uint32_t *>(q)[k] = reinterpret_cast<uint32_t *>(u.c)[k];
+            else if constexpr (E == 2) reinterpret_cast<uint16_t *>(q)[k] = reinterpret_cast<uint16_t *>(u.c)[k];
+            else reinterpret_cast<uint8_t *>(q)[k] = u.c[k];
+        }
+}
+
+// What one wave needs of its tensor.
+struct AdamTensor {
+    AdamSeg s;
+    float scale, decay, size;
+    uint32_t key;
+};
+
+// Four groups of 256 elements of one wave (lane l: elements 4l .. 4l+3 of each
+// group, the first group at element e0 of the tensor): the step, its stores,
+// and the changed flags (bit 4g+k) and new view values for the patch.
+template <bool FULL, bool BF16G, bool EIGHT, bool PATCH>
+__device__ __forceinline__ uint32_t aw_chunk(const AdamArgs &a, const AdamTensor &t, int64_t e0, uint32_t nvp[8]) {
+    typedef typename GradVec<BF16G>::T GV;
+    const int64_t n = t.s.n;
+    const int64_t el = e0 + 4 * lane_id();
+    u32x4 pv[4];
+    GV gv[4];
+    u32x4 mv[4], vv[4];
+    uint32_t mc[4], vc[4];
+    u32x2 ov[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int64_t e = el + g * 256;
+        pv[g] = load4<FULL, u32x4>(t.s.p, e, n);
+        gv[g] = load4<FULL, GV>(t.s.g, e, n);
+        if constexpr (EIGHT) {
+            mc[g] = load4<FULL, uint32_t>(t.s.m, e, n);
+            vc[g] = load4<FULL, uint32_t>(t.s.v, e, n);
+        } else {
+            mv[g] = load4<FULL, u32x4>(t.s.m, e, n);
+            vv[g] = load4<FULL, u32x4>(t.s.v, e, n);
+        }
+        if constexpr (PATCH) ov[g] = load4<FULL, u32x2>(t.s.b, e, n);
+    }
+    // the blocks' scales: lane g of the wave holds block e0 / 256 + g
+    float ms = 0.0f, vs = 0.0f;
+    if constexpr (EIGHT) {
+        const int64_t blk = e0 / AW_BLOCK + (lane_id() & 3);
+        if (FULL || blk * AW_BLOCK < n) {
+            ms = t.s.m_scale[blk];
+            vs = t.s.v_scale[blk];
+        }
+    }
+    uint32_t flags = 0, mmax[4], umax[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float m4[4], v4[4];
+        if constexpr (EIGHT) {
+            const float sm = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(ms), g));
+            const float sv = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(vs), g));
+            const f32x2_t m01 = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc[g], false);
+            const f32x2_t m23 = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc[g], true);
+            const f32x2_t u01 = __builtin_amdgcn_cvt_pk_f32_fp8((int)vc[g], false);
+            const f32x2_t u23 = __builtin_amdgcn_cvt_pk_f32_fp8((int)vc[g], true);
+            m4[0] = m01.x * sm, m4[1] = m01.y * sm, m4[2] = m23.x * sm, m4[3] = m23.y * sm;
+            v4[0] = u01.x * sv, v4[1] = u01.y * sv, v4[2] = u23.x * sv, v4[3] = u23.y * sv;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v4[k] = v4[k] * v4[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m4[k] = __uint_as_float(mv[g][k]), v4[k] = __uint_as_float(vv[g][k]);
+        }
+        float p4[4], u4[4];
+        uint32_t mm = 0, um = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float gr = grad_of<BF16G>(gv[g], k) * t.scale;
+            m4[k] = m4[k] * a.b1 + gr * a.omb1;
+            v4[k] = v4[k] * a.b2 + (gr * gr) * a.omb2;
+            u4[k] = sqrtf(v4[k]);
+            const float upd = m4[k] / (u4[k] * a.inv_sqrt_bc2 + a.eps);
+            p4[k] = __uint_as_float(pv[g][k]) * t.decay - upd * t.size;
+            if constexpr (EIGHT) {
+                const uint32_t mb = __float_as_uint(m4[k]) & 0x7FFFFFFFu, ub = __float_as_uint(u4[k]) & 0x7FFFFFFFu;
+                mm = mb > mm ? mb : mm;
+                um = ub > um ? ub : um;
+            }
+        }
+        const int64_t e = el + g * 256;
+        store4v<FULL, u32x4>(t.s.p, e, n, u32x4{__float_as_uint(p4[0]), __float_as_uint(p4[1]), __float_as_uint(p4[2]),
+                                                __float_as_uint(p4[3])});
+        if (t.s.b) {
+            const uint32_t q0 = cast_pair(p4[0], p4[1]), q1 = cast_pair(p4[2], p4[3]);
+            store4v<FULL, u32x2>(t.s.b, e, n, u32x2{q0, q1});
+            if constexpr (PATCH) {
+                uint32_t f = (uint32_t)pair_flags(q0 ^ ov[g].x, q1 ^ ov[g].y);
+                if (!FULL) {
+                    const int64_t left = n - e;
+                    f &= left >= 4 ? 0xFu : (left > 0 ? (1u << left) - 1u : 0u);
+                }
+                flags |= f << (4 * g);
+                nvp[2 * g] = q0;
+                nvp[2 * g + 1] = q1;
+            }
+        }
+        if constexpr (EIGHT) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mv[g][k] = __float_as_uint(m4[k]), vv[g][k] = __float_as_uint(u4[k]);
+            mmax[g] = aw_wave_max(mm);
+            umax[g] = aw_wave_max(um);
+        } else {
+            store4v<FULL, u32x4>(t.s.m, e, n, u32x4{__float_as_uint(m4[0]), __float_as_uint(m4[1]),
+                                                    __float_as_uint(m4[2]), __float_as_uint(m4[3])});
+            store4v<FULL, u32x4>(t.s.v, e, n, u32x4{__float_as_uint(v4[0]), __float_as_uint(v4[1]),
+                                                    __float_as_uint(v4[2]), __float_as_uint(v4[3])});
+        }
+    }
+    if constexpr (EIGHT) {
+        // the eight blocks' scales in one pass of divisions: lane 2g + (0: m, 1: u)
+        const int q = lane_id() & 7;
+        uint32_t ab = 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            ab = q == 2 * g ? mmax[g] : ab;
+            ab = q == 2 * g + 1 ? umax[g] : ab;
+        }
+        const float amax = __uint_as_float(ab);
+        const bool live = !(amax < kTinyBlock);
+        const float scale = live ? amax / 448.0f : 0.0f;
+        const float inv = live ? 448.0f / amax : 0.0f;
+        const int64_t blk = e0 / AW_BLOCK + (q >> 1);
+        if (lane_id() < 8 && (FULL || blk * AW_BLOCK < n)) ((q & 1) ? t.s.v_scale : t.s.m_scale)[blk] = scale;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int64_t e = el + g * 256;
+            const float im = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(inv), 2 * g));
+            const float iu = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(inv), 2 * g + 1));
+            uint32_t cm = 0, cu = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t r = aw_mix((uint32_t)e + (uint32_t)k + t.key);
+                const float m = __uint_as_float(mv[g][k]), u = __uint_as_float(vv[g][k]);
+                const uint32_t c = aw_code(m, im, r & 0xFFFFFu) | ((mv[g][k] >> 24) & 0x80u);
+                uint32_t d = aw_code(u, iu, r >> 12);
+                if (d == 0 && u > 0.0f && iu > 0.0f) d = 1;
+                cm |= c << (8 * k);
+                cu |= d << (8 * k);
+            }
+            store4v<FULL, uint32_t>(t.s.m, e, n, cm);
+            store4v<FULL, uint32_t>(t.s.v, e, n, cu);
+        }
+    }
+    return flags;
+}
+
+// One workgroup per piece of 1024 CH elements x 4 waves (CH = 4: a whole tile,
+// CH = 1: a quarter).  With a patch the piece is a ticket (one atomic) and its
+// first entry comes from a look-back over the pieces before it, as in the
+// codec's own passes; without one it is the workgroup's number.
+template <int CH, bool BF16G, bool EIGHT, bool PATCH>
+__global__ __launch_bounds__(CD_THREADS) void k_adamw(AdamArgs a) {
+    constexpr int kPerTile = 4 / CH;
+    __shared__ uint32_t s_tile, s_tag;
+    __shared__ typename std::conditional<PATCH, CdShared, int>::type sh;
+    uint32_t piece = blockIdx.x, tag = 0;
+    if constexpr (PATCH) {
+        if (threadIdx.x == 0) {
+            uint32_t tile;
+            ws_begin(a.hdr, a.npieces, &tile, &tag);
+            s_tile = tile;
+            s_tag = tag;
+        }
+        __syncthreads();
+        piece = (uint32_t)__builtin_amdgcn_readfirstlane((int)s_tile);
+        tag = s_tag;
+        if (piece >= a.npieces) {  // inconsistent workspace state: touch nothing
+            if (threadIdx.x == 0) or_agent32(a.d_status, 8u /*PULSE_DS_WORKSPACE*/);
+            return;
+        }
+    }
+    const uint32_t tile = piece / kPerTile;
+    const uint32_t s = (uint32_t)__builtin_amdgcn_readfirstlane((int)a.tile_seg[tile]);
+    AdamTensor t{};
+    if (s < (uint32_t)a.nseg) t.s = a.segs[s];
+    const int64_t lt = (int64_t)tile - t.s.tile0;
+    const uintptr_t all = reinterpret_cast<uintptr_t>(t.s.p) | reinterpret_cast<uintptr_t>(t.s.g) |
+                          reinterpret_cast<uintptr_t>(t.s.m) | reinterpret_cast<uintptr_t>(t.s.v) |
+                          reinterpret_cast<uintptr_t>(t.s.b);
+    const bool ok = s < (uint32_t)a.nseg && t.s.n >= 1 && t.s.n <= 2147483647ll && lt >= 0 && lt * CD_TILE < t.s.n &&
+                    (all & 15u) == 0 && t.s.p && t.s.g && t.s.m && t.s.v && (!PATCH || t.s.b) &&
+                    (!EIGHT || (t.s.m_scale && t.s.v_scale));
+    t.scale = a.d_scale ? *a.d_scale : 1.0f;
+    const float lr = a.lr * t.s.lr_mult;
+    t.decay = 1.0f - lr * t.s.weight_decay;
+    t.size = lr * a.inv_bc1;
+    t.key = aw_mix(a.seed + (s + 1u) * 0x9E3779B1u);
+    const bool skip = !(__builtin_fabsf(t.scale) <= 3.402823466e38f);  // NaN or infinite: no step
+    const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
+    const int64_t wbase = lt * CD_TILE + (int64_t)(piece % kPerTile) * (CH * 4096) + (int64_t)w * (CH * 1024);
+    uint32_t nvp[PATCH ? CH * 8 : 8];
+    uint64_t flags = 0;
+    if (ok && !skip && wbase < t.s.n) {
+        if (wbase + CH * 1024 <= t.s.n) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                flags |= (uint64_t)aw_chunk<true, BF16G, EIGHT, PATCH>(a, t, wbase + c * 1024, nvp + (PATCH ? 8 * c : 0))
+                         << (16 * c);
+                sched_fence();
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                if (wbase + c * 1024 < t.s.n)
+                    flags |= (uint64_t)aw_chunk<false, BF16G, EIGHT, PATCH>(a, t, wbase + c * 1024,
+                                                                           nvp + (PATCH ? 8 * c : 0))
+                             << (16 * c);
+                sched_fence();
+            }
+        }
+    }
+    if constexpr (PATCH) {
+        const uint32_t wtot = wave_reduce_sum((uint32_t)__builtin_popcountll(flags));
+        if (l == 0) sh.wtot[w] = wtot;
+        __syncthreads();
+        uint32_t count = 0, wpre = 0;
+#pragma unroll
+        for (int i = 0; i < CD_THREADS / kWave; ++i) {
+            if (i < w) wpre += sh.wtot[i];
+            count += sh.wtot[i];
+        }
+        if (w == 0) {
+            bool failed = false;
+            const uint64_t pre = lookback_wave(a.status, piece, tag, count, &failed);
+            if (l == 0) {
+                if (failed) or_agent32(a.d_status, 8u /*PULSE_DS_WORKSPACE*/);
+                if (!ok) or_agent32(a.d_status, 0x10u /*PULSE_DS_BADSEGMENT*/);
+                sh.prefix = pre;
+                if (ok && lt == 0 && piece % kPerTile == 0) a.seg_offsets[s] = (int64_t)pre;
+                if (piece == a.npieces - 1) a.seg_offsets[a.nseg] = (int64_t)(pre + count);
+                if ((int64_t)(pre + count) > a.cap) or_agent32(a.d_status, 1u /*PULSE_DS_CAPACITY*/);
+            }
+        }
+        __syncthreads();
+        if (count != 0)
+            cd_pass2<4 * CH>(a, flags, nvp, wbase, 4 * l, (int64_t)sh.prefix + wpre, sh.sbi[w], sh.sbv[w]);
+    } else if (!ok && threadIdx.x == 0) {
+        or_agent32(a.d_status, 0x10u /*PULSE_DS_BADSEGMENT*/);
+    }
+}
+
+// ---- the norm of a list of gradients --------------------------------------------
+// Squares are summed in float64 (a float32 square overflows at 1.8e19 and
+// underflows below 1e-22), each workgroup's sum over its tiles goes to its own
+// slot, and the workgroup that finishes last adds the slots in their order: no
+// atomic's order reaches the result.
+constexpr int GN_THREADS = 256;
+constexpr int GN_MAX_BLOCKS = 2048;
+
+struct NormArgs {
+    const GradSeg *segs;
+    const uint32_t *tile_seg;
+    int32_t nseg;
+    uint32_t npieces;
+    double mul, max_norm;
+    float *out;
+    uint32_t *done;    // workgroups finished; the last one sets it back to zero
+    double *partial;
+};
+
+template <int CH, bool BF16G>
+__global__ __launch_bounds__(GN_THREADS) void k_grad_norm(NormArgs a) {
+    typedef typename GradVec<BF16G>::T GV;
+    constexpr int kPerTile = 4 / CH;
+    __shared__ double s_sum[GN_THREADS / kWave];
+    __shared__ uint32_t s_last;
+    double acc = 0.0;
+    for (uint32_t piece = blockIdx.x; piece < a.npieces; piece += gridDim.x) {
+        const uint32_t tile = piece / kPerTile;
+        const uint32_t s = a.tile_seg[tile];
+        GradSeg d{};
+        if (s < (uint32_t)a.nseg) d = a.segs[s];
+        const int64_t lt = (int64_t)tile - d.tile0;
+        if (!(d.g && (reinterpret_cast<uintptr_t>(d.g) & 15u) == 0 && lt >= 0 && lt * CD_TILE < d.n)) {
+            acc = __builtin_nan("");  // a broken table entry: the norm is not a number
+            continue;
+        }
+        const int64_t base = lt * CD_TILE + (int64_t)(piece % kPerTile) * (CH * 4096) + 4 * threadIdx.x;
+        GV v[CH * 4];
+        if (base - 4 * (int64_t)threadIdx.x + CH * 4096 <= d.n) {
+#pragma unroll
+            for (int g = 0; g < CH * 4; ++g) v[g] = load4<true, GV>(d.g, base + g * 1024, d.n);
+        } else {
+#pragma unroll
+            for (int g = 0; g < CH * 4; ++g) v[g] = load4<false, GV>(d.g, base + g * 1024, d.n);
+        }
+#pragma unroll
+        for (int g = 0; g < CH * 4; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const double x = (double)grad_of<BF16G>(v[g], k);
+                acc = __builtin_fma(x, x, acc);
+            }
+    }
+    acc = wave_reduce_sum(acc);
+    if (lane_id() == 0) s_sum[wave_id()] = acc;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double t = 0.0;
+#pragma unroll
+        for (int w = 0; w < GN_THREADS / kWave; ++w) t += s_sum[w];
+        __hip_atomic_store(&a.partial[blockIdx.x], t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint32_t before = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        s_last = before == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    double t = 0.0;
+    for (uint32_t i = threadIdx.x; i < gridDim.x; i += GN_THREADS)
+        t += __hip_atomic_load(&a.partial[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    t = wave_reduce_sum(t);
+    if (lane_id() == 0) s_sum[wave_id()] = t;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double tot = 0.0;
+#pragma unroll
+        for (int w = 0; w < GN_THREADS / kWave; ++w) tot += s_sum[w];
+        const double norm = __builtin_sqrt(tot) * a.mul;
+        const double coef = a.max_norm / (norm + 1e-6);
+        double scale = a.mul * (coef < 1.0 ? coef : 1.0);
+        if (!(norm <= 1.7976931348623157e308)) scale = __builtin_nan("");
+        a.out[0] = (float)scale;
+        a.out[1] = (float)norm;
+        st_agent32(a.done, 0u);
+    }
+}
+
+}  // namespace pulse
+
+using namespace pulse;
+
+extern "C" size_t pulse_adamw_ws_bytes(int64_t ntiles) {
+    return sizeof(WsHeader) + (size_t)(ntiles > 0 ? ntiles : 1) * 4 * sizeof(uint64_t);
+}
+
+extern "C" size_t pulse_grad_norm_ws_bytes(void) { return 256 + GN_MAX_BLOCKS * sizeof(double); }
+
+namespace {
+
+// Lists of fewer tiles than 4 per compute unit are cut into quarter tiles, so
+// that they spread over the chip.
+constexpr int64_t kWholeTiles = 1024;
+
+template <int CH, bool BF16G, bool EIGHT>
+void launch_adamw(const AdamArgs &a, hipStream_t stream) {
+    const dim3 grid(a.npieces), block(CD_THREADS);
+    if (a.idx) k_adamw<CH, BF16G, EIGHT, true><<<grid, block, 0, stream>>>(a);
+    else k_adamw<CH, BF16G, EIGHT, false><<<grid, block, 0, stream>>>(a);
+}
+
+template <int CH>
+void launch_adamw_types(const AdamArgs &a, bool bf16, bool eight, hipStream_t stream) {
+    if (bf16) {
+        if (eight) launch_adamw<CH, true, true>(a, stream);
+        else launch_adamw<CH, true, false>(a, stream);
+    } else {
+        if (eight) launch_adamw<CH, false, true>(a, stream);
+        else launch_adamw<CH, false, false>(a, stream);
+    }
+}
+
+}  // namespace
+
+extern "C" int pulse_launch_adamw(const void *segs, int32_t nseg, const uint32_t *tile_seg, int64_t ntiles,
+                                  const float *hyper, uint32_t seed, int32_t grad_bf16, int32_t state_bits,
+                                  const float *d_scale, int32_t *idx, uint16_t *val, int64_t cap,
+                                  int64_t *seg_offsets, uint32_t *d_status, void *ws, hipStream_t stream) {
+    AdamArgs a{};
+    a.segs = static_cast<const AdamSeg *>(segs);
+    a.tile_seg = tile_seg;
+    a.d_scale = d_scale;
+    a.nseg = nseg;
+    a.seed = seed;
+    a.lr = hyper[0];
+    a.b1 = hyper[1];
+    a.omb1 = hyper[2];
+    a.b2 = hyper[3];
+    a.omb2 = hyper[4];
+    a.eps = hyper[5];
+    a.inv_bc1 = hyper[6];
+    a.inv_sqrt_bc2 = hyper[7];
+    a.idx = idx;
+    a.val = val;
+    a.cap = cap;
+    a.seg_offsets = seg_offsets;
+    a.d_status = d_status;
+    a.hdr = reinterpret_cast<WsHeader *>(ws);
+    a.status = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + sizeof(WsHeader));
+    if (ntiles >= kWholeTiles) {
+        a.npieces = (uint32_t)ntiles;
+        launch_adamw_types<4>(a, grad_bf16 != 0, state_bits == 8, stream);
+    } else {
+        a.npieces = (uint32_t)(ntiles * 4);
+        launch_adamw_types<1>(a, grad_bf16 != 0, state_bits == 8, stream);
+    }
+    return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+
+extern "C" int pulse_launch_grad_norm(const void *segs, int32_t nseg, const uint32_t *tile_seg, int64_t ntiles,
+                                      int32_t grad_bf16, double mul, double max_norm, float *out, void *ws,
+                                      hipStream_t stream) {
+    NormArgs a{};
+    a.segs = static_cast<const GradSeg *>(segs);
+    a.tile_seg = tile_seg;
+    a.nseg = nseg;
+    a.mul = mul;
+    a.max_norm = max_norm;
+    a.out = out;
+    a.done = static_cast<uint32_t *>(ws);
+    a.partial = reinterpret_cast<double *>(static_cast<char *>(ws) + 256);
+    const bool whole = ntiles >= kWholeTiles;
+    const int64_t pieces = whole ? ntiles : ntiles * 4;
+    a.npieces = (uint32_t)pieces;
+    const dim3 grid((unsigned)(pieces < GN_MAX_BLOCKS ? pieces : GN_MAX_BLOCKS)), block(GN_THREADS);
+    if (whole) {
+        if (grad_bf16) k_grad_norm<4, true><<<grid, block, 0, stream>>>(a);
+        else k_grad_norm<4, false><<<grid, block, 0, stream>>>(a);
+    } else {
+        if (grad_bf16) k_grad_norm<1, true><<<grid, block, 0, stream>>>(a);
+        else k_grad_norm<1, false><<<grid, block, 0, stream>>>(a);
+    }
+    return hipGetLastError() == hipSuccess ? 0 : -5;
+}

@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 extern "C" {
@@ -64,12 +65,20 @@ int pulse_build_apply_quant_plan(const void *, int32_t, int64_t, void *, int64_t
 int pulse_launch_apply_quant(uint16_t *, int64_t, const int32_t *, const uint16_t *, const int64_t *, int64_t,
                              const void *, int64_t, uint32_t *, void *, hipStream_t);
 size_t pulse_apply_quant_ws_bytes(int64_t n);
+size_t pulse_adamw_ws_bytes(int64_t ntiles);
+size_t pulse_grad_norm_ws_bytes(void);
+int pulse_launch_adamw(const void *, int32_t, const uint32_t *, int64_t, const float *, uint32_t, int32_t, int32_t,
+                       const float *, int32_t *, uint16_t *, int64_t, int64_t *, uint32_t *, void *, hipStream_t);
+int pulse_launch_grad_norm(const void *, int32_t, const uint32_t *, int64_t, int32_t, double, double, float *, void *,
+                           hipStream_t);
 }
 
 namespace {
 
 constexpr int64_t kMaxIndexed = 2147483647;    // int32 patch indices
 constexpr int64_t kMaxPayload = (1ll << 39) - 2; // look-back value field
+
+constexpr int64_t kMaxTiles = 0x1FFFFFFF;  // list calls that cut a tile into four pieces count them in 31 bits
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -110,6 +119,8 @@ size_t pulse_workspace_bytes(int op, int64_t n, int64_t aux) {
         if (aux != 16384 && aux != 32768 && aux != 65536) return 0;
         return pulse_cast_diff_lz4_ws_bytes(n, (int32_t)aux);
     case PULSE_OP_APPLY_QUANT: return pulse_apply_quant_ws_bytes(n);
+    case PULSE_OP_GRAD_NORM: return pulse_grad_norm_ws_bytes();
+    case PULSE_OP_ADAMW: return pulse_adamw_ws_bytes(n);
     default: return 0;
     }
 }
@@ -500,6 +511,48 @@ int pulse_apply_quant(uint16_t *b, int64_t n, const int32_t *patch_idx, const ui
     if (!ws || ws_bytes < pulse_workspace_bytes(PULSE_OP_APPLY_QUANT, n, 0)) return PULSE_EWORKSPACE;
     return pulse_launch_apply_quant(b, n, patch_idx, patch_val, d_count, max_count, plan, nblocks, d_status, ws,
                                     stream);
+}
+
+}  // extern "C"
+
+extern "C" {
+
+static_assert(sizeof(pulse_grad_segment) == 24, "pulse_grad_segment is three 8-byte fields");
+static_assert(sizeof(pulse_adamw_segment) == 80, "pulse_adamw_segment is ten 8-byte fields");
+static_assert(sizeof(pulse_adamw_params) == 56, "pulse_adamw_params has no padding");
+
+int pulse_grad_norm(const pulse_grad_segment *segs, int32_t nseg, const uint32_t *tile_seg, int64_t ntiles,
+                    int32_t grad_bf16, double grad_mul, double max_norm, float *d_out, void *ws, size_t ws_bytes,
+                    hipStream_t stream) {
+    if (!segs || !tile_seg || !d_out || nseg < 1 || ntiles < nseg || (grad_bf16 != 0 && grad_bf16 != 1))
+        return PULSE_EINVAL;
+    if (!(grad_mul > 0.0) || !std::isfinite(grad_mul) || !(max_norm > 0.0)) return PULSE_EINVAL;
+    if (ntiles > kMaxTiles) return PULSE_ERANGE;
+    if (!ws || ws_bytes < pulse_grad_norm_ws_bytes()) return PULSE_EWORKSPACE;
+    return pulse_launch_grad_norm(segs, nseg, tile_seg, ntiles, grad_bf16, grad_mul, max_norm, d_out, ws, stream);
+}
+
+int pulse_adamw_step(const pulse_adamw_segment *segs, int32_t nseg, const uint32_t *tile_seg, int64_t ntiles,
+                     const pulse_adamw_params *params, const float *d_scale, int32_t *patch_idx,
+                     uint16_t *patch_val, int64_t patch_cap, int64_t *seg_offsets, uint32_t *d_status, void *ws,
+                     size_t ws_bytes, hipStream_t stream) {
+    if (!segs || !tile_seg || !params || !d_status || nseg < 1 || ntiles < nseg || patch_cap < 0) return PULSE_EINVAL;
+    const pulse_adamw_params &q = *params;
+    if (!(q.lr >= 0.0) || !std::isfinite(q.lr) || !(q.beta1 >= 0.0 && q.beta1 < 1.0) ||
+        !(q.beta2 >= 0.0 && q.beta2 < 1.0) || !(q.eps > 0.0) || !std::isfinite(q.eps) || q.step < 1 ||
+        (q.grad_bf16 != 0 && q.grad_bf16 != 1) || (q.state_bits != 32 && q.state_bits != 8) || q.reserved != 0)
+        return PULSE_EINVAL;
+    const bool patch = patch_idx || patch_val || seg_offsets;
+    if (patch && !(patch_idx && patch_val && seg_offsets)) return PULSE_EINVAL;
+    if (ntiles > kMaxTiles) return PULSE_ERANGE;
+    if (patch && (!ws || ws_bytes < pulse_adamw_ws_bytes(ntiles))) return PULSE_EWORKSPACE;
+    const double t = (double)q.step;
+    const float hyper[8] = {(float)q.lr,    (float)q.beta1, (float)(1.0 - q.beta1),
+                            (float)q.beta2, (float)(1.0 - q.beta2), (float)q.eps,
+                            (float)(1.0 / (1.0 - std::pow(q.beta1, t))),
+                            (float)(1.0 / std::sqrt(1.0 - std::pow(q.beta2, t)))};
+    return pulse_launch_adamw(segs, nseg, tile_seg, ntiles, hyper, q.seed, q.grad_bf16, q.state_bits, d_scale,
+                              patch_idx, patch_val, patch_cap, seg_offsets, d_status, ws, stream);
 }
 
 }  // extern "C"
