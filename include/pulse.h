@@ -670,6 +670,70 @@ int pulse_adamw_step(const pulse_adamw_segment *segs, int32_t nseg, const uint32
                      uint16_t *patch_val, int64_t patch_cap, int64_t *seg_offsets, uint32_t *d_status, void *ws,
                      size_t ws_bytes, hipStream_t stream);
 
+/* ---- low-rank adapters of many requests beside a shared projection ----------
+ * RL post-training also trains low-rank adapters over a frozen base model, whose
+ * update is small by construction ([Jiang talk], on adapters); the sampler adds
+ * them to the projection that the base weights give, a token at a time or by
+ * whole prompts, each token with the adapter of its request.
+ *
+ * For token t with adapter i = ids[t] (or none), x = its input row [K], y = its
+ * row of the projection's output [N]:
+ *   h = scale_i A_i x,   y += B_i^T h                                 (forward)
+ *   dh = scale_i B_i dy, dx += A_i^T dh, dA_i = sum dh x^T, dB_i = sum h dy^T
+ * Sums are held in float32.  h and dh are rounded to BF16 for the products with
+ * B and A, once; in dA and dB they enter as the sum of two BF16 (16 bits of
+ * mantissa).  y and dx are rounded once, after the addition.
+ *
+ * Layouts: x [T][ldx], y [T][ldy], dy, dx BF16 rows with any row stride that is
+ * a multiple of 8 elements; a [S][R][K] and b [S][R][N] BF16 (b is stored with
+ * the output axis last), adapters of a smaller rank padded with zero rows;
+ * scales [S] float32.  K and N are multiples of 8 up to 2^24, R a multiple of 8
+ * up to PULSE_LORA_MAX_RANK, S up to PULSE_LORA_MAX_ADAPTERS, T up to 2^24.
+ * Every pointer but ids and scales is 16-byte aligned. */
+#define PULSE_LORA_MAX_RANK 128
+#define PULSE_LORA_MAX_ADAPTERS 1024
+
+/* Bytes of a plan's buffer, of a saved h, and of the workspace of a forward pass
+ * (train = 0) or of forward and backward passes (train = 1); each serves any
+ * number of tokens up to n_tokens.  Negative: PULSE_EINVAL or PULSE_ERANGE. */
+int64_t pulse_lora_plan_bytes(int64_t n_tokens, int32_t n_adapters);
+int64_t pulse_lora_hidden_bytes(int64_t n_tokens, int64_t rank, int32_t n_adapters);
+int64_t pulse_lora_ws_bytes(int64_t n_tokens, int64_t k, int64_t n, int64_t rank, int32_t n_adapters, int32_t train);
+
+/* Groups the tokens by adapter, once for all the projections of a batch.
+ *   ids       [n_tokens] int32 adapter of each token (read), -1 for none.
+ *   plan      (device) buffer of pulse_lora_plan_bytes (written); it serves the
+ *             calls below with the same n_tokens and n_adapters.
+ *   d_status  PULSE_DS_BADINDEX when an id is neither -1 nor in [0, n_adapters)
+ *             (the token is taken to have no adapter). */
+int pulse_lora_plan(const int32_t *ids, int64_t n_tokens, int32_t n_adapters, void *plan, int64_t plan_bytes,
+                    uint32_t *d_status, hipStream_t stream);
+
+/* y += scale B^T A x for every token that has an adapter; other rows of y are
+ * neither read nor written.
+ *   h     buffer of pulse_lora_hidden_bytes that keeps h for the backward pass
+ *         (written), or NULL.
+ *   ws    pulse_lora_ws_bytes(n_tokens, k, n, rank, n_adapters, h != NULL),
+ *         zeroed before its first use (pulse_workspace_init). */
+int pulse_lora_forward(const uint16_t *x, int64_t ldx, const uint16_t *a, const uint16_t *b, const float *scales,
+                       const void *plan, int64_t plan_bytes, int64_t n_tokens, int64_t k, int64_t n, int64_t rank,
+                       int32_t n_adapters, uint16_t *y, int64_t ldy, void *h, int64_t h_bytes, void *ws,
+                       size_t ws_bytes, hipStream_t stream);
+
+/* The gradients of pulse_lora_forward.
+ *   h     as the forward pass with the same plan kept it (read).
+ *   dx    [T][lddx] BF16, updated: rows of tokens with an adapter are added to
+ *         (the shared projection's own gradient may be there), or NULL.
+ *   da    [S][R][K] float32, db [S][R][N] float32: written, zero for an adapter
+ *         without tokens; with accumulate = 1 added to.
+ *   ws    pulse_lora_ws_bytes(..., 1), zeroed before its first use; it may be
+ *         the forward pass's. */
+int pulse_lora_backward(const uint16_t *x, int64_t ldx, const uint16_t *dy, int64_t lddy, const uint16_t *a,
+                        const uint16_t *b, const float *scales, const void *plan, int64_t plan_bytes,
+                        int64_t n_tokens, int64_t k, int64_t n, int64_t rank, int32_t n_adapters, const void *h,
+                        int64_t h_bytes, uint16_t *dx, int64_t lddx, float *da, float *db, int32_t accumulate,
+                        void *ws, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

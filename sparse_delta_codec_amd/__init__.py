@@ -25,7 +25,8 @@ __all__ = [
     "pulse_cast_diff_segments", "pulse_apply_patch_segments", "lz4_decode_parse", "lz4_decode_apply",
     "pulse_cast_diff_lz4_noalloc", "PULSE_NOALLOC_SCRATCH_BYTES",
     "PULSE_OP_GRAD_NORM", "PULSE_OP_ADAMW", "PULSE_ADAMW_BLOCK", "GradTable", "AdamWTable", "pulse_grad_norm",
-    "pulse_adamw_step",
+    "pulse_adamw_step", "PULSE_LORA_MAX_RANK", "PULSE_LORA_MAX_ADAPTERS", "LoraPlan", "lora_workspace", "lora_hidden",
+    "pulse_lora_plan", "pulse_lora_forward", "pulse_lora_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -96,7 +97,17 @@ _lib.pulse_apply_quant_plan.argtypes = [_P, _I32, _I64, _P, _I64, _P]
 _lib.pulse_apply_quant.argtypes = [_P, _I64, _P, _P, _P, _I64, _P, _I64, _P, _P, _SZ, _P]
 _lib.pulse_grad_norm.argtypes = [_P, _I32, _P, _I64, _I32, ctypes.c_double, ctypes.c_double, _P, _P, _SZ, _P]
 _lib.pulse_adamw_step.argtypes = [_P, _I32, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _P, _SZ, _P]
-for _f in ("pulse_grad_norm", "pulse_adamw_step", "pulse_cast_diff_segments", "pulse_apply_patch_segments", "patch_pack", "patch_unpack",
+_lib.pulse_lora_plan_bytes.argtypes = [_I64, _I32]
+_lib.pulse_lora_hidden_bytes.argtypes = [_I64, _I64, _I32]
+_lib.pulse_lora_ws_bytes.argtypes = [_I64, _I64, _I64, _I64, _I32, _I32]
+for _f in ("pulse_lora_plan_bytes", "pulse_lora_hidden_bytes", "pulse_lora_ws_bytes"):
+    getattr(_lib, _f).restype = _I64
+_lib.pulse_lora_plan.argtypes = [_P, _I64, _I32, _P, _I64, _P, _P]
+_lib.pulse_lora_forward.argtypes = [_P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64,
+                                    _P, _SZ, _P]
+_lib.pulse_lora_backward.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I32, _P, _I64,
+                                     _P, _I64, _P, _P, _I32, _P, _SZ, _P]
+for _f in ("pulse_lora_plan", "pulse_lora_forward", "pulse_lora_backward", "pulse_grad_norm", "pulse_adamw_step", "pulse_cast_diff_segments", "pulse_apply_patch_segments", "patch_pack", "patch_unpack",
            "pulse_workspace_init", "pulse_cast_diff", "pulse_compact", "pulse_apply_patch",
            "xor_mask_apply", "lz4_encode_blocks", "lz4_decode_blocks", "fp8_block_quant",
            "fp8_view_delta", "fp8_view_apply", "pulse_loco_gate", "pulse_loco_accumulate",
@@ -783,3 +794,101 @@ def pulse_adamw_step(table, step, lr, betas=(0.9, 0.999), eps=1e-8, d_scale=None
         _dev(d_scale, "d_scale", torch.float32), _dev(patch_idx, "patch_idx", torch.int32),
         _dev(patch_val, "patch_val", _U16), cap, _dev(seg_offsets, "seg_offsets", torch.int64),
         _dev(d_status, "d_status", torch.int32), wsp, wsb, _stream(stream)), "pulse_adamw_step")
+
+
+PULSE_LORA_MAX_RANK = 128
+PULSE_LORA_MAX_ADAPTERS = 1024
+
+
+def _size(n, what):
+    """A size from the library, or its error."""
+    if n < 0:
+        raise RuntimeError(f"{what}: {_lib.pulse_status_string(int(n)).decode()} ({n})")
+    return int(n)
+
+
+class LoraPlan:
+    """The device buffer of a plan for batches of up to max_tokens tokens and
+    n_adapters adapters; n_tokens is the size of the batch it was last made for."""
+
+    def __init__(self, max_tokens, n_adapters, device="cuda"):
+        nbytes = _size(_lib.pulse_lora_plan_bytes(max_tokens, n_adapters), "pulse_lora_plan_bytes")
+        self.max_tokens, self.n_adapters, self.n_tokens = max_tokens, n_adapters, 0
+        self.buffer = torch.empty((max(nbytes, 16) + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def lora_workspace(n_tokens, k, n, rank, n_adapters, train=False, device="cuda"):
+    """A zeroed workspace for pulse_lora_forward, or with train for both passes."""
+    nbytes = _size(_lib.pulse_lora_ws_bytes(n_tokens, k, n, rank, n_adapters, int(train)), "pulse_lora_ws_bytes")
+    return torch.zeros((nbytes + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def lora_hidden(n_tokens, rank, n_adapters, device="cuda"):
+    """A buffer that keeps a forward pass's h for its backward pass."""
+    nbytes = _size(_lib.pulse_lora_hidden_bytes(n_tokens, rank, n_adapters), "pulse_lora_hidden_bytes")
+    return torch.empty((max(nbytes, 16) + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def _rows(t, rows, cols, name):
+    """A BF16 matrix [rows, cols] with contiguous columns and any row stride that is
+    a multiple of 8.  Returns (data pointer, row stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype not in _U16:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {_U16}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    if cols > 1 and rows > 0 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), t.stride(0) if rows > 1 else max(t.stride(0), cols)
+
+
+def _pools(a, b, scales, plan):
+    """Checks the adapter pools; returns (rank, k, n)."""
+    if a.dim() != 3 or b.dim() != 3 or a.shape[:2] != b.shape[:2] or a.shape[0] != plan.n_adapters:
+        raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} must be [{plan.n_adapters}, rank, ...]")
+    _need(scales, 4 * plan.n_adapters, "scales")
+    return a.shape[1], a.shape[2], b.shape[2]
+
+
+def pulse_lora_plan(plan, ids, d_status, stream=None):
+    """Groups the tokens of a batch by adapter: ids int32, -1 for no adapter."""
+    if ids.numel() > plan.max_tokens:
+        raise ValueError(f"ids holds {ids.numel()} tokens, the plan at most {plan.max_tokens}")
+    _need(d_status, 4, "d_status")
+    _check(_lib.pulse_lora_plan(_dev(ids, "ids", torch.int32), ids.numel(), plan.n_adapters, plan.buffer.data_ptr(),
+                                plan.buffer.numel(), _dev(d_status, "d_status", torch.int32), _stream(stream)),
+           "pulse_lora_plan")
+    plan.n_tokens = ids.numel()
+
+
+def pulse_lora_forward(x, a, b, scales, plan, y, ws, h=None, stream=None):
+    """y [tokens, n] += scale B^T A x for the tokens of the plan's batch: x [tokens, k],
+    a [adapters, rank, k], b [adapters, rank, n] BF16, scales float32; h keeps what the
+    backward pass needs."""
+    r, k, n = _pools(a, b, scales, plan)
+    px, ldx = _rows(x, plan.n_tokens, k, "x")
+    py, ldy = _rows(y, plan.n_tokens, n, "y")
+    wsp, wsb = _ws(ws)
+    _check(_lib.pulse_lora_forward(
+        px, ldx, _dev(a, "a", _U16), _dev(b, "b", _U16), _dev(scales, "scales", torch.float32), plan.buffer.data_ptr(),
+        plan.buffer.numel(), plan.n_tokens, k, n, r, plan.n_adapters, py, ldy, _dev(h, "h", torch.uint8),
+        0 if h is None else h.numel(), wsp, wsb, _stream(stream)), "pulse_lora_forward")
+
+
+def pulse_lora_backward(x, dy, a, b, scales, plan, h, dx, da, db, ws, accumulate=False, stream=None):
+    """The gradients of pulse_lora_forward: dx [tokens, k] BF16 is added to (None: not
+    wanted), da and db (float32, the pools' shapes) are written or, with accumulate,
+    added to."""
+    r, k, n = _pools(a, b, scales, plan)
+    px, ldx = _rows(x, plan.n_tokens, k, "x")
+    pdy, lddy = _rows(dy, plan.n_tokens, n, "dy")
+    pdx, lddx = (None, 0) if dx is None else _rows(dx, plan.n_tokens, k, "dx")
+    _need(da, 4 * a.numel(), "da")
+    _need(db, 4 * b.numel(), "db")
+    wsp, wsb = _ws(ws)
+    _check(_lib.pulse_lora_backward(
+        px, ldx, pdy, lddy, _dev(a, "a", _U16), _dev(b, "b", _U16), _dev(scales, "scales", torch.float32),
+        plan.buffer.data_ptr(), plan.buffer.numel(), plan.n_tokens, k, n, r, plan.n_adapters,
+        _dev(h, "h", torch.uint8), h.numel(), pdx, lddx, _dev(da, "da", torch.float32),
+        _dev(db, "db", torch.float32), int(accumulate), wsp, wsb, _stream(stream)), "pulse_lora_backward")

@@ -71,6 +71,17 @@ int pulse_launch_adamw(const void *, int32_t, const uint32_t *, int64_t, const f
                        const float *, int32_t *, uint16_t *, int64_t, int64_t *, uint32_t *, void *, hipStream_t);
 int pulse_launch_grad_norm(const void *, int32_t, const uint32_t *, int64_t, int32_t, double, double, float *, void *,
                            hipStream_t);
+int64_t pulse_lora_plan_size(int64_t T, int64_t S);
+int64_t pulse_lora_hidden_size(int64_t T, int64_t S, int64_t R);
+int64_t pulse_lora_ws_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t S, int32_t train);
+int pulse_launch_lora_plan(const int32_t *, int64_t, int32_t, void *, uint32_t *, hipStream_t);
+int pulse_launch_lora_forward(const uint16_t *, int64_t, const uint16_t *, const uint16_t *, const float *,
+                              const void *, int64_t, int64_t, int64_t, int64_t, int64_t, uint16_t *, int64_t, void *,
+                              void *, hipStream_t);
+int pulse_launch_lora_backward(const uint16_t *, int64_t, const uint16_t *, int64_t, const uint16_t *,
+                               const uint16_t *, const float *, const void *, int64_t, int64_t, int64_t, int64_t,
+                               int64_t, const void *, uint16_t *, int64_t, float *, float *, int32_t, void *,
+                               hipStream_t);
 }
 
 namespace {
@@ -78,6 +89,7 @@ namespace {
 constexpr int64_t kMaxIndexed = 2147483647;    // int32 patch indices
 constexpr int64_t kMaxPayload = (1ll << 39) - 2; // look-back value field
 
+constexpr int64_t kMaxLora = 1 << 24;          // tokens and widths of the adapter calls
 constexpr int64_t kMaxTiles = 0x1FFFFFFF;  // list calls that cut a tile into four pieces count them in 31 bits
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -553,6 +565,103 @@ int pulse_adamw_step(const pulse_adamw_segment *segs, int32_t nseg, const uint32
                             (float)(1.0 / std::sqrt(1.0 - std::pow(q.beta2, t)))};
     return pulse_launch_adamw(segs, nseg, tile_seg, ntiles, hyper, q.seed, q.grad_bf16, q.state_bits, d_scale,
                               patch_idx, patch_val, patch_cap, seg_offsets, d_status, ws, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// sizes shared by the adapter calls
+int check_lora_sizes(int64_t T, int64_t k, int64_t n, int64_t rank, int32_t n_adapters) {
+    if (T < 0 || n_adapters < 1 || rank < 8 || rank % 8 != 0 || k < 8 || k % 8 != 0 || n < 8 || n % 8 != 0)
+        return PULSE_EINVAL;
+    if (T > kMaxLora || k > kMaxLora || n > kMaxLora || rank > PULSE_LORA_MAX_RANK ||
+        n_adapters > PULSE_LORA_MAX_ADAPTERS)
+        return PULSE_ERANGE;
+    // workgroups of the widest launch
+    if ((T / 64 + n_adapters + 1) * (((k > n ? k : n) + 511) / 512 + 8) > 0x7FFFFFFF) return PULSE_ERANGE;
+    return PULSE_OK;
+}
+
+bool bad_stride(int64_t ld, int64_t cols) { return ld < cols || ld % 8 != 0; }
+
+}  // namespace
+
+extern "C" {
+
+int64_t pulse_lora_plan_bytes(int64_t n_tokens, int32_t n_adapters) {
+    const int rc = check_lora_sizes(n_tokens, 8, 8, 8, n_adapters);
+    return rc != PULSE_OK ? rc : pulse_lora_plan_size(n_tokens, n_adapters);
+}
+
+int64_t pulse_lora_hidden_bytes(int64_t n_tokens, int64_t rank, int32_t n_adapters) {
+    const int rc = check_lora_sizes(n_tokens, 8, 8, rank, n_adapters);
+    return rc != PULSE_OK ? rc : pulse_lora_hidden_size(n_tokens, n_adapters, rank);
+}
+
+int64_t pulse_lora_ws_bytes(int64_t n_tokens, int64_t k, int64_t n, int64_t rank, int32_t n_adapters, int32_t train) {
+    const int rc = check_lora_sizes(n_tokens, k, n, rank, n_adapters);
+    if (rc != PULSE_OK) return rc;
+    if (train != 0 && train != 1) return PULSE_EINVAL;
+    return pulse_lora_ws_size(n_tokens, k, n, rank, n_adapters, train);
+}
+
+int pulse_lora_plan(const int32_t *ids, int64_t n_tokens, int32_t n_adapters, void *plan, int64_t plan_bytes,
+                    uint32_t *d_status, hipStream_t stream) {
+    if (!plan || !d_status || (!ids && n_tokens != 0)) return PULSE_EINVAL;
+    const int rc = check_lora_sizes(n_tokens, 8, 8, 8, n_adapters);
+    if (rc != PULSE_OK) return rc;
+    if (!aligned16(plan)) return PULSE_EALIGN;
+    if (plan_bytes < pulse_lora_plan_size(n_tokens, n_adapters)) return PULSE_EWORKSPACE;
+    if (n_tokens == 0) return PULSE_OK;
+    return pulse_launch_lora_plan(ids, n_tokens, n_adapters, plan, d_status, stream);
+}
+
+int pulse_lora_forward(const uint16_t *x, int64_t ldx, const uint16_t *a, const uint16_t *b, const float *scales,
+                       const void *plan, int64_t plan_bytes, int64_t n_tokens, int64_t k, int64_t n, int64_t rank,
+                       int32_t n_adapters, uint16_t *y, int64_t ldy, void *h, int64_t h_bytes, void *ws,
+                       size_t ws_bytes, hipStream_t stream) {
+    const int rc = check_lora_sizes(n_tokens, k, n, rank, n_adapters);
+    if (rc != PULSE_OK) return rc;
+    if (n_tokens == 0) return PULSE_OK;
+    if (!x || !a || !b || !scales || !plan || !y || bad_stride(ldx, k) || bad_stride(ldy, n)) return PULSE_EINVAL;
+    if (!aligned16(x) || !aligned16(a) || !aligned16(b) || !aligned16(plan) || !aligned16(y) || !aligned16(h) ||
+        !aligned16(ws))
+        return PULSE_EALIGN;
+    if (plan_bytes < pulse_lora_plan_size(n_tokens, n_adapters) ||
+        (h && h_bytes < pulse_lora_hidden_size(n_tokens, n_adapters, rank)) || !ws ||
+        ws_bytes < (size_t)pulse_lora_ws_size(n_tokens, k, n, rank, n_adapters, h != nullptr))
+        return PULSE_EWORKSPACE;
+    return pulse_launch_lora_forward(x, ldx, a, b, scales, plan, n_tokens, k, n, rank, n_adapters, y, ldy, h, ws,
+                                     stream);
+}
+
+int pulse_lora_backward(const uint16_t *x, int64_t ldx, const uint16_t *dy, int64_t lddy, const uint16_t *a,
+                        const uint16_t *b, const float *scales, const void *plan, int64_t plan_bytes,
+                        int64_t n_tokens, int64_t k, int64_t n, int64_t rank, int32_t n_adapters, const void *h,
+                        int64_t h_bytes, uint16_t *dx, int64_t lddx, float *da, float *db, int32_t accumulate,
+                        void *ws, size_t ws_bytes, hipStream_t stream) {
+    const int rc = check_lora_sizes(n_tokens, k, n, rank, n_adapters);
+    if (rc != PULSE_OK) return rc;
+    if (!da || !db || (accumulate != 0 && accumulate != 1)) return PULSE_EINVAL;
+    if (!aligned16(da) || !aligned16(db)) return PULSE_EALIGN;
+    if (n_tokens == 0) {  // no token: the gradients are zero
+        if (accumulate) return PULSE_OK;
+        const int z = pulse_launch_fill_zero(da, (size_t)n_adapters * rank * k * 4, stream);
+        return z != PULSE_OK ? z : pulse_launch_fill_zero(db, (size_t)n_adapters * rank * n * 4, stream);
+    }
+    if (!x || !dy || !a || !b || !scales || !plan || !h || bad_stride(ldx, k) || bad_stride(lddy, n) ||
+        (dx && bad_stride(lddx, k)))
+        return PULSE_EINVAL;
+    if (!aligned16(x) || !aligned16(dy) || !aligned16(a) || !aligned16(b) || !aligned16(plan) || !aligned16(h) ||
+        !aligned16(dx) || !aligned16(ws))
+        return PULSE_EALIGN;
+    if (plan_bytes < pulse_lora_plan_size(n_tokens, n_adapters) ||
+        h_bytes < pulse_lora_hidden_size(n_tokens, n_adapters, rank) || !ws ||
+        ws_bytes < (size_t)pulse_lora_ws_size(n_tokens, k, n, rank, n_adapters, 1))
+        return PULSE_EWORKSPACE;
+    return pulse_launch_lora_backward(x, ldx, dy, lddy, a, b, scales, plan, n_tokens, k, n, rank, n_adapters, h, dx,
+                                      lddx, da, db, accumulate, ws, stream);
 }
 
 }  // extern "C"
