@@ -681,8 +681,8 @@ int pulse_adamw_step(const pulse_adamw_segment *segs, int32_t nseg, const uint32
  *   h = scale_i A_i x,   y += B_i^T h                                 (forward)
  *   dh = scale_i B_i dy, dx += A_i^T dh, dA_i = sum dh x^T, dB_i = sum h dy^T
  * Sums are held in float32.  h and dh are rounded to BF16 for the products with
- * B and A, once; in dA and dB they enter as the sum of two BF16 (16 bits of
- * mantissa).  y and dx are rounded once, after the addition.
+ * B and A, once; in dA and dB they enter as float32 (the sum of three BF16).  y
+ * and dx are rounded once, after the addition.
  *
  * Layouts: x [T][ldx], y [T][ldy], dy, dx BF16 rows with any row stride that is
  * a multiple of 8 elements; a [S][R][K] and b [S][R][N] BF16 (b is stored with
@@ -713,8 +713,8 @@ int pulse_lora_plan(const int32_t *ids, int64_t n_tokens, int32_t n_adapters, vo
  * neither read nor written.
  *   h     buffer of pulse_lora_hidden_bytes that keeps h for the backward pass
  *         (written), or NULL.
- *   ws    pulse_lora_ws_bytes(n_tokens, k, n, rank, n_adapters, h != NULL),
- *         zeroed before its first use (pulse_workspace_init). */
+ *   ws    pulse_lora_ws_bytes(n_tokens, k, n, rank, n_adapters, h != NULL); it
+ *         may hold anything before a call, and nothing is kept there after it. */
 int pulse_lora_forward(const uint16_t *x, int64_t ldx, const uint16_t *a, const uint16_t *b, const float *scales,
                        const void *plan, int64_t plan_bytes, int64_t n_tokens, int64_t k, int64_t n, int64_t rank,
                        int32_t n_adapters, uint16_t *y, int64_t ldy, void *h, int64_t h_bytes, void *ws,
@@ -726,8 +726,7 @@ int pulse_lora_forward(const uint16_t *x, int64_t ldx, const uint16_t *a, const 
  *         (the shared projection's own gradient may be there), or NULL.
  *   da    [S][R][K] float32, db [S][R][N] float32: written, zero for an adapter
  *         without tokens; with accumulate = 1 added to.
- *   ws    pulse_lora_ws_bytes(..., 1), zeroed before its first use; it may be
- *         the forward pass's. */
+ *   ws    pulse_lora_ws_bytes(..., 1); it may be the forward pass's. */
 int pulse_lora_backward(const uint16_t *x, int64_t ldx, const uint16_t *dy, int64_t lddy, const uint16_t *a,
                         const uint16_t *b, const float *scales, const void *plan, int64_t plan_bytes,
                         int64_t n_tokens, int64_t k, int64_t n, int64_t rank, int32_t n_adapters, const void *h,

@@ -149,8 +149,11 @@ def _need(t, nbytes, name):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The handle of a stream; None: the current device's current stream (asked for
+    directly, 0.3 us: torch.cuda.current_stream() builds a Stream object in 2.7 us)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 _U16 = (torch.uint16, torch.int16, torch.bfloat16)
@@ -818,9 +821,9 @@ class LoraPlan:
 
 
 def lora_workspace(n_tokens, k, n, rank, n_adapters, train=False, device="cuda"):
-    """A zeroed workspace for pulse_lora_forward, or with train for both passes."""
+    """A workspace for pulse_lora_forward, or with train for both passes."""
     nbytes = _size(_lib.pulse_lora_ws_bytes(n_tokens, k, n, rank, n_adapters, int(train)), "pulse_lora_ws_bytes")
-    return torch.zeros((nbytes + 15) // 16 * 16, dtype=torch.uint8, device=device)
+    return torch.empty((max(nbytes, 16) + 15) // 16 * 16, dtype=torch.uint8, device=device)
 
 
 def lora_hidden(n_tokens, rank, n_adapters, device="cuda"):

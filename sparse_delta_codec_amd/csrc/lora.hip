@@ -31,8 +31,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int LT = 64;            // places of a tile
-constexpr int LP_THREADS = 512;   // the plan's workgroup, two adapters a thread
-constexpr int LP_WAVES = LP_THREADS / kWave;
+constexpr int LP_ADAPTERS = 1024;  // most adapters
 
 // The plan's parts for T tokens and S adapters (32-bit words in one buffer).
 struct LoraPlan {
@@ -41,10 +40,17 @@ struct LoraPlan {
     int32_t *tile_count;  // [max_tiles] tokens of a tile
     int32_t *slot_tile;   // [S + 1] first tile of an adapter
     int32_t *order;       // [max_tiles * 64] token of a place, -1: empty
+    int32_t *group;       // [max_groups] tile * 4 + its 16 places, for every 16 that hold a token, -1: unused
 };
 
 __host__ __device__ inline int64_t lora_max_tiles(int64_t T, int64_t S) {
     const int64_t t = (T + LT - 1) / LT + S;
+    return T < t ? T : t;
+}
+
+// the 16 places that hold a token: one for each 16 tokens, and one more for each adapter
+__host__ __device__ inline int64_t lora_max_groups(int64_t T, int64_t S) {
+    const int64_t t = (T + 15) / 16 + S;
     return T < t ? T : t;
 }
 
@@ -58,116 +64,176 @@ __host__ __device__ inline LoraPlan lora_plan_parts(void *plan, int64_t T, int64
     p.tile_count = p.tile_slot + lora_round4(mt);
     p.slot_tile = p.tile_count + lora_round4(mt);
     p.order = p.slot_tile + lora_round4(S + 1);
+    p.group = p.order + mt * LT;
     return p;
 }
 
 inline int64_t lora_plan_size(int64_t T, int64_t S) {
     const int64_t mt = lora_max_tiles(T, S);
-    return 4 * (16 + 2 * lora_round4(mt) + lora_round4(S + 1) + mt * LT);
+    return 4 * (16 + 2 * lora_round4(mt) + lora_round4(S + 1) + lora_round4(lora_max_groups(T, S)) + mt * LT);
 }
 
 // ---- the plan: a stable counting sort by adapter -----------------------------
-// One workgroup.  Wave w owns the tokens [w T/8, (w+1) T/8) and counts them
-// per adapter in its own row of an LDS table; the rows' prefix sums give each
-// wave its first place for every adapter; then every wave deals its tokens out
-// in order, 64 at a time, ranking equal adapters with ballots.
-__global__ __launch_bounds__(LP_THREADS) void k_lora_plan(const int32_t *__restrict__ ids, int32_t T, int32_t S,
-                                                          LoraPlan p, int32_t max_tiles, uint32_t *d_status) {
-    extern __shared__ int32_t sh[];  // [8][S] counts, then first places
-    __shared__ int32_t s_scan[LP_WAVES];
+// One workgroup of NW waves.  Wave w owns a run of tokens and counts them per
+// adapter in its own row of an LDS table; the rows' prefix sums give each wave
+// its first place for every adapter; then every wave deals its tokens out in
+// order, 64 at a time, ranking equal adapters with ballots.  It is bound by
+// latency: the ids are read eight loads at a time, and one lane of each adapter
+// counts for the 64 (equal lanes' LDS atomics would queue).
+constexpr int LP_AHEAD = 8;
+
+// a lane's ids of the next tokens; -1 past the end
+__device__ __forceinline__ void read_ids(const int32_t *__restrict__ ids, int t, int t1, int (&id)[LP_AHEAD]) {
+#pragma unroll
+    for (int k = 0; k < LP_AHEAD; ++k) id[k] = t + k * kWave < t1 ? ids[t + k * kWave] : -1;
+}
+
+// the lanes whose id (-1: none) equals this lane's; bits: of the largest adapter's number
+__device__ __forceinline__ uint64_t equal_lanes(int id, int bits) {
+    uint64_t same = __ballot(id >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t m = __ballot((id >> b) & 1);
+        same &= ((id >> b) & 1) ? m : ~m;
+    }
+    return same;
+}
+
+template <int NW>
+__global__ __launch_bounds__(NW *kWave) void k_lora_plan(const int32_t *__restrict__ ids, int32_t T, int32_t S,
+                                                         LoraPlan p, int32_t max_tiles, int32_t max_groups,
+                                                         uint32_t *d_status) {
+    constexpr int kThreads = NW * kWave, kPer = LP_ADAPTERS / kThreads > 1 ? LP_ADAPTERS / kThreads : 1;
+    extern __shared__ int32_t sh[];  // [NW][S] counts, then first places; [S] counts; [S] first tiles; [S] first groups
+    __shared__ int32_t s_scan[NW];
+    int32_t *const s_cnt = sh + NW * S, *const s_tile = s_cnt + S, *const s_group = s_tile + S;
     const int tid = threadIdx.x, w = wave_id(), l = lane_id();
-    for (int i = tid; i < LP_WAVES * S; i += LP_THREADS) sh[i] = 0;
-    __syncthreads();
-    const int per = ((T + LP_WAVES - 1) / LP_WAVES + kWave - 1) / kWave * kWave;
+    const int per = ((T + NW - 1) / NW + kWave - 1) / kWave * kWave;
     const int t0 = w * per, t1 = t0 + per < T ? t0 + per : T;
+    const int bits = S > 1 ? 32 - __builtin_clz(S - 1) : 0;
+    int id[LP_AHEAD];
+    read_ids(ids, t0 + l, t1, id);
+    for (int i = tid; i < NW * S; i += kThreads) sh[i] = 0;
+    __syncthreads();
     bool bad = false;
-    for (int t = t0 + l; t < t1; t += kWave) {
-        const int id = ids[t];
-        if (id >= 0 && id < S) atomicAdd(&sh[w * S + id], 1);
-        else if (id != -1) bad = true;
+    for (int tb = t0; tb < t1; tb += LP_AHEAD * kWave) {
+        if (tb != t0) read_ids(ids, tb + l, t1, id);
+#pragma unroll
+        for (int k = 0; k < LP_AHEAD; ++k) {
+            if (tb + k * kWave >= t1) break;
+            const int a = id[k] >= 0 && id[k] < S ? id[k] : -1;
+            bad |= a != id[k] && id[k] != -1;
+            const uint64_t same = equal_lanes(a, bits);
+            if (a >= 0 && (same >> l) == 1ull) atomicAdd(&sh[w * S + a], __builtin_popcountll(same));
+        }
     }
     if (__ballot(bad) && l == 0) or_agent32(d_status, 2u /*PULSE_DS_BADINDEX*/);
     __syncthreads();
-    // adapters 2 tid and 2 tid + 1: their counts, their tiles, every wave's first place
-    int cnt[2] = {0, 0}, tiles[2], total;
+    // a thread's adapters: their counts, their tiles, every wave's first place
+    int cnt[kPer], tiles[kPer], sum = 0, gsum = 0, total, gtotal;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int a = 2 * tid + k;
+    for (int k = 0; k < kPer; ++k) {
+        const int a = kPer * tid + k;
+        cnt[k] = 0;
         if (a < S) {
 #pragma unroll
-            for (int i = 0; i < LP_WAVES; ++i) {
+            for (int i = 0; i < NW; ++i) {
                 const int c = sh[i * S + a];
                 sh[i * S + a] = cnt[k];
                 cnt[k] += c;
             }
         }
         tiles[k] = (cnt[k] + LT - 1) / LT;
+        sum += tiles[k];
+        gsum += (cnt[k] + 15) / 16;
     }
-    int first = block_excl_sum<LP_WAVES>(tiles[0] + tiles[1], s_scan, &total);
+    int first = block_excl_sum<NW>(sum, s_scan, &total);
+    int gfirst = block_excl_sum<NW>(gsum, s_scan, &gtotal);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int a = 2 * tid + k;
+    for (int k = 0; k < kPer; ++k) {
+        const int a = kPer * tid + k;
         if (a < S) {
 #pragma unroll
-            for (int i = 0; i < LP_WAVES; ++i) sh[i * S + a] += first * LT;
+            for (int i = 0; i < NW; ++i) sh[i * S + a] += first * LT;
+            s_cnt[a] = cnt[k];
+            s_tile[a] = first;
+            s_group[a] = gfirst;
             p.slot_tile[a] = first;
-            for (int i = 0; i < tiles[k]; ++i) {
-                p.tile_slot[first + i] = a;
-                p.tile_count[first + i] = cnt[k] - i * LT < LT ? cnt[k] - i * LT : LT;
-            }
             for (int i = cnt[k]; i < tiles[k] * LT; ++i) p.order[first * LT + i] = -1;
         }
         first += tiles[k];
+        gfirst += (cnt[k] + 15) / 16;
     }
     if (tid == 0) {
         p.slot_tile[S] = total;
         *p.ntiles = total;
     }
-    for (int i = total + tid; i < max_tiles; i += LP_THREADS) p.tile_slot[i] = -1;
     __syncthreads();
     volatile int32_t *mine = sh + w * S;
-    for (int tb = t0; tb < t1; tb += kWave) {
-        const int t = tb + l;
-        int id = t < t1 ? ids[t] : -1;
-        if (id < 0 || id >= S) id = -1;
-        uint64_t same = __ballot(id >= 0);
-        for (int b = 1; b < S; b <<= 1) {
-            const uint64_t m = __ballot(id & b);
-            same &= (id & b) ? m : ~m;
+    for (int tb = t0; tb < t1; tb += LP_AHEAD * kWave) {
+        if (t0 + LP_AHEAD * kWave < t1) read_ids(ids, tb + l, t1, id);
+#pragma unroll
+        for (int k = 0; k < LP_AHEAD; ++k) {
+            if (tb + k * kWave >= t1) break;
+            const int a = id[k] >= 0 && id[k] < S ? id[k] : -1;
+            const uint64_t same = equal_lanes(a, bits);
+            if (a >= 0) {
+                const int place = mine[a] + (int)lanes_below(same);
+                p.order[place] = tb + k * kWave + l;
+                // the last of the equal lanes moves the adapter's next place on (all have read it:
+                // a wave's LDS accesses are in order)
+                if ((same >> l) == 1ull) mine[a] = place + 1;
+            }
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         }
-        if (id >= 0) {
-            const uint32_t rank = lanes_below(same);
-            const int place = mine[id] + (int)rank;
-            p.order[place] = t;
-            // the last of the equal lanes moves the adapter's next place on (all have read it:
-            // a wave's LDS accesses are in order)
-            if ((same >> l) == 1ull) mine[id] = place + 1;
+    }
+    // the adapter of a tile (or of 16 places): the last one that begins at or before it (an empty
+    // one begins where the next does)
+    const auto owner = [&](const int32_t *begin, int i) {
+        int lo = 0, hi = S;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (begin[mid] <= i) lo = mid;
+            else hi = mid;
         }
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        return lo;
+    };
+    for (int i = tid; i < max_tiles; i += kThreads) {
+        const int a = i < total ? owner(s_tile, i) : -1;
+        p.tile_slot[i] = a;
+        if (a >= 0) {
+            const int c = s_cnt[a] - (i - s_tile[a]) * LT;
+            p.tile_count[i] = c < LT ? c : LT;
+        }
+    }
+    for (int i = tid; i < max_groups; i += kThreads) {
+        int v = -1;
+        if (i < gtotal) {
+            const int a = owner(s_group, i);
+            v = s_tile[a] * 4 + i - s_group[a];
+        }
+        p.group[i] = v;
     }
 }
 
 // ---- what the kernels share -----------------------------------------------------
-// h (or dh) of every place, in the three forms its readers want: BF16
-// [place][Rp] for expand; for outer, whose sums over tokens go out in float32,
-// the float32 value as the sum of two BF16 (16 bits of mantissa), each [Rp][place].
+// h (or dh) of every place, in the forms its readers want: BF16 [place][Rp] for
+// expand; for outer, whose sums over tokens go out in float32, the float32 value
+// as the exact sum of three BF16 (8 bits of mantissa each), each [Rp][place].
 struct LoraHidden {
     uint16_t *rows;
-    uint16_t *hi;
-    uint16_t *lo;
+    uint16_t *part[3];
 };
 
 inline int64_t lora_hidden_size(int64_t T, int64_t S, int64_t R, bool train) {
     const int64_t rp = (R + 15) / 16 * 16, places = lora_max_tiles(T, S) * LT;
-    return places * rp * 2 * (train ? 3 : 1);
+    return places * rp * 2 * (train ? 4 : 1);
 }
 
 inline LoraHidden lora_hidden_parts(void *h, int64_t T, int64_t S, int64_t R, bool train) {
     const int64_t rp = (R + 15) / 16 * 16, places = lora_max_tiles(T, S) * LT;
     LoraHidden p;
     p.rows = static_cast<uint16_t *>(h);
-    p.hi = train ? p.rows + places * rp : nullptr;
-    p.lo = train ? p.hi + places * rp : nullptr;
+    for (int i = 0; i < 3; ++i) p.part[i] = train ? p.rows + (i + 1) * places * rp : nullptr;
     return p;
 }
 
@@ -179,18 +245,21 @@ __device__ __forceinline__ u32x4 ld16(const uint16_t *p) { return *reinterpret_c
 
 __device__ __forceinline__ bf16x8 as_bf(const u32x4 &v) { return __builtin_bit_cast(bf16x8, v); }
 
-// h's four values of ranks r .. r+3 at one place, in its three forms
+// h's four values of ranks r .. r+3 at one place, in its forms
 __device__ __forceinline__ void store_hidden(const LoraHidden &h, int64_t place, int64_t places, int rp, int r,
                                              const f32x4 &v) {
     const uint32_t p0 = cast_pair(v[0], v[1]), p1 = cast_pair(v[2], v[3]);
     *reinterpret_cast<u32x2 *>(h.rows + place * rp + r) = u32x2{p0, p1};
-    if (h.hi) {
+    if (h.part[0]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t top = (i < 2 ? p0 : p1) >> (16 * (i & 1)) & 0xFFFFu;
             const float rest = v[i] - __uint_as_float(top << 16);
-            h.hi[(r + i) * places + place] = (uint16_t)top;
-            h.lo[(r + i) * places + place] = (uint16_t)cast_pair(rest, 0.0f);
+            const uint32_t mid = cast_pair(rest, 0.0f);
+            const int64_t at = (r + i) * places + place;
+            h.part[0][at] = (uint16_t)top;
+            h.part[1][at] = (uint16_t)mid;
+            h.part[2][at] = (uint16_t)cast_pair(rest - __uint_as_float(mid << 16), 0.0f);
         }
     }
 }
@@ -203,171 +272,255 @@ struct ShrinkArgs {
     const float *scales;
     LoraPlan plan;
     LoraHidden h;
-    float *partial;     // [ksplit][places][Rp] (ksplit > 1)
-    uint32_t *done;     // [tiles * 4] (ksplit > 1) workgroups finished; the last one sets it back to zero
+    float *partial;  // [gridDim.y][places][Rp] (PART)
     int64_t places;
-    int32_t T, S, C, R, ksplit;
+    int32_t T, S, C, R, max_tiles, max_groups;
 };
 
-// A workgroup takes 16 places of a tile; its four waves, and ksplit workgroups,
-// share the long axis.  Matrix instruction: rows = ranks, columns = places, 32
-// elements of the long axis, so both operands are 16-byte pieces of rows.
-template <int RT>
-__global__ __launch_bounds__(256) void k_lora_shrink(ShrinkArgs g) {
-    __shared__ f32x4 s_acc[3][RT][kWave];
-    __shared__ uint32_t s_last;
-    const int tile = blockIdx.x >> 2, sub = blockIdx.x & 3;
+// A wave's piece of LDS: rows of 128 columns, sixteen 16-byte pieces each, which
+// it writes as they were loaded (four rows an instruction, 256 contiguous bytes
+// each) and reads as a matrix instruction wants them (16 rows, 64 bytes each).
+// Piece p of row r lies at p ^ r, so that neither side has two lanes in a bank.
+__device__ __forceinline__ int staged(int row, int piece) { return row * 16 + (piece ^ (row & 15)); }
+
+// Waves of a workgroup: as many as their LDS leaves room for.
+constexpr int shrink_waves(int rt, int mt) { return rt + mt <= 2 ? 16 : (rt + mt <= 4 ? 8 : 4); }
+
+// A workgroup takes 16 MT places of a tile; its waves, and with PART gridDim.y
+// workgroups, share the long axis in steps of 128 columns, and the waves' sums
+// are added through LDS, in their order.  Matrix instruction: rows = ranks,
+// columns = places, 32 elements of the long axis.  Read as the instruction wants
+// them, 64 bytes of 16 rows at once, rows came in at 10 to 15 bytes a clock and
+// compute unit; 256 bytes of 4 rows, turned round in LDS, are not held back.
+// The rows of the next step are read while these are multiplied.
+template <int RT, int MT, bool PART>
+__global__ __launch_bounds__(shrink_waves(RT, MT) * kWave) void k_lora_shrink(ShrinkArgs g) {
+    constexpr int NW = shrink_waves(RT, MT);
+    __shared__ u32x4 s_stage[NW][(MT + RT) * 256];
+    __shared__ int s_tok[16 * MT];
+    // 16 places: from the plan's list, which leaves out the empty ones (a workgroup that finds nothing
+    // to do still takes the LDS of a whole one)
+    const int at = MT == 1 ? g.plan.group[blockIdx.x] : (int)blockIdx.x * MT;
+    if ((uint32_t)at >= (uint32_t)g.max_tiles * 4) return;
+    const int tile = at >> 2, sub = at & 3;
     const int slot = g.plan.tile_slot[tile];
     if ((uint32_t)slot >= (uint32_t)g.S || sub * 16 >= g.plan.tile_count[tile]) return;
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), c16 = l & 15, q = l >> 4;
-    const int64_t place = (int64_t)tile * LT + sub * 16 + c16;
-    const int tok = token_of(g.plan.order[place], g.T);
-    const uint16_t *px = g.x + (int64_t)(tok < 0 ? 0 : tok) * g.ldx + q * 8;
-    const uint16_t *pa = g.a + ((int64_t)slot * g.R + c16) * g.C + q * 8;
-    const int steps = (g.C + 31) / 32, parts = g.ksplit * 4;
-    const int part = blockIdx.y * 4 + w;
-    const int per = (steps + parts - 1) / parts;
-    const int k0 = part * per * 32, k1 = (part + 1) * per * 32 < g.C ? (part + 1) * per * 32 : g.C;
-    f32x4 acc[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) acc[rt] = f32x4{0, 0, 0, 0};
-#pragma unroll 4
-    for (int k = k0; k < k1; k += 32) {
-        const bool in = k + q * 8 < g.C;
-        u32x4 xv = {0, 0, 0, 0};
-        if (in && tok >= 0) xv = ld16(px + k);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            u32x4 av = {0, 0, 0, 0};
-            if (in && rt * 16 + c16 < g.R) av = ld16(pa + (int64_t)rt * 16 * g.C + k);
-            acc[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(av), as_bf(xv), acc[rt], 0, 0, 0);
-        }
-    }
-    if (w > 0) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) s_acc[w - 1][rt][l] = acc[rt];
-    }
-    __syncthreads();
-    const int rp = RT * 16;
+    const int64_t place0 = (int64_t)at * 16;
     const float scale = g.scales[slot];
-    if (w == 0) {
+    const uint16_t *const pa = g.a + ((int64_t)slot * g.R + q) * g.C;
+    const uint16_t *px[MT][4];
+    int tok[MT][4];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            f32x4 v = acc[rt];
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 3; ++i) v += s_acc[i][rt][l];
-            if (g.ksplit == 1) {
-                store_hidden(g.h, place, g.places, rp, rt * 16 + q * 4, v * scale);
-            } else {
-                float *o = g.partial + ((int64_t)blockIdx.y * g.places + place) * rp + rt * 16 + q * 4;
+        for (int i = 0; i < 4; ++i) tok[m][i] = token_of(g.plan.order[place0 + m * 16 + i * 4 + q], g.T);
+    const int some = __builtin_amdgcn_readfirstlane(tok[0][0]) < 0 ? 0 : __builtin_amdgcn_readfirstlane(tok[0][0]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    __hip_atomic_store(o + i, v[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (w == 0 && c16 == 0) s_tok[m * 16 + i * 4 + q] = tok[m][i];
+            px[m][i] = g.x + (int64_t)(tok[m][i] < 0 ? some : tok[m][i]) * g.ldx;  // an empty place's sums are dropped
+        }
+    const int steps = (g.C + 127) / 128, stride = NW * (int)gridDim.y;
+    u32x4 xr[MT][4], ar[RT][4];
+    auto load = [&](int s) {
+        const int k = s * 128 + c16 * 8, kc = k < g.C ? k : 0;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ar[rt][i] = u32x4{0, 0, 0, 0};
+                if (rt * 16 + i * 4 < g.R) ar[rt][i] = ld16(pa + (int64_t)(rt * 16 + i * 4) * g.C + kc);
+            }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xr[m][i] = ld16(px[m][i] + kc);
+        if (s * 128 + 128 > g.C && k >= g.C) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ar[rt][i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xr[m][i] = u32x4{0, 0, 0, 0};
+        }
+    };
+    f32x4 acc[MT][RT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) acc[m][rt] = f32x4{0, 0, 0, 0};
+    u32x4 *const st = s_stage[w];
+    int s = (int)blockIdx.y * NW + w;
+    if (s < steps) load(s);
+    for (; s < steps; s += stride) {
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // the last step's reads are done
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st[m * 256 + staged(i * 4 + q, c16)] = xr[m][i];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st[(MT + rt) * 256 + staged(i * 4 + q, c16)] = ar[rt][i];
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // the lanes' pieces are visible to the wave
+        if (s + stride < steps) load(s + stride);
+        sched_fence();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            u32x4 xv[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) xv[m] = st[m * 256 + staged(c16, k * 4 + q)];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const u32x4 av = st[(MT + rt) * 256 + staged(c16, k * 4 + q)];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    acc[m][rt] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(av), as_bf(xv[m]), acc[m][rt], 0, 0, 0);
             }
         }
-        if (g.ksplit > 1) {
-            // the partial sums were written through to memory; they have arrived before the count goes up
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            if (l == 0) s_last = add_agent32(&g.done[blockIdx.x], 1u) == (uint32_t)g.ksplit - 1;
-        }
     }
-    if (g.ksplit == 1) return;
-    __syncthreads();
-    if (!s_last) return;
-    // the last workgroup of the 16 places adds the parts in their order
-    for (int i = threadIdx.x; i < 16 * RT * 4; i += 256) {
-        const int64_t pl = (int64_t)tile * LT + sub * 16 + (i & 15);
-        const int r = (i >> 4) * 4;
-        f32x4 v = {0, 0, 0, 0};
-        for (int s = 0; s < g.ksplit; ++s) {
-            const float *o = g.partial + ((int64_t)s * g.places + pl) * rp + r;
+    __syncthreads();  // the stages are free: the waves' sums go there
+    f32x4 *const sums = reinterpret_cast<f32x4 *>(&s_stage[0][0]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] += __hip_atomic_load(o + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        store_hidden(g.h, pl, g.places, rp, r, v * scale);
+    for (int c = 0; c < RT * MT; ++c) sums[(w * RT * MT + c) * kWave + l] = acc[c / RT][c % RT];
+    __syncthreads();
+    for (int c = w; c < RT * MT; c += NW) {
+        f32x4 v = sums[c * kWave + l];
+#pragma unroll
+        for (int p = 1; p < NW; ++p) v += sums[(p * RT * MT + c) * kWave + l];
+        const int m = c / RT, r = (c % RT) * 16 + q * 4;
+        const int64_t place = place0 + m * 16 + c16;
+        const bool live = s_tok[m * 16 + c16] >= 0 && r < g.R;  // R is a multiple of 8: all four ranks or none
+        v = live ? v * scale : f32x4{0, 0, 0, 0};
+        if constexpr (PART)
+            *reinterpret_cast<f32x4 *>(g.partial + ((int64_t)blockIdx.y * g.places + place) * (RT * 16) + r) = v;
+        else store_hidden(g.h, place, g.places, RT * 16, r, v);
     }
-    if (threadIdx.x == 0) st_agent32(&g.done[blockIdx.x], 0u);
 }
 
 // ---- expand: y += W^T h ---------------------------------------------------------
 struct ExpandArgs {
-    const uint16_t *h;  // [place][Rp]
-    const uint16_t *w;  // [S][R][C]
+    const uint16_t *h;     // [place][Rp]
+    const float *partial;  // or its parts [parts][place][Rp] (PART)
+    const uint16_t *w;     // [S][R][C]
     uint16_t *y;
     int64_t ldy;
     LoraPlan plan;
-    int32_t T, S, C, R, max_tiles;
+    int64_t places;
+    int32_t T, S, C, R, max_tiles, per, groups;  // per: tiles of a workgroup; groups: workgroups of a column block
+    int32_t parts;
 };
 
-// A wave takes 128 columns of one tile's 64 places.  Matrix instruction: rows =
-// columns of y, columns = places, 16 ranks.  Lane c of the row axis holds the
-// 8-column piece pi(c) = 4 (c mod 4) + c / 4, instruction j its column j: then
-// the lane's results i = 0..3 are, for j = 0..7, eight neighbouring columns of
-// piece 4 i + q, one 16-byte access to y, and the four lanes of a token touch
-// 64 contiguous bytes.
-template <int RT>
+// A wave takes 128 columns of the 64 places of each of its tiles.  Matrix
+// instruction: rows = places, columns = columns of y, 16 ranks.  Lane c of the
+// column axis holds the 8-column piece c, instruction j its column j: then the
+// lane's results i = 0..3 are, for j = 0..7, one 16-byte piece of the row of
+// place 4 q + i, and sixteen lanes touch 256 contiguous bytes.  The rows of the
+// next 16 places are read while these are computed and written.
+template <int RT, bool PART>
 __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), c16 = l & 15, q = l >> 4;
     // workgroups go round the eight XCDs: with eight column blocks or more, one XCD keeps to
     // every eighth block and goes through all tiles of it, whose adapters then stay in its L2
     const int b = blockIdx.x, blocks = (g.C + 511) / 512;
-    const int cb = blocks >= 8 ? ((b >> 3) / g.max_tiles) * 8 + (b & 7) : b % blocks;
-    const int tile = blocks >= 8 ? (b >> 3) % g.max_tiles : b / blocks;
-    const int base = (cb * 4 + w) * 128;
-    const int slot = g.plan.tile_slot[tile];
-    if ((uint32_t)slot >= (uint32_t)g.S || base >= g.C) return;
-    const int count = g.plan.tile_count[tile] < LT ? g.plan.tile_count[tile] : LT;
-    const int col = base + ((c16 & 3) * 4 + (c16 >> 2)) * 8;
+    const int cb = blocks >= 8 ? ((b >> 3) / g.groups) * 8 + (b & 7) : b % blocks;
+    const int ta = (blocks >= 8 ? (b >> 3) % g.groups : b / blocks) * g.per;
+    const int base = (cb * 4 + w) * 128, col = base + c16 * 8;
+    if (base >= g.C) return;
+    const bool colok = col < g.C;
+    const int tb = ta + g.per < g.max_tiles ? ta + g.per : g.max_tiles;
+    uint16_t *const ycol = g.y + (colok ? col : base);
     s16x4 frag[RT][8];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        u32x4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = rt * 16 + q * 4 + i;
-            v[i] = u32x4{0, 0, 0, 0};
-            if (r < g.R && col < g.C) v[i] = ld16(g.w + ((int64_t)slot * g.R + r) * g.C + col);
-        }
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const u32x2 lo = {__builtin_amdgcn_perm(v[1][d], v[0][d], 0x05040100u),
-                              __builtin_amdgcn_perm(v[3][d], v[2][d], 0x05040100u)};
-            const u32x2 hi = {__builtin_amdgcn_perm(v[1][d], v[0][d], 0x07060302u),
-                              __builtin_amdgcn_perm(v[3][d], v[2][d], 0x07060302u)};
-            frag[rt][2 * d] = __builtin_bit_cast(s16x4, lo);
-            frag[rt][2 * d + 1] = __builtin_bit_cast(s16x4, hi);
-        }
-    }
-    for (int sub = 0; sub * 16 < count; ++sub) {
-        const int64_t place = (int64_t)tile * LT + sub * 16 + c16;
-        const int tok = token_of(g.plan.order[place], g.T);
-        uint16_t *py = g.y + (int64_t)(tok < 0 ? 0 : tok) * g.ldy + base + q * 8;
+    int cur = -1;
+    for (int tile = ta; tile < tb; ++tile) {
+        const int slot = __builtin_amdgcn_readfirstlane(g.plan.tile_slot[tile]);
+        if ((uint32_t)slot >= (uint32_t)g.S) return;
+        const int raw = __builtin_amdgcn_readfirstlane(g.plan.tile_count[tile]), count = raw < LT ? raw : LT;
+        const int64_t place0 = (int64_t)tile * LT;
+        const int32_t *ord = g.plan.order + place0 + q * 4;
+        // a lane's token of places 4 q + i, -1 also where its columns are past the end; empty
+        // places read the row of the tile's first
+        const int some = token_of(__builtin_amdgcn_readfirstlane(g.plan.order[place0]), g.T);
+        i32x4 tok = *reinterpret_cast<const i32x4 *>(ord);
         u32x4 yv[4];
+        auto rows = [&](i32x4 &t, u32x4 *v) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            yv[i] = u32x4{0, 0, 0, 0};
-            if (tok >= 0 && base + (i * 4 + q) * 8 < g.C) yv[i] = ld16(py + i * 32);
+            for (int i = 0; i < 4; ++i) {
+                t[i] = colok ? token_of(t[i], g.T) : -1;
+                v[i] = ld16(ycol + (int64_t)(t[i] >= 0 ? t[i] : (some < 0 ? 0 : some)) * g.ldy);
+            }
+        };
+        rows(tok, yv);
+        if (slot != cur) {
+            cur = slot;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                u32x4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = rt * 16 + q * 4 + i;
+                    v[i] = u32x4{0, 0, 0, 0};
+                    if (r < g.R && colok) v[i] = ld16(g.w + ((int64_t)slot * g.R + r) * g.C + col);
+                }
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const u32x2 lo = {__builtin_amdgcn_perm(v[1][d], v[0][d], 0x05040100u),
+                                      __builtin_amdgcn_perm(v[3][d], v[2][d], 0x05040100u)};
+                    const u32x2 hi = {__builtin_amdgcn_perm(v[1][d], v[0][d], 0x07060302u),
+                                      __builtin_amdgcn_perm(v[3][d], v[2][d], 0x07060302u)};
+                    frag[rt][2 * d] = __builtin_bit_cast(s16x4, lo);
+                    frag[rt][2 * d + 1] = __builtin_bit_cast(s16x4, hi);
+                }
+            }
         }
-        f32x4 acc[8];
+        for (int sub = 0; sub * 16 < count; ++sub) {
+            i32x4 tok1 = {-1, -1, -1, -1};
+            u32x4 yv1[4];
+            const bool more = (sub + 1) * 16 < count;
+            s16x4 hv[RT];
+            const int64_t at = (place0 + sub * 16 + c16) * (RT * 16) + q * 4;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = f32x4{0, 0, 0, 0};
+            for (int rt = 0; rt < RT; ++rt) {
+                if constexpr (PART) {
+                    f32x4 v = *reinterpret_cast<const f32x4 *>(g.partial + at + rt * 16);
+                    for (int p = 1; p < g.parts; ++p)
+                        v += *reinterpret_cast<const f32x4 *>(g.partial + p * g.places * (RT * 16) + at + rt * 16);
+                    hv[rt] = __builtin_bit_cast(s16x4, u32x2{cast_pair(v[0], v[1]), cast_pair(v[2], v[3])});
+                } else {
+                    hv[rt] = __builtin_bit_cast(s16x4, *reinterpret_cast<const u32x2 *>(g.h + at + rt * 16));
+                }
+            }
+            if (more) {
+                tok1 = *reinterpret_cast<const i32x4 *>(ord + (sub + 1) * 16);
+                rows(tok1, yv1);
+            }
+            f32x4 acc[8];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const s16x4 hv =
-                __builtin_bit_cast(s16x4, *reinterpret_cast<const u32x2 *>(g.h + place * (RT * 16) + rt * 16 + q * 4));
+            for (int j = 0; j < 8; ++j) acc[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                acc[j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(frag[rt][j], hv, acc[j], 0, 0, 0);
-        }
+            for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (tok >= 0 && base + (i * 4 + q) * 8 < g.C) {
+                for (int j = 0; j < 8; ++j)
+                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(hv[rt], frag[rt][j], acc[j], 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
                 u32x4 o;
 #pragma unroll
                 for (int d = 0; d < 4; ++d)
                     o[d] = cast_pair(__uint_as_float(yv[i][d] << 16) + acc[2 * d][i],
                                      __uint_as_float(yv[i][d] & 0xFFFF0000u) + acc[2 * d + 1][i]);
-                *reinterpret_cast<u32x4 *>(py + i * 32) = o;
+                if (tok[i] >= 0) *reinterpret_cast<u32x4 *>(ycol + (int64_t)tok[i] * g.ldy) = o;
+            }
+            if (more) {
+                tok = tok1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) yv[i] = yv1[i];
             }
         }
     }
@@ -375,7 +528,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
 
 // ---- outer: G_i = sum over i's tokens of u z^T ------------------------------------
 struct OuterSide {
-    const uint16_t *hi, *lo;  // u: [Rp][place]
+    const uint16_t *part[3];  // u: [Rp][place], its three parts
     const uint16_t *z;        // [tokens][ldz]
     int64_t ldz;
     float *out;               // [S][R][C]
@@ -403,13 +556,15 @@ struct ZVec<4> {
     typedef u32x2 T;
 };
 
-// A wave takes 16 W columns and one chunk of q tiles.  Matrix instruction: rows
-// = ranks, columns = columns of z, 32 tokens.  Lane c of the column axis holds
-// W neighbouring columns of eight tokens, transposed in registers; instruction
-// j takes its column j.  A chunk may cover several adapters and an adapter
-// several chunks: a run that lies in one chunk goes straight to the output, the
-// others to the chunk's partial sums (0: continues an earlier chunk's run, 1:
-// begins here), which k_lora_outer_sum adds in order.
+// A wave takes 16 W columns and one chunk of q tiles, 32 places at a time: the
+// rows of the next 32 are read while these are multiplied, the places' tokens
+// one step before that.  Matrix instruction: rows = ranks, columns = columns of
+// z, 32 places.  Lane c of the column axis holds W neighbouring columns of eight
+// places, transposed in registers; instruction j takes its column j, once for
+// each part of u.  A chunk may cover several adapters and an adapter several
+// chunks: a run that lies in one chunk goes straight to the output, the others
+// to the chunk's partial sums (0: continues an earlier chunk's run, 1: begins
+// here), which k_lora_outer_sum adds in order.
 template <int RT, int W>
 __global__ __launch_bounds__(256) void k_lora_outer(OuterArgs g) {
     typedef typename ZVec<W>::T ZV;
@@ -420,8 +575,11 @@ __global__ __launch_bounds__(256) void k_lora_outer(OuterArgs g) {
     if (cb >= s.waves) return;
     const int ntiles = *g.plan.ntiles < g.max_tiles ? *g.plan.ntiles : g.max_tiles;
     const int ta = chunk * g.q, tb = ta + g.q < ntiles ? ta + g.q : ntiles;
+    if (ta >= tb) return;
     const int col = cb * 16 * W + c16 * W;
     const bool colok = col < s.C;
+    const uint16_t *const zcol = s.z + (colok ? col : cb * 16 * W);
+    const int some = token_of(__builtin_amdgcn_readfirstlane(g.plan.order[(int64_t)ta * LT]), g.T);
     f32x4 acc[RT][W];
     auto flush = [&](int slot) {
         const int t0 = g.plan.slot_tile[slot], t1 = g.plan.slot_tile[slot + 1];
@@ -444,56 +602,81 @@ __global__ __launch_bounds__(256) void k_lora_outer(OuterArgs g) {
                 }
             }
     };
-    int cur = -1;
-    for (int t = ta; t < tb; ++t) {
-        const int slot = __builtin_amdgcn_readfirstlane(g.plan.tile_slot[t]);
-        const int raw = __builtin_amdgcn_readfirstlane(g.plan.tile_count[t]), count = raw < LT ? raw : LT;
-        if ((uint32_t)slot >= (uint32_t)g.S) break;
-        if (slot != cur) {
-            if (cur >= 0) flush(cur);
-            cur = slot;
+    // the eight places of lane q in the 32 from place h 32 on
+    auto order_at = [&](int h, i32x4 *o) {
+        const int32_t *p = g.plan.order + (int64_t)h * 32 + q * 8;
+        o[0] = *reinterpret_cast<const i32x4 *>(p);
+        o[1] = *reinterpret_cast<const i32x4 *>(p + 4);
+    };
+    auto rows_at = [&](const i32x4 *o, ZV *z) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int t = token_of(o[i >> 2][i & 3], g.T);
+            z[i] = *reinterpret_cast<const ZV *>(zcol + (int64_t)(t >= 0 ? t : (some < 0 ? 0 : some)) * s.ldz);
+        }
+    };
+    i32x4 ord[2], ord1[2];
+    ZV z[8], z1[8];
+    order_at(2 * ta, ord);
+    rows_at(ord, z);
+    order_at(2 * ta + 1, ord1);
+    int cur = -1, count = 0;
+    for (int h = 2 * ta; h < 2 * tb; ++h) {
+        if (!(h & 1)) {
+            const int slot = __builtin_amdgcn_readfirstlane(g.plan.tile_slot[h >> 1]);
+            if ((uint32_t)slot >= (uint32_t)g.S) break;
+            const int raw = __builtin_amdgcn_readfirstlane(g.plan.tile_count[h >> 1]);
+            count = raw < LT ? raw : LT;
+            if (slot != cur) {
+                if (cur >= 0) flush(cur);
+                cur = slot;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int j = 0; j < W; ++j) acc[rt][j] = f32x4{0, 0, 0, 0};
+            }
+        }
+        const int first = (h & 1) * 32, left = count - first;
+        u32x4 u[3][RT];
+        if (left > 0) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int j = 0; j < W; ++j) acc[rt][j] = f32x4{0, 0, 0, 0};
+                for (int p = 0; p < 3; ++p)
+                    u[p][rt] = ld16(s.part[p] + (int64_t)(rt * 16 + c16) * g.places + (int64_t)h * 32 + q * 8);
         }
-        for (int half = 0; half * 32 < count; ++half) {
-            const int64_t place = (int64_t)t * LT + half * 32 + q * 8;
-            const i32x4 o0 = *reinterpret_cast<const i32x4 *>(g.plan.order + place);
-            const i32x4 o1 = *reinterpret_cast<const i32x4 *>(g.plan.order + place + 4);
-            ZV z[8];
+        if (h + 1 < 2 * tb) rows_at(ord1, z1);
+        if (left > 0) {
+            if (left < 32) {  // empty places: no row, and past the last 16 that hold a token no u
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int tok = token_of(i < 4 ? o0[i & 3] : o1[i & 3], g.T);
-                z[i] = ZV{};
-                if (tok >= 0 && colok) z[i] = *reinterpret_cast<const ZV *>(s.z + (int64_t)tok * s.ldz + col);
-            }
-            // places past the last 16 that hold a token have no u
-            const bool some = half * 32 + q * 8 < (count + 15) / 16 * 16;
-            u32x4 uh[RT], ul[RT];
+                for (int i = 0; i < 8; ++i)
+                    if (token_of(ord[i >> 2][i & 3], g.T) < 0) z[i] = ZV{};
+                const bool none = q * 8 >= (left + 15) / 16 * 16;
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                uh[rt] = u32x4{0, 0, 0, 0};
-                ul[rt] = u32x4{0, 0, 0, 0};
-                if (some) {
-                    uh[rt] = ld16(s.hi + (int64_t)(rt * 16 + c16) * g.places + place);
-                    ul[rt] = ld16(s.lo + (int64_t)(rt * 16 + c16) * g.places + place);
-                }
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+                        if (none) u[p][rt] = u32x4{0, 0, 0, 0};
             }
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
                 u32x4 zt;
 #pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    zt[d] = __builtin_amdgcn_perm(z[2 * d + 1][j >> 1], z[2 * d][j >> 1], sel);
+                for (int d = 0; d < 4; ++d) zt[d] = __builtin_amdgcn_perm(z[2 * d + 1][j >> 1], z[2 * d][j >> 1], sel);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    acc[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(ul[rt]), as_bf(zt), acc[rt][j], 0, 0, 0);
-                    acc[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(uh[rt]), as_bf(zt), acc[rt][j], 0, 0, 0);
-                }
+                for (int p = 2; p >= 0; --p)
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        acc[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(u[p][rt]), as_bf(zt), acc[rt][j], 0,
+                                                                            0, 0);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) ord[i] = ord1[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = z1[i];
+        if (h + 2 < 2 * tb) order_at(h + 2, ord1);
     }
     if (cur >= 0) flush(cur);
 }
@@ -520,76 +703,72 @@ __global__ __launch_bounds__(256) void k_lora_outer_sum(OuterArgs g) {
 }
 
 // ---- launches ---------------------------------------------------------------------
-// Parts of the long axis in shrink: enough that the tiles' workgroups come to
-// about 1024, each wave keeping 4 steps of 32 or more.
-int lora_ksplit(int64_t T, int64_t S, int64_t C) {
-    const int64_t groups = (T + 15) / 16 > lora_max_tiles(T, S) ? (T + 15) / 16 : lora_max_tiles(T, S);
-    const int64_t most = C / 512 > 1 ? C / 512 : 1;
-    int64_t k = 1024 / groups;
-    if (k > most) k = most;
-    if (k > 16) k = 16;
-    return (int)(k < 1 ? 1 : k);
-}
+// Columns of a wave in outer: 128, or 64 where 128 columns' sums leave no registers to read ahead.
+int lora_outer_width(int64_t R) { return R > 48 ? 64 : 128; }
 
-// Bytes of shrink's counters and partial sums, for this T and every smaller one.
-// ksplit > 1 means at most 512 tiles, so 2048 counters, and 1024 tiles times
-// parts.  The counters stay at the front whatever the sizes: they are zero
-// between calls, and no call may leave anything else there.
-constexpr int64_t kShrinkCounters = 2048;
-
-int64_t lora_shrink_ws(int64_t T, int64_t S, int64_t R) {
-    const int64_t rp = (R + 15) / 16 * 16, mt = lora_max_tiles(T, S), parts = mt * 16 < 1024 ? mt * 16 : 1024;
-    return kShrinkCounters * 4 + parts * LT * rp * 4;
-}
-
-// Tiles of a chunk in outer: about 2048 waves over both sides, 256 tokens or more.
 int64_t lora_outer_waves(int64_t K, int64_t N, int64_t R) {
-    const int64_t width = R > 64 ? 64 : 128;
+    const int64_t width = lora_outer_width(R);
     return (K + width - 1) / width + (N + width - 1) / width;
 }
 
+// Tiles of a chunk in outer: about 2048 waves over both sides, 128 tokens or more.
 int lora_chunk(int64_t T, int64_t S, int64_t K, int64_t N, int64_t R) {
     const int64_t q = lora_max_tiles(T, S) * lora_outer_waves(K, N, R) / 2048;
-    return (int)(q < 4 ? 4 : (q > 64 ? 64 : q));
+    return (int)(q < 2 ? 2 : (q > 64 ? 64 : q));
 }
 
 int64_t lora_chunks(int64_t T, int64_t S, int q) { return (lora_max_tiles(T, S) + q - 1) / q; }
 
-// Most chunks of this T and every smaller one: a chunk has 4 tiles, or more
-// than 4/5 of the tiles that make 2048 waves, or 64 tiles.
+// Most chunks of this T and every smaller one: a chunk has 2 tiles (and there are
+// fewer than 3 times those that make 2048 waves), or more than 3/4 of the tiles
+// that make 2048 waves, or 64 tiles.
 int64_t lora_most_chunks(int64_t T, int64_t S, int64_t K, int64_t N, int64_t R) {
-    const int64_t mt = lora_max_tiles(T, S), a = mt / 4 + 1, b = 2560 / lora_outer_waves(K, N, R) + 2, c = mt / 64 + 1;
+    const int64_t mt = lora_max_tiles(T, S), a = mt / 2 + 1, b = 3072 / lora_outer_waves(K, N, R) + 2, c = mt / 64 + 1;
     const int64_t m = a < b ? a : b;
     return m > c ? m : c;
 }
 
-void launch_shrink(const ShrinkArgs &g, int64_t tiles, int rt, hipStream_t stream) {
-    const dim3 grid((unsigned)(tiles * 4), (unsigned)g.ksplit), block(256);
+template <int MT, bool PART>
+void launch_shrink(const ShrinkArgs &g, int parts, int rt, hipStream_t stream) {
+    const dim3 grid((unsigned)(MT == 1 ? g.max_groups : g.max_tiles * (4 / MT)), (unsigned)parts);
+    const auto block = [](int r) { return dim3(shrink_waves(r, MT) * kWave); };
     switch (rt) {
-    case 1: k_lora_shrink<1><<<grid, block, 0, stream>>>(g); break;
-    case 2: k_lora_shrink<2><<<grid, block, 0, stream>>>(g); break;
-    case 3: k_lora_shrink<3><<<grid, block, 0, stream>>>(g); break;
-    case 4: k_lora_shrink<4><<<grid, block, 0, stream>>>(g); break;
-    case 5: k_lora_shrink<5><<<grid, block, 0, stream>>>(g); break;
-    case 6: k_lora_shrink<6><<<grid, block, 0, stream>>>(g); break;
-    case 7: k_lora_shrink<7><<<grid, block, 0, stream>>>(g); break;
-    default: k_lora_shrink<8><<<grid, block, 0, stream>>>(g); break;
+    case 1: k_lora_shrink<1, MT, PART><<<grid, block(1), 0, stream>>>(g); break;
+    case 2: k_lora_shrink<2, MT, PART><<<grid, block(2), 0, stream>>>(g); break;
+    case 3: k_lora_shrink<3, MT, PART><<<grid, block(3), 0, stream>>>(g); break;
+    case 4: k_lora_shrink<4, MT, PART><<<grid, block(4), 0, stream>>>(g); break;
+    case 5: k_lora_shrink<5, MT, PART><<<grid, block(5), 0, stream>>>(g); break;
+    case 6: k_lora_shrink<6, MT, PART><<<grid, block(6), 0, stream>>>(g); break;
+    case 7: k_lora_shrink<7, MT, PART><<<grid, block(7), 0, stream>>>(g); break;
+    default:  // eight rank tiles leave room for 16 places only
+        k_lora_shrink<8, 1, PART><<<dim3((unsigned)g.max_groups, (unsigned)parts), dim3(shrink_waves(8, 1) * kWave), 0,
+                                    stream>>>(g);
     }
 }
 
+template <bool PART>
 void launch_expand(const ExpandArgs &g, int rt, hipStream_t stream) {
     const int64_t blocks = ((int64_t)g.C + 511) / 512;
-    const dim3 grid((unsigned)((blocks >= 8 ? (blocks + 7) / 8 * 8 : blocks) * g.max_tiles)), block(256);
+    const dim3 grid((unsigned)((blocks >= 8 ? (blocks + 7) / 8 * 8 : blocks) * g.groups)), block(256);
     switch (rt) {
-    case 1: k_lora_expand<1><<<grid, block, 0, stream>>>(g); break;
-    case 2: k_lora_expand<2><<<grid, block, 0, stream>>>(g); break;
-    case 3: k_lora_expand<3><<<grid, block, 0, stream>>>(g); break;
-    case 4: k_lora_expand<4><<<grid, block, 0, stream>>>(g); break;
-    case 5: k_lora_expand<5><<<grid, block, 0, stream>>>(g); break;
-    case 6: k_lora_expand<6><<<grid, block, 0, stream>>>(g); break;
-    case 7: k_lora_expand<7><<<grid, block, 0, stream>>>(g); break;
-    default: k_lora_expand<8><<<grid, block, 0, stream>>>(g); break;
+    case 1: k_lora_expand<1, PART><<<grid, block, 0, stream>>>(g); break;
+    case 2: k_lora_expand<2, PART><<<grid, block, 0, stream>>>(g); break;
+    case 3: k_lora_expand<3, PART><<<grid, block, 0, stream>>>(g); break;
+    case 4: k_lora_expand<4, PART><<<grid, block, 0, stream>>>(g); break;
+    case 5: k_lora_expand<5, PART><<<grid, block, 0, stream>>>(g); break;
+    case 6: k_lora_expand<6, PART><<<grid, block, 0, stream>>>(g); break;
+    case 7: k_lora_expand<7, PART><<<grid, block, 0, stream>>>(g); break;
+    default: k_lora_expand<8, PART><<<grid, block, 0, stream>>>(g); break;
     }
+}
+
+// Workgroups that share the long axis in a forward pass that keeps no h: as many
+// as bring the groups of 16 places that hold a token to about 256, one step a wave
+// or more.  Each writes its own part of h, which expand adds up.
+int lora_parts(int64_t T, int64_t S, int64_t C, int64_t R) {
+    const int64_t groups = (T + 15) / 16 + (S < T ? S : T), waves = shrink_waves((int)((R + 15) / 16), 1);
+    const int64_t most = (C + 127) / 128 / waves, parts = 256 / groups < most ? 256 / groups : most;
+    return (int)(parts < 1 ? 1 : (parts > 8 ? 8 : parts));
 }
 
 void launch_outer(const OuterArgs &g, int rt, int64_t wgs, int64_t chunks, hipStream_t stream) {
@@ -598,12 +777,20 @@ void launch_outer(const OuterArgs &g, int rt, int64_t wgs, int64_t chunks, hipSt
     case 1: k_lora_outer<1, 8><<<grid, block, 0, stream>>>(g); break;
     case 2: k_lora_outer<2, 8><<<grid, block, 0, stream>>>(g); break;
     case 3: k_lora_outer<3, 8><<<grid, block, 0, stream>>>(g); break;
-    case 4: k_lora_outer<4, 8><<<grid, block, 0, stream>>>(g); break;
+    case 4: k_lora_outer<4, 4><<<grid, block, 0, stream>>>(g); break;
     case 5: k_lora_outer<5, 4><<<grid, block, 0, stream>>>(g); break;
     case 6: k_lora_outer<6, 4><<<grid, block, 0, stream>>>(g); break;
     case 7: k_lora_outer<7, 4><<<grid, block, 0, stream>>>(g); break;
     default: k_lora_outer<8, 4><<<grid, block, 0, stream>>>(g); break;
     }
+}
+
+// Bytes of h's parts, for this T and every smaller one.  Parts are made where the
+// groups of 16 places come to 128 or fewer: then there are 128 tiles or fewer, and
+// groups times parts come to 256 or fewer, of at most 64 places each.
+int64_t lora_parts_size(int64_t T, int64_t S, int64_t R) {
+    const int64_t rp = (R + 15) / 16 * 16, mt = lora_max_tiles(T, S), n = mt * 8 < 256 ? mt * 8 : 256;
+    return n * LT * rp * 4;
 }
 
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
@@ -616,49 +803,59 @@ extern "C" int64_t pulse_lora_plan_size(int64_t T, int64_t S) { return lora_plan
 
 extern "C" int64_t pulse_lora_hidden_size(int64_t T, int64_t S, int64_t R) { return lora_hidden_size(T, S, R, true); }
 
-// Workspace: the workgroup counters and partial sums of shrink, at the front and
-// any T up to the one given; then h of a forward pass, or in a backward pass dh
-// and the partial sums of both gradients.
+// Workspace: h of a forward pass, whole or in parts, or in a backward pass dh and the partial sums of both gradients.
 extern "C" int64_t pulse_lora_ws_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t S, int32_t train) {
-    int64_t n = round256(lora_shrink_ws(T, S, R)) + round256(lora_hidden_size(T, S, R, train != 0));
+    int64_t n = round256(lora_hidden_size(T, S, R, train != 0));
+    if (n < lora_parts_size(T, S, R)) n = lora_parts_size(T, S, R);
     if (train) n += lora_most_chunks(T, S, K, N, R) * 2 * R * (K + N) * 4;
     return n;
 }
 
 extern "C" int pulse_launch_lora_plan(const int32_t *ids, int64_t T, int32_t S, void *plan, uint32_t *d_status,
                                       hipStream_t stream) {
-    k_lora_plan<<<dim3(1), dim3(LP_THREADS), (size_t)LP_WAVES * S * 4, stream>>>(
-        ids, (int32_t)T, S, lora_plan_parts(plan, T, S), (int32_t)lora_max_tiles(T, S), d_status);
+    // sixteen waves where their counts of all adapters stay below 64 KB of LDS
+    const LoraPlan p = lora_plan_parts(plan, T, S);
+    const int32_t mt = (int32_t)lora_max_tiles(T, S), mg = (int32_t)lora_max_groups(T, S);
+    if (S <= 512)
+        k_lora_plan<16><<<dim3(1), dim3(1024), (size_t)19 * S * 4, stream>>>(ids, (int32_t)T, S, p, mt, mg, d_status);
+    else k_lora_plan<8><<<dim3(1), dim3(512), (size_t)11 * S * 4, stream>>>(ids, (int32_t)T, S, p, mt, mg, d_status);
     return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
 namespace {
 
+// h goes to its forms, or with parts > 1 to `partial`
 void shrink(const uint16_t *x, int64_t ldx, const uint16_t *a, const float *scales, const LoraPlan &plan,
-            const LoraHidden &h, void *ws, int64_t T, int64_t C, int64_t R, int64_t S, hipStream_t stream) {
-    const int64_t mt = lora_max_tiles(T, S);
+            const LoraHidden &h, float *partial, int parts, int64_t T, int64_t C, int64_t R, int64_t S,
+            hipStream_t stream) {
+    const int rt = (int)((R + 15) / 16);
     ShrinkArgs g{};
+    g.max_tiles = (int32_t)lora_max_tiles(T, S);
+    g.max_groups = (int32_t)lora_max_groups(T, S);
     g.x = x;
     g.ldx = ldx;
     g.a = a;
     g.scales = scales;
     g.plan = plan;
     g.h = h;
-    g.done = static_cast<uint32_t *>(ws);
-    g.partial = reinterpret_cast<float *>(static_cast<char *>(ws) + kShrinkCounters * 4);
-    g.places = mt * LT;
+    g.partial = partial;
+    g.places = (int64_t)g.max_tiles * LT;
     g.T = (int32_t)T;
     g.S = (int32_t)S;
     g.C = (int32_t)C;
     g.R = (int32_t)R;
-    g.ksplit = lora_ksplit(T, S, C);
-    launch_shrink(g, mt, (int)((R + 15) / 16), stream);
+    // 32 places a workgroup, so that the adapter is read half as often, once that still fills the chip
+    // and few adapters end in the first half of a tile
+    if (parts > 1) launch_shrink<1, true>(g, parts, rt, stream);
+    else if (T >= 8192 && T / S >= 128) launch_shrink<2, false>(g, 1, rt, stream);
+    else launch_shrink<1, false>(g, 1, rt, stream);
 }
 
-void expand(const uint16_t *h, const uint16_t *w, uint16_t *y, int64_t ldy, const LoraPlan &plan, int64_t T, int64_t C,
-            int64_t R, int64_t S, hipStream_t stream) {
+void expand(const uint16_t *h, const float *partial, int parts, const uint16_t *w, uint16_t *y, int64_t ldy,
+            const LoraPlan &plan, int64_t T, int64_t C, int64_t R, int64_t S, hipStream_t stream) {
     ExpandArgs g{};
     g.h = h;
+    g.partial = partial;
     g.w = w;
     g.y = y;
     g.ldy = ldy;
@@ -667,8 +864,16 @@ void expand(const uint16_t *h, const uint16_t *w, uint16_t *y, int64_t ldy, cons
     g.S = (int32_t)S;
     g.C = (int32_t)C;
     g.R = (int32_t)R;
+    g.parts = parts;
     g.max_tiles = (int32_t)lora_max_tiles(T, S);
-    launch_expand(g, (int)((R + 15) / 16), stream);
+    g.places = (int64_t)g.max_tiles * LT;
+    // tiles of a workgroup, whose adapter is then read and transposed once: up to 4, 2048 workgroups or more
+    const int64_t per = g.max_tiles * ((C + 511) / 512) / 2048;
+    g.per = (int32_t)(per < 1 ? 1 : (per > 4 ? 4 : per));
+    g.groups = (g.max_tiles + g.per - 1) / g.per;
+    const int rt = (int)((R + 15) / 16);
+    if (parts > 1) launch_expand<true>(g, rt, stream);
+    else launch_expand<false>(g, rt, stream);
 }
 
 }  // namespace
@@ -677,10 +882,11 @@ extern "C" int pulse_launch_lora_forward(const uint16_t *x, int64_t ldx, const u
                                          const float *scales, const void *plan, int64_t T, int64_t K, int64_t N, int64_t R,
                                          int64_t S, uint16_t *y, int64_t ldy, void *h, void *ws, hipStream_t stream) {
     const LoraPlan p = lora_plan_parts(const_cast<void *>(plan), T, S);
-    const LoraHidden hp = h ? lora_hidden_parts(h, T, S, R, true)
-                            : lora_hidden_parts(static_cast<char *>(ws) + round256(lora_shrink_ws(T, S, R)), T, S, R, false);
-    shrink(x, ldx, a, scales, p, hp, ws, T, K, R, S, stream);
-    expand(hp.rows, b, y, ldy, p, T, N, R, S, stream);
+    const LoraHidden hp = lora_hidden_parts(h ? h : ws, T, S, R, h != nullptr);
+    const int parts = h ? 1 : lora_parts(T, S, K, R);
+    float *partial = static_cast<float *>(ws);
+    shrink(x, ldx, a, scales, p, hp, partial, parts, T, K, R, S, stream);
+    expand(hp.rows, partial, parts, b, y, ldy, p, T, N, R, S, stream);
     return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
@@ -690,11 +896,11 @@ extern "C" int pulse_launch_lora_backward(const uint16_t *x, int64_t ldx, const 
                                           uint16_t *dx, int64_t lddx, float *da, float *db, int32_t accumulate,
                                           void *ws, hipStream_t stream) {
     const LoraPlan p = lora_plan_parts(const_cast<void *>(plan), T, S);
-    char *w = static_cast<char *>(ws) + round256(lora_shrink_ws(T, S, R));
+    char *w = static_cast<char *>(ws);
     const LoraHidden dh = lora_hidden_parts(w, T, S, R, true), hp = lora_hidden_parts(const_cast<void *>(h), T, S, R, true);
-    shrink(dy, lddy, b, scales, p, dh, ws, T, N, R, S, stream);
-    if (dx) expand(dh.rows, a, dx, lddx, p, T, K, R, S, stream);
-    const int rt = (int)((R + 15) / 16), width = rt > 4 ? 64 : 128;
+    shrink(dy, lddy, b, scales, p, dh, nullptr, 1, T, N, R, S, stream);
+    if (dx) expand(dh.rows, nullptr, 1, a, dx, lddx, p, T, K, R, S, stream);
+    const int rt = (int)((R + 15) / 16), width = lora_outer_width(R);
     OuterArgs g{};
     g.plan = p;
     g.places = lora_max_tiles(T, S) * LT;
@@ -707,8 +913,8 @@ extern "C" int pulse_launch_lora_backward(const uint16_t *x, int64_t ldx, const 
     const int64_t chunks = lora_chunks(T, S, g.q);
     g.chunks = (int32_t)chunks;
     float *part = reinterpret_cast<float *>(w + round256(lora_hidden_size(T, S, R, true)));
-    g.side[0] = OuterSide{dh.hi, dh.lo, x, ldx, da, part, (int32_t)K, (int32_t)((K + width - 1) / width)};
-    g.side[1] = OuterSide{hp.hi, hp.lo, dy, lddy, db, part + chunks * 2 * R * K, (int32_t)N,
+    g.side[0] = OuterSide{{dh.part[0], dh.part[1], dh.part[2]}, x, ldx, da, part, (int32_t)K, (int32_t)((K + width - 1) / width)};
+    g.side[1] = OuterSide{{hp.part[0], hp.part[1], hp.part[2]}, dy, lddy, db, part + chunks * 2 * R * K, (int32_t)N,
                           (int32_t)((N + width - 1) / width)};
     g.wg0 = (g.side[0].waves + 3) / 4;
     launch_outer(g, rt, g.wg0 + (g.side[1].waves + 3) / 4, chunks, stream);
