@@ -662,9 +662,10 @@ typedef struct pulse_adamw_params {
  *   patch_idx, patch_val, patch_cap, seg_offsets  the patch of the view's
  *              changed elements as pulse_cast_diff_segments writes it (b is
  *              both the old and the new view), or all NULL.
- *   d_status   PULSE_DS_CAPACITY, PULSE_DS_BADSEGMENT, PULSE_DS_WORKSPACE.
- *   ws         pulse_workspace_bytes(PULSE_OP_ADAMW, ntiles, 0) when a patch is
- *              asked for; ignored otherwise. */
+ *   d_status   PULSE_DS_CAPACITY, PULSE_DS_BADSEGMENT.
+ *   ws         16-byte aligned, pulse_workspace_bytes(PULSE_OP_ADAMW, ntiles, 0)
+ *              when a patch is asked for (it may hold anything before a call, and
+ *              nothing is kept there after it); ignored otherwise. */
 int pulse_adamw_step(const pulse_adamw_segment *segs, int32_t nseg, const uint32_t *tile_seg, int64_t ntiles,
                      const pulse_adamw_params *params, const float *d_scale, int32_t *patch_idx,
                      uint16_t *patch_val, int64_t patch_cap, int64_t *seg_offsets, uint32_t *d_status, void *ws,

@@ -20,8 +20,6 @@
 // bits are a mix of the element's place, its tensor's number and the caller's
 // seed.  A u above zero gets at least the smallest code: a zero would divide
 // the next update by eps alone.
-#include <type_traits>
-
 #include "compact.hpp"
 
 namespace pulse {
@@ -60,8 +58,8 @@ struct AdamArgs {
     int64_t cap;
     int64_t *seg_offsets;
     uint32_t *d_status;
-    WsHeader *hdr;
-    uint64_t *status;
+    uint32_t *counts;  // [step's waves] changed elements
+    uint16_t *flags;   // [step's waves][64][CH] a lane's changed flags, bit 4 g + k of each 1024 elements
 };
 
 constexpr int AW_BLOCK = 256;  // elements of a state block: one group of a wave
@@ -165,9 +163,9 @@ struct AdamTensor {
 
 // Four groups of 256 elements of one wave (lane l: elements 4l .. 4l+3 of each
 // group, the first group at element e0 of the tensor): the step, its stores,
-// and the changed flags (bit 4g+k) and new view values for the patch.
+// and the changed flags (bit 4g+k) for the patch.
 template <bool FULL, bool BF16G, bool EIGHT, bool PATCH>
-__device__ __forceinline__ uint32_t aw_chunk(const AdamArgs &a, const AdamTensor &t, int64_t e0, uint32_t nvp[8]) {
+__device__ __forceinline__ uint32_t aw_chunk(const AdamArgs &a, const AdamTensor &t, int64_t e0) {
     typedef typename GradVec<BF16G>::T GV;
     const int64_t n = t.s.n;
     const int64_t el = e0 + 4 * lane_id();
@@ -247,8 +245,6 @@ __device__ __forceinline__ uint32_t aw_chunk(const AdamArgs &a, const AdamTensor
                     f &= left >= 4 ? 0xFu : (left > 0 ? (1u << left) - 1u : 0u);
                 }
                 flags |= f << (4 * g);
-                nvp[2 * g] = q0;
-                nvp[2 * g + 1] = q1;
             }
         }
         if constexpr (EIGHT) {
@@ -301,32 +297,13 @@ __device__ __forceinline__ uint32_t aw_chunk(const AdamArgs &a, const AdamTensor
     return flags;
 }
 
-// One workgroup per piece of 1024 CH elements x 4 waves (CH = 4: a whole tile,
-// CH = 1: a quarter).  With a patch the piece is a ticket (one atomic) and its
-// first entry comes from a look-back over the pieces before it, as in the
-// codec's own passes; without one it is the workgroup's number.
+// One workgroup of four waves per piece, 1024 CH elements a wave (CH = 4: a whole
+// tile, CH = 1: a quarter).  With a patch each wave leaves its changed flags and
+// their number for k_adamw_patch.
 template <int CH, bool BF16G, bool EIGHT, bool PATCH>
 __global__ __launch_bounds__(CD_THREADS) void k_adamw(AdamArgs a) {
     constexpr int kPerTile = 4 / CH;
-    __shared__ uint32_t s_tile, s_tag;
-    __shared__ typename std::conditional<PATCH, CdShared, int>::type sh;
-    uint32_t piece = blockIdx.x, tag = 0;
-    if constexpr (PATCH) {
-        if (threadIdx.x == 0) {
-            uint32_t tile;
-            ws_begin(a.hdr, a.npieces, &tile, &tag);
-            s_tile = tile;
-            s_tag = tag;
-        }
-        __syncthreads();
-        piece = (uint32_t)__builtin_amdgcn_readfirstlane((int)s_tile);
-        tag = s_tag;
-        if (piece >= a.npieces) {  // inconsistent workspace state: touch nothing
-            if (threadIdx.x == 0) or_agent32(a.d_status, 8u /*PULSE_DS_WORKSPACE*/);
-            return;
-        }
-    }
-    const uint32_t tile = piece / kPerTile;
+    const uint32_t piece = blockIdx.x, tile = piece / kPerTile;
     const uint32_t s = (uint32_t)__builtin_amdgcn_readfirstlane((int)a.tile_seg[tile]);
     AdamTensor t{};
     if (s < (uint32_t)a.nseg) t.s = a.segs[s];
@@ -345,54 +322,103 @@ __global__ __launch_bounds__(CD_THREADS) void k_adamw(AdamArgs a) {
     const bool skip = !(__builtin_fabsf(t.scale) <= 3.402823466e38f);  // NaN or infinite: no step
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
     const int64_t wbase = lt * CD_TILE + (int64_t)(piece % kPerTile) * (CH * 4096) + (int64_t)w * (CH * 1024);
-    uint32_t nvp[PATCH ? CH * 8 : 8];
     uint64_t flags = 0;
     if (ok && !skip && wbase < t.s.n) {
         if (wbase + CH * 1024 <= t.s.n) {
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                flags |= (uint64_t)aw_chunk<true, BF16G, EIGHT, PATCH>(a, t, wbase + c * 1024, nvp + (PATCH ? 8 * c : 0))
-                         << (16 * c);
+                flags |= (uint64_t)aw_chunk<true, BF16G, EIGHT, PATCH>(a, t, wbase + c * 1024) << (16 * c);
                 sched_fence();
             }
         } else {
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 if (wbase + c * 1024 < t.s.n)
-                    flags |= (uint64_t)aw_chunk<false, BF16G, EIGHT, PATCH>(a, t, wbase + c * 1024,
-                                                                           nvp + (PATCH ? 8 * c : 0))
-                             << (16 * c);
+                    flags |= (uint64_t)aw_chunk<false, BF16G, EIGHT, PATCH>(a, t, wbase + c * 1024) << (16 * c);
                 sched_fence();
             }
         }
     }
     if constexpr (PATCH) {
-        const uint32_t wtot = wave_reduce_sum((uint32_t)__builtin_popcountll(flags));
-        if (l == 0) sh.wtot[w] = wtot;
-        __syncthreads();
-        uint32_t count = 0, wpre = 0;
-#pragma unroll
-        for (int i = 0; i < CD_THREADS / kWave; ++i) {
-            if (i < w) wpre += sh.wtot[i];
-            count += sh.wtot[i];
+        const int64_t wave = (int64_t)piece * 4 + w;
+        const uint32_t count = wave_reduce_sum((uint32_t)__builtin_popcountll(flags));
+        if (l == 0) a.counts[wave] = count;
+        if (count != 0) {
+            if constexpr (CH == 4) reinterpret_cast<uint64_t *>(a.flags)[wave * kWave + l] = flags;
+            else a.flags[wave * kWave + l] = (uint16_t)flags;
         }
-        if (w == 0) {
-            bool failed = false;
-            const uint64_t pre = lookback_wave(a.status, piece, tag, count, &failed);
-            if (l == 0) {
-                if (failed) or_agent32(a.d_status, 8u /*PULSE_DS_WORKSPACE*/);
-                if (!ok) or_agent32(a.d_status, 0x10u /*PULSE_DS_BADSEGMENT*/);
-                sh.prefix = pre;
-                if (ok && lt == 0 && piece % kPerTile == 0) a.seg_offsets[s] = (int64_t)pre;
-                if (piece == a.npieces - 1) a.seg_offsets[a.nseg] = (int64_t)(pre + count);
-                if ((int64_t)(pre + count) > a.cap) or_agent32(a.d_status, 1u /*PULSE_DS_CAPACITY*/);
+    }
+    if (!ok && threadIdx.x == 0) or_agent32(a.d_status, 0x10u /*PULSE_DS_BADSEGMENT*/);
+}
+
+// The patch: a workgroup takes a run of the step's waves, whose first entry is
+// the sum of the counts before it; each of its waves goes through its share,
+// reads the changed elements' new view and writes their entries.  The step has
+// no place in the patch to wait for: placing a piece's entries by a ticket and
+// a look-back within the step itself cost 23 ns a piece, one after the other,
+// and 41 us before the first 1800 pieces had begun.
+template <int CH>
+__global__ __launch_bounds__(CD_THREADS) void k_adamw_patch(AdamArgs a) {
+    constexpr int kPerTile = 16 / CH;  // the step's waves of a tile
+    __shared__ int32_t s_idx[CD_THREADS / kWave][CD_SB];
+    __shared__ uint16_t s_val[CD_THREADS / kWave][CD_SB];
+    __shared__ uint64_t s_sum[CD_THREADS / kWave];
+    const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
+    const int64_t nw = (int64_t)a.npieces * 4;
+    const int64_t w0 = nw * blockIdx.x / gridDim.x, w1 = nw * (blockIdx.x + 1) / gridDim.x;
+    const int64_t first = w0 + (w1 - w0) * w / 4, last = w0 + (w1 - w0) * (w + 1) / 4;
+    uint64_t sum = 0;
+    const u32x4 *c4 = reinterpret_cast<const u32x4 *>(a.counts);
+    for (int64_t i = threadIdx.x; i < w0 / 4; i += CD_THREADS) {
+        const u32x4 c = c4[i];
+        sum += (uint64_t)c.x + c.y + ((uint64_t)c.z + c.w);
+    }
+    if (threadIdx.x < (w0 & 3)) sum += a.counts[w0 / 4 * 4 + threadIdx.x];
+    sum = wave_reduce_sum(sum);
+    if (l == 0) s_sum[w] = sum;
+    __syncthreads();
+    uint64_t run = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+    uint32_t mine = 0;
+    for (int64_t i = w0 + l; i < first; i += kWave) mine += a.counts[i];
+    run += wave_reduce_sum(mine);
+    for (int64_t i = first; i < last; ++i) {
+        const uint32_t count = (uint32_t)__builtin_amdgcn_readfirstlane((int)a.counts[i]);
+        const uint32_t tile = (uint32_t)(i / kPerTile);
+        const uint32_t s = (uint32_t)__builtin_amdgcn_readfirstlane((int)a.tile_seg[tile]);
+        if (s < (uint32_t)a.nseg) {
+            const int64_t lt = (int64_t)tile - a.segs[s].tile0;
+            if (l == 0 && lt == 0 && i % kPerTile == 0) a.seg_offsets[s] = (int64_t)run;
+            if (count != 0) {
+                const int64_t wbase = lt * CD_TILE + (i % kPerTile) * (CH * 1024);
+                uint64_t flags;
+                if constexpr (CH == 4) flags = reinterpret_cast<const uint64_t *>(a.flags)[i * kWave + l];
+                else flags = a.flags[i * kWave + l];
+                const uint16_t *b = a.segs[s].b + wbase + 4 * l;
+                const int64_t left = a.segs[s].n - wbase - 4 * l;
+                uint32_t nvp[CH * 8];
+#pragma unroll
+                for (int g = 0; g < CH * 4; ++g) {
+                    const uint32_t f = (uint32_t)(flags >> (4 * g)) & 0xFu;
+                    u32x2 v = {0, 0};
+                    if (f) {
+                        if (left >= g * 256 + 4) v = *reinterpret_cast<const u32x2 *>(b + g * 256);
+                        else {  // the tensor's last one to three elements
+                            v.x = b[g * 256];
+                            if (f & 2u) v.x |= (uint32_t)b[g * 256 + 1] << 16;
+                            if (f & 4u) v.y = b[g * 256 + 2];
+                        }
+                    }
+                    nvp[2 * g] = v.x;
+                    nvp[2 * g + 1] = v.y;
+                }
+                cd_pass2<4 * CH>(a, flags, nvp, wbase, 4 * l, (int64_t)run, s_idx[w], s_val[w]);
             }
         }
-        __syncthreads();
-        if (count != 0)
-            cd_pass2<4 * CH>(a, flags, nvp, wbase, 4 * l, (int64_t)sh.prefix + wpre, sh.sbi[w], sh.sbv[w]);
-    } else if (!ok && threadIdx.x == 0) {
-        or_agent32(a.d_status, 0x10u /*PULSE_DS_BADSEGMENT*/);
+        run += count;
+    }
+    if (last == nw && first < last && l == 0) {
+        a.seg_offsets[a.nseg] = (int64_t)run;
+        if ((int64_t)run > a.cap) or_agent32(a.d_status, 1u /*PULSE_DS_CAPACITY*/);
     }
 }
 
@@ -401,8 +427,8 @@ __global__ __launch_bounds__(CD_THREADS) void k_adamw(AdamArgs a) {
 // underflows below 1e-22), each workgroup's sum over its tiles goes to its own
 // slot, and the workgroup that finishes last adds the slots in their order: no
 // atomic's order reaches the result.
-constexpr int GN_THREADS = 256;
-constexpr int GN_MAX_BLOCKS = 2048;
+constexpr int GN_THREADS = 512;
+constexpr int GN_MAX_BLOCKS = 512;
 
 struct NormArgs {
     const GradSeg *segs;
@@ -415,40 +441,82 @@ struct NormArgs {
     double *partial;
 };
 
-template <int CH, bool BF16G>
+// 16 bytes of a tensor of n elements at element e (FULL: all inside); elements past n read as zero.
+template <bool FULL, bool BF16G>
+__device__ __forceinline__ u32x4 grad16(const void *p, int64_t e, int64_t n) {
+    constexpr int kPer = BF16G ? 8 : 4;
+    if (FULL || e + kPer <= n)
+        return __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4 *>(static_cast<const char *>(p) + e * (16 / kPer)));
+    union {
+        u32x4 v;
+        uint32_t w[4];
+        uint16_t h[8];
+    } u = {};
+#pragma unroll
+    for (int k = 0; k < kPer - 1; ++k)
+        if (e + k < n) {
+            if constexpr (BF16G) u.h[k] = static_cast<const uint16_t *>(p)[e + k];
+            else u.w[k] = static_cast<const uint32_t *>(p)[e + k];
+        }
+    return u.v;
+}
+
+// A thread takes V 16-byte pieces of every gridDim-th part of a tile; the next
+// part's are read while these are added, so that a workgroup has its loads in
+// flight all the time (waiting for each part alone reached 2.7 to 4 TB/s).
+template <int V, bool BF16G>
 __global__ __launch_bounds__(GN_THREADS) void k_grad_norm(NormArgs a) {
-    typedef typename GradVec<BF16G>::T GV;
-    constexpr int kPerTile = 4 / CH;
+    constexpr int kPer = BF16G ? 8 : 4, kPart = V * GN_THREADS * kPer, kParts = CD_TILE / kPart;
     __shared__ double s_sum[GN_THREADS / kWave];
     __shared__ uint32_t s_last;
-    double acc = 0.0;
-    for (uint32_t piece = blockIdx.x; piece < a.npieces; piece += gridDim.x) {
-        const uint32_t tile = piece / kPerTile;
-        const uint32_t s = a.tile_seg[tile];
+    double sum[4] = {0.0, 0.0, 0.0, 0.0};
+    const auto fetch = [&](uint32_t piece, u32x4 *v) {
+        const uint32_t tile = piece / kParts;
+        const uint32_t s = (uint32_t)__builtin_amdgcn_readfirstlane((int)a.tile_seg[tile]);
         GradSeg d{};
         if (s < (uint32_t)a.nseg) d = a.segs[s];
         const int64_t lt = (int64_t)tile - d.tile0;
         if (!(d.g && (reinterpret_cast<uintptr_t>(d.g) & 15u) == 0 && lt >= 0 && lt * CD_TILE < d.n)) {
-            acc = __builtin_nan("");  // a broken table entry: the norm is not a number
-            continue;
-        }
-        const int64_t base = lt * CD_TILE + (int64_t)(piece % kPerTile) * (CH * 4096) + 4 * threadIdx.x;
-        GV v[CH * 4];
-        if (base - 4 * (int64_t)threadIdx.x + CH * 4096 <= d.n) {
+            sum[0] = __builtin_nan("");  // a broken table entry: the norm is not a number
 #pragma unroll
-            for (int g = 0; g < CH * 4; ++g) v[g] = load4<true, GV>(d.g, base + g * 1024, d.n);
+            for (int i = 0; i < V; ++i) v[i] = u32x4{0, 0, 0, 0};
+            return;
+        }
+        const int64_t base = lt * CD_TILE + (int64_t)(piece % kParts) * kPart, e = base + kPer * (int)threadIdx.x;
+        if (base + kPart <= d.n) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = grad16<true, BF16G>(d.g, e + i * (GN_THREADS * kPer), d.n);
         } else {
 #pragma unroll
-            for (int g = 0; g < CH * 4; ++g) v[g] = load4<false, GV>(d.g, base + g * 1024, d.n);
+            for (int i = 0; i < V; ++i) v[i] = grad16<false, BF16G>(d.g, e + i * (GN_THREADS * kPer), d.n);
         }
+    };
+    u32x4 v[V], next[V];
+    uint32_t piece = blockIdx.x;
+    if (piece < a.npieces) fetch(piece, v);
+    while (piece < a.npieces) {
+        piece += gridDim.x;
+        if (piece < a.npieces) fetch(piece, next);
+        sched_fence();
 #pragma unroll
-        for (int g = 0; g < CH * 4; ++g)
+        for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const double x = (double)grad_of<BF16G>(v[g], k);
-                acc = __builtin_fma(x, x, acc);
+                if constexpr (BF16G) {
+                    const double x = (double)__uint_as_float(v[i][k] << 16);
+                    const double y = (double)__uint_as_float(v[i][k] & 0xFFFF0000u);
+                    sum[k] = __builtin_fma(x, x, sum[k]);
+                    sum[k] = __builtin_fma(y, y, sum[k]);
+                } else {
+                    const double x = (double)__uint_as_float(v[i][k]);
+                    sum[k] = __builtin_fma(x, x, sum[k]);
+                }
             }
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = next[i];
     }
+    double acc = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     acc = wave_reduce_sum(acc);
     if (lane_id() == 0) s_sum[wave_id()] = acc;
     __syncthreads();
@@ -457,8 +525,11 @@ __global__ __launch_bounds__(GN_THREADS) void k_grad_norm(NormArgs a) {
 #pragma unroll
         for (int w = 0; w < GN_THREADS / kWave; ++w) t += s_sum[w];
         __hip_atomic_store(&a.partial[blockIdx.x], t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const uint32_t before = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = before == gridDim.x - 1;
+        // the partial sum was written through to memory and has arrived there before the count goes
+        // up: a release and acquire here would write back and invalidate the XCD's whole L2, and
+        // 1024 of them took 50 us
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        s_last = add_agent32(a.done, 1u) == gridDim.x - 1;
     }
     __syncthreads();
     if (!s_last) return;
@@ -486,8 +557,9 @@ __global__ __launch_bounds__(GN_THREADS) void k_grad_norm(NormArgs a) {
 
 using namespace pulse;
 
+// A bit per element and a 4-byte count per wave of the step (4 or 16 of a tile).
 extern "C" size_t pulse_adamw_ws_bytes(int64_t ntiles) {
-    return sizeof(WsHeader) + (size_t)(ntiles > 0 ? ntiles : 1) * 4 * sizeof(uint64_t);
+    return (size_t)(ntiles > 0 ? ntiles : 1) * (CD_TILE / 8 + 16 * sizeof(uint32_t));
 }
 
 extern "C" size_t pulse_grad_norm_ws_bytes(void) { return 256 + GN_MAX_BLOCKS * sizeof(double); }
@@ -498,11 +570,17 @@ namespace {
 // that they spread over the chip.
 constexpr int64_t kWholeTiles = 1024;
 
+constexpr unsigned kPatchBlocks = 2048;
+
 template <int CH, bool BF16G, bool EIGHT>
 void launch_adamw(const AdamArgs &a, hipStream_t stream) {
     const dim3 grid(a.npieces), block(CD_THREADS);
-    if (a.idx) k_adamw<CH, BF16G, EIGHT, true><<<grid, block, 0, stream>>>(a);
-    else k_adamw<CH, BF16G, EIGHT, false><<<grid, block, 0, stream>>>(a);
+    if (a.idx) {
+        k_adamw<CH, BF16G, EIGHT, true><<<grid, block, 0, stream>>>(a);
+        k_adamw_patch<CH><<<dim3(a.npieces < kPatchBlocks ? a.npieces : kPatchBlocks), block, 0, stream>>>(a);
+    } else {
+        k_adamw<CH, BF16G, EIGHT, false><<<grid, block, 0, stream>>>(a);
+    }
 }
 
 template <int CH>
@@ -541,8 +619,8 @@ extern "C" int pulse_launch_adamw(const void *segs, int32_t nseg, const uint32_t
     a.cap = cap;
     a.seg_offsets = seg_offsets;
     a.d_status = d_status;
-    a.hdr = reinterpret_cast<WsHeader *>(ws);
-    a.status = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + sizeof(WsHeader));
+    a.flags = static_cast<uint16_t *>(ws);
+    a.counts = ws ? reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + ntiles * (CD_TILE / 8)) : nullptr;
     if (ntiles >= kWholeTiles) {
         a.npieces = (uint32_t)ntiles;
         launch_adamw_types<4>(a, grad_bf16 != 0, state_bits == 8, stream);
@@ -565,16 +643,17 @@ extern "C" int pulse_launch_grad_norm(const void *segs, int32_t nseg, const uint
     a.out = out;
     a.done = static_cast<uint32_t *>(ws);
     a.partial = reinterpret_cast<double *>(static_cast<char *>(ws) + 256);
+    // 32 KB of gradients at a time, or in lists that would not give every workgroup one 16 KB
     const bool whole = ntiles >= kWholeTiles;
-    const int64_t pieces = whole ? ntiles : ntiles * 4;
+    const int64_t pieces = ntiles * (whole ? 1 : 2) * (grad_bf16 ? 1 : 2);
     a.npieces = (uint32_t)pieces;
     const dim3 grid((unsigned)(pieces < GN_MAX_BLOCKS ? pieces : GN_MAX_BLOCKS)), block(GN_THREADS);
     if (whole) {
         if (grad_bf16) k_grad_norm<4, true><<<grid, block, 0, stream>>>(a);
         else k_grad_norm<4, false><<<grid, block, 0, stream>>>(a);
     } else {
-        if (grad_bf16) k_grad_norm<1, true><<<grid, block, 0, stream>>>(a);
-        else k_grad_norm<1, false><<<grid, block, 0, stream>>>(a);
+        if (grad_bf16) k_grad_norm<2, true><<<grid, block, 0, stream>>>(a);
+        else k_grad_norm<2, false><<<grid, block, 0, stream>>>(a);
     }
     return hipGetLastError() == hipSuccess ? 0 : -5;
 }

@@ -557,6 +557,7 @@ int pulse_adamw_step(const pulse_adamw_segment *segs, int32_t nseg, const uint32
     const bool patch = patch_idx || patch_val || seg_offsets;
     if (patch && !(patch_idx && patch_val && seg_offsets)) return PULSE_EINVAL;
     if (ntiles > kMaxTiles) return PULSE_ERANGE;
+    if (patch && !aligned16(ws)) return PULSE_EALIGN;
     if (patch && (!ws || ws_bytes < pulse_adamw_ws_bytes(ntiles))) return PULSE_EWORKSPACE;
     const double t = (double)q.step;
     const float hyper[8] = {(float)q.lr,    (float)q.beta1, (float)(1.0 - q.beta1),
