@@ -405,6 +405,8 @@ __global__ __launch_bounds__(shrink_waves(RT, MT) * kWave) void k_lora_shrink(Sh
 }
 
 // ---- expand: y += W^T h ---------------------------------------------------------
+constexpr int EX_TILES = 4;  // most tiles of a workgroup
+
 struct ExpandArgs {
     const uint16_t *h;     // [place][Rp]
     const float *partial;  // or its parts [parts][place][Rp] (PART)
@@ -417,46 +419,90 @@ struct ExpandArgs {
     int32_t parts;
 };
 
+// What 16 places of a tile need in expand: a lane's tokens of places 4 q + i,
+// their rows, and h of place c.
+template <int RT>
+struct ExpandRows {
+    i32x4 tok;
+    u32x4 y[4];
+    s16x4 h[RT];
+};
+
 // A wave takes 128 columns of the 64 places of each of its tiles.  Matrix
 // instruction: rows = places, columns = columns of y, 16 ranks.  Lane c of the
 // column axis holds the 8-column piece c, instruction j its column j: then the
 // lane's results i = 0..3 are, for j = 0..7, one 16-byte piece of the row of
-// place 4 q + i, and sixteen lanes touch 256 contiguous bytes.  The rows of the
-// next 16 places are read while these are computed and written.
+// place 4 q + i, and sixteen lanes touch 256 contiguous bytes; neighbouring
+// workgroups take neighbouring columns of the same rows.  The rows and h of the
+// next 16 places are on their way while these are computed and written, into the
+// other of two buffers.  Loads and stores count down one counter in their order,
+// so the body has no branch around either: an empty place stands for the first
+// of its 16 and a lane past the last column for the wave's first piece, and both
+// write again what that one writes.
 template <int RT, bool PART>
 __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), c16 = l & 15, q = l >> 4;
-    // workgroups go round the eight XCDs: with eight column blocks or more, one XCD keeps to
-    // every eighth block and goes through all tiles of it, whose adapters then stay in its L2
-    const int b = blockIdx.x, blocks = (g.C + 511) / 512;
-    const int cb = blocks >= 8 ? ((b >> 3) / g.groups) * 8 + (b & 7) : b % blocks;
-    const int ta = (blocks >= 8 ? (b >> 3) % g.groups : b / blocks) * g.per;
-    const int base = (cb * 4 + w) * 128, col = base + c16 * 8;
+    const int blocks = (g.C + 511) / 512;
+    const int base = ((int)blockIdx.x % blocks * 4 + w) * 128, col = base + c16 * 8 < g.C ? base + c16 * 8 : base;
+    const int ta = (int)blockIdx.x / blocks * g.per, tb = ta + g.per < g.max_tiles ? ta + g.per : g.max_tiles;
+    // the tiles' adapters and tokens wait in LDS: a load behind the stores of a row would wait for those too
+    __shared__ int32_t s_order[EX_TILES * LT], s_slot[EX_TILES], s_count[EX_TILES];
+    const int ti = (int)threadIdx.x / LT;
+    if (ta + ti < tb) {
+        s_order[threadIdx.x] = g.plan.order[(int64_t)ta * LT + threadIdx.x];
+        if (l == 0) {
+            s_slot[ti] = g.plan.tile_slot[ta + ti];
+            s_count[ti] = g.plan.tile_count[ta + ti];
+        }
+    }
+    __syncthreads();
     if (base >= g.C) return;
-    const bool colok = col < g.C;
-    const int tb = ta + g.per < g.max_tiles ? ta + g.per : g.max_tiles;
-    uint16_t *const ycol = g.y + (colok ? col : base);
-    s16x4 frag[RT][8];
-    int cur = -1;
-    for (int tile = ta; tile < tb; ++tile) {
-        const int slot = __builtin_amdgcn_readfirstlane(g.plan.tile_slot[tile]);
-        if ((uint32_t)slot >= (uint32_t)g.S) return;
-        const int raw = __builtin_amdgcn_readfirstlane(g.plan.tile_count[tile]), count = raw < LT ? raw : LT;
-        const int64_t place0 = (int64_t)tile * LT;
-        const int32_t *ord = g.plan.order + place0 + q * 4;
-        // a lane's token of places 4 q + i, -1 also where its columns are past the end; empty
-        // places read the row of the tile's first
-        const int some = token_of(__builtin_amdgcn_readfirstlane(g.plan.order[place0]), g.T);
-        i32x4 tok = *reinterpret_cast<const i32x4 *>(ord);
-        u32x4 yv[4];
-        auto rows = [&](i32x4 &t, u32x4 *v) {
+    uint16_t *const ycol = g.y + col;
+    // a tile's adapter, -1: none, and the number of its tokens
+    const auto slot_of = [&](int tile) {
+        const int s = tile < tb ? __builtin_amdgcn_readfirstlane(s_slot[tile - ta]) : -1;
+        return (uint32_t)s < (uint32_t)g.S ? s : -1;
+    };
+    const auto count_of = [&](int tile) {
+        const int n = __builtin_amdgcn_readfirstlane(s_count[tile - ta]);
+        return n < 1 ? 1 : (n < LT ? n : LT);
+    };
+    const auto read = [&](ExpandRows<RT> &r, int tile, int sub, int count) {
+        const int32_t *const order = s_order + (tile - ta) * LT + sub * 16;
+        const int in = count - sub * 16;  // places of the 16 that hold a token
+        const int64_t at = ((int64_t)tile * LT + sub * 16 + (c16 < in ? c16 : 0)) * (RT * 16) + q * 4;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                t[i] = colok ? token_of(t[i], g.T) : -1;
-                v[i] = ld16(ycol + (int64_t)(t[i] >= 0 ? t[i] : (some < 0 ? 0 : some)) * g.ldy);
+        for (int rt = 0; rt < RT; ++rt) {
+            if constexpr (PART) {
+                f32x4 v = *reinterpret_cast<const f32x4 *>(g.partial + at + rt * 16);
+                for (int p = 1; p < g.parts; ++p)
+                    v += *reinterpret_cast<const f32x4 *>(g.partial + p * g.places * (RT * 16) + at + rt * 16);
+                r.h[rt] = __builtin_bit_cast(s16x4, u32x2{cast_pair(v[0], v[1]), cast_pair(v[2], v[3])});
+            } else {
+                r.h[rt] = __builtin_bit_cast(s16x4, *reinterpret_cast<const u32x2 *>(g.h + at + rt * 16));
             }
-        };
-        rows(tok, yv);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = order[q * 4 + i < in ? q * 4 + i : 0];
+            r.tok[i] = (uint32_t)t < (uint32_t)g.T ? t : 0;
+            r.y[i] = ld16(ycol + (int64_t)r.tok[i] * g.ldy);
+        }
+    };
+    int tile = ta, sub = 0, cur = -1, slot = slot_of(ta);
+    if (slot < 0) return;
+    int count = count_of(ta);
+    s16x4 frag[RT][8];
+    // one step: the next 16 places (or, at the end, these once more) into `next`, these out of `now`
+    const auto step = [&](ExpandRows<RT> &now, ExpandRows<RT> &next) {
+        int tile1 = tile, sub1 = sub + 1, slot1 = slot, count1 = count;
+        if (sub1 * 16 >= count) {
+            slot1 = slot_of(tile + 1);
+            tile1 = tile + 1;
+            sub1 = 0;
+            if (slot1 >= 0) count1 = count_of(tile1);
+        }
+        const bool more = slot1 >= 0;
         if (slot != cur) {
             cur = slot;
 #pragma unroll
@@ -465,9 +511,11 @@ __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = rt * 16 + q * 4 + i;
-                    v[i] = u32x4{0, 0, 0, 0};
-                    if (r < g.R && colok) v[i] = ld16(g.w + ((int64_t)slot * g.R + r) * g.C + col);
+                    v[i] = ld16(g.w + ((int64_t)slot * g.R + (r < g.R ? r : 0)) * g.C + col);
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (rt * 16 + q * 4 + i >= g.R) v[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
                     const u32x2 lo = {__builtin_amdgcn_perm(v[1][d], v[0][d], 0x05040100u),
@@ -479,50 +527,31 @@ __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
                 }
             }
         }
-        for (int sub = 0; sub * 16 < count; ++sub) {
-            i32x4 tok1 = {-1, -1, -1, -1};
-            u32x4 yv1[4];
-            const bool more = (sub + 1) * 16 < count;
-            s16x4 hv[RT];
-            const int64_t at = (place0 + sub * 16 + c16) * (RT * 16) + q * 4;
+        read(next, more ? tile1 : tile, more ? sub1 : sub, more ? count1 : count);
+        sched_fence();
+        f32x4 acc[8];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                if constexpr (PART) {
-                    f32x4 v = *reinterpret_cast<const f32x4 *>(g.partial + at + rt * 16);
-                    for (int p = 1; p < g.parts; ++p)
-                        v += *reinterpret_cast<const f32x4 *>(g.partial + p * g.places * (RT * 16) + at + rt * 16);
-                    hv[rt] = __builtin_bit_cast(s16x4, u32x2{cast_pair(v[0], v[1]), cast_pair(v[2], v[3])});
-                } else {
-                    hv[rt] = __builtin_bit_cast(s16x4, *reinterpret_cast<const u32x2 *>(g.h + at + rt * 16));
-                }
-            }
-            if (more) {
-                tok1 = *reinterpret_cast<const i32x4 *>(ord + (sub + 1) * 16);
-                rows(tok1, yv1);
-            }
-            f32x4 acc[8];
+        for (int j = 0; j < 8; ++j) acc[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] = f32x4{0, 0, 0, 0};
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+            for (int j = 0; j < 8; ++j)
+                acc[j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(now.h[rt], frag[rt][j], acc[j], 0, 0, 0);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(hv[rt], frag[rt][j], acc[j], 0, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+            u32x4 o;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                u32x4 o;
-#pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    o[d] = cast_pair(__uint_as_float(yv[i][d] << 16) + acc[2 * d][i],
-                                     __uint_as_float(yv[i][d] & 0xFFFF0000u) + acc[2 * d + 1][i]);
-                if (tok[i] >= 0) *reinterpret_cast<u32x4 *>(ycol + (int64_t)tok[i] * g.ldy) = o;
-            }
-            if (more) {
-                tok = tok1;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) yv[i] = yv1[i];
-            }
+            for (int d = 0; d < 4; ++d)
+                o[d] = cast_pair(__uint_as_float(now.y[i][d] << 16) + acc[2 * d][i],
+                                 __uint_as_float(now.y[i][d] & 0xFFFF0000u) + acc[2 * d + 1][i]);
+            *reinterpret_cast<u32x4 *>(ycol + (int64_t)now.tok[i] * g.ldy) = o;
         }
+        tile = tile1, sub = sub1, slot = slot1, count = count1;
+        return more;
+    };
+    ExpandRows<RT> even, odd;
+    read(even, tile, 0, count);
+    while (step(even, odd) && step(odd, even)) {
     }
 }
 
@@ -749,7 +778,7 @@ void launch_shrink(const ShrinkArgs &g, int parts, int rt, hipStream_t stream) {
 template <bool PART>
 void launch_expand(const ExpandArgs &g, int rt, hipStream_t stream) {
     const int64_t blocks = ((int64_t)g.C + 511) / 512;
-    const dim3 grid((unsigned)((blocks >= 8 ? (blocks + 7) / 8 * 8 : blocks) * g.groups)), block(256);
+    const dim3 grid((unsigned)(blocks * g.groups)), block(256);
     switch (rt) {
     case 1: k_lora_expand<1, PART><<<grid, block, 0, stream>>>(g); break;
     case 2: k_lora_expand<2, PART><<<grid, block, 0, stream>>>(g); break;
@@ -867,9 +896,9 @@ void expand(const uint16_t *h, const float *partial, int parts, const uint16_t *
     g.parts = parts;
     g.max_tiles = (int32_t)lora_max_tiles(T, S);
     g.places = (int64_t)g.max_tiles * LT;
-    // tiles of a workgroup, whose adapter is then read and transposed once: up to 4, 2048 workgroups or more
+    // tiles of a workgroup, whose adapter is then read and transposed once: up to EX_TILES, 2048 workgroups or more
     const int64_t per = g.max_tiles * ((C + 511) / 512) / 2048;
-    g.per = (int32_t)(per < 1 ? 1 : (per > 4 ? 4 : per));
+    g.per = (int32_t)(per < 1 ? 1 : (per > EX_TILES ? EX_TILES : per));
     g.groups = (g.max_tiles + g.per - 1) / g.per;
     const int rt = (int)((R + 15) / 16);
     if (parts > 1) launch_expand<true>(g, rt, stream);
