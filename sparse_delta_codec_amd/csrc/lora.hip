@@ -78,9 +78,10 @@ inline int64_t lora_plan_size(int64_t T, int64_t S) {
 // adapter in its own row of an LDS table; the rows' prefix sums give each wave
 // its first place for every adapter; then every wave deals its tokens out in
 // order, 64 at a time, ranking equal adapters with ballots.  It is bound by
-// latency: the ids are read eight loads at a time, and one lane of each adapter
+// latency: the ids are read sixteen loads at a time and stay in registers up to 16384
+// tokens, and one lane of each adapter
 // counts for the 64 (equal lanes' LDS atomics would queue).
-constexpr int LP_AHEAD = 8;
+constexpr int LP_AHEAD = 16;
 
 // a lane's ids of the next tokens; -1 past the end
 __device__ __forceinline__ void read_ids(const int32_t *__restrict__ ids, int t, int t1, int (&id)[LP_AHEAD]) {
@@ -104,7 +105,7 @@ __global__ __launch_bounds__(NW *kWave) void k_lora_plan(const int32_t *__restri
                                                          uint32_t *d_status) {
     constexpr int kThreads = NW * kWave, kPer = LP_ADAPTERS / kThreads > 1 ? LP_ADAPTERS / kThreads : 1;
     extern __shared__ int32_t sh[];  // [NW][S] counts, then first places; [S] counts; [S] first tiles; [S] first groups
-    __shared__ int32_t s_scan[NW];
+    __shared__ int32_t s_scan[2][NW];
     int32_t *const s_cnt = sh + NW * S, *const s_tile = s_cnt + S, *const s_group = s_tile + S;
     const int tid = threadIdx.x, w = wave_id(), l = lane_id();
     const int per = ((T + NW - 1) / NW + kWave - 1) / kWave * kWave;
@@ -128,39 +129,52 @@ __global__ __launch_bounds__(NW *kWave) void k_lora_plan(const int32_t *__restri
     }
     if (__ballot(bad) && l == 0) or_agent32(d_status, 2u /*PULSE_DS_BADINDEX*/);
     __syncthreads();
-    // a thread's adapters: their counts, their tiles, every wave's first place
-    int cnt[kPer], tiles[kPer], sum = 0, gsum = 0, total, gtotal;
+    // a thread's adapters: every wave's tokens before it, tiles, and groups of 16 places
+    int before[kPer][NW], cnt[kPer], tsum = 0, gsum = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int a = kPer * tid + k;
-        cnt[k] = 0;
-        if (a < S) {
 #pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                const int c = sh[i * S + a];
-                sh[i * S + a] = cnt[k];
-                cnt[k] += c;
-            }
+        for (int i = 0; i < NW; ++i) before[k][i] = a < S ? sh[i * S + a] : 0;
+        cnt[k] = 0;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            const int c = before[k][i];
+            before[k][i] = cnt[k];
+            cnt[k] += c;
         }
-        tiles[k] = (cnt[k] + LT - 1) / LT;
-        sum += tiles[k];
+        tsum += (cnt[k] + LT - 1) / LT;
         gsum += (cnt[k] + 15) / 16;
     }
-    int first = block_excl_sum<NW>(sum, s_scan, &total);
-    int gfirst = block_excl_sum<NW>(gsum, s_scan, &gtotal);
+    // the first tile and group of the thread's adapters, and the totals
+    int first = wave_incl_sum(tsum), gfirst = wave_incl_sum(gsum), total = 0, gtotal = 0;
+    if (l == kWave - 1) {
+        s_scan[0][w] = first;
+        s_scan[1][w] = gfirst;
+    }
+    first -= tsum;
+    gfirst -= gsum;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        const int t = s_scan[0][i], n = s_scan[1][i];
+        first += i < w ? t : 0;
+        gfirst += i < w ? n : 0;
+        total += t;
+        gtotal += n;
+    }
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int a = kPer * tid + k;
         if (a < S) {
 #pragma unroll
-            for (int i = 0; i < NW; ++i) sh[i * S + a] += first * LT;
+            for (int i = 0; i < NW; ++i) sh[i * S + a] = first * LT + before[k][i];
             s_cnt[a] = cnt[k];
             s_tile[a] = first;
             s_group[a] = gfirst;
             p.slot_tile[a] = first;
-            for (int i = cnt[k]; i < tiles[k] * LT; ++i) p.order[first * LT + i] = -1;
         }
-        first += tiles[k];
+        first += (cnt[k] + LT - 1) / LT;
         gfirst += (cnt[k] + 15) / 16;
     }
     if (tid == 0) {
@@ -186,33 +200,33 @@ __global__ __launch_bounds__(NW *kWave) void k_lora_plan(const int32_t *__restri
             __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         }
     }
-    // the adapter of a tile (or of 16 places): the last one that begins at or before it (an empty
-    // one begins where the next does)
-    const auto owner = [&](const int32_t *begin, int i) {
-        int lo = 0, hi = S;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (begin[mid] <= i) lo = mid;
-            else hi = mid;
-        }
-        return lo;
-    };
-    for (int i = tid; i < max_tiles; i += kThreads) {
-        const int a = i < total ? owner(s_tile, i) : -1;
-        p.tile_slot[i] = a;
-        if (a >= 0) {
-            const int c = s_cnt[a] - (i - s_tile[a]) * LT;
-            p.tile_count[i] = c < LT ? c : LT;
-        }
+    // the places past an adapter's last token are empty
+    for (int a = w; a < S; a += NW) {
+        const int c = s_cnt[a];
+        if (l >= c % LT && c % LT != 0) p.order[(s_tile[a] + c / LT) * LT + l] = -1;
     }
+    // a group's adapter: the last one that begins at or before it (an empty one begins where the next
+    // does); every fourth of an adapter begins a tile
     for (int i = tid; i < max_groups; i += kThreads) {
         int v = -1;
         if (i < gtotal) {
-            const int a = owner(s_group, i);
-            v = s_tile[a] * 4 + i - s_group[a];
+            int lo = 0, hi = S;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (s_group[mid] <= i) lo = mid;
+                else hi = mid;
+            }
+            const int n = i - s_group[lo];
+            v = s_tile[lo] * 4 + n;
+            if (n % 4 == 0) {
+                const int c = s_cnt[lo] - n * 16;
+                p.tile_slot[v / 4] = lo;
+                p.tile_count[v / 4] = c < LT ? c : LT;
+            }
         }
         p.group[i] = v;
     }
+    for (int i = total + tid; i < max_tiles; i += kThreads) p.tile_slot[i] = -1;
 }
 
 // ---- what the kernels share -----------------------------------------------------
@@ -241,7 +255,23 @@ inline LoraHidden lora_hidden_parts(void *h, int64_t T, int64_t S, int64_t R, bo
 // tokens, adapters, counts and chunks out of range are taken as empty or cut off.
 __device__ __forceinline__ int token_of(int t, int T) { return (uint32_t)t < (uint32_t)T ? t : -1; }
 
+// Where the row of place i of a list that begins with a tile lies; an empty place
+// stands for the first of its 16, or of its tile where those are all empty.
+__device__ __forceinline__ int64_t row_of(const int32_t *order, int i, int T, int64_t ld) {
+    int t = token_of(order[i], T);
+    if (t < 0) t = token_of(order[i & ~15], T);
+    if (t < 0) t = token_of(order[i & ~(LT - 1)], T);
+    return (t < 0 ? 0 : t) * ld;
+}
+
 __device__ __forceinline__ u32x4 ld16(const uint16_t *p) { return *reinterpret_cast<const u32x4 *>(p); }
+
+// What is read once goes past the last-level cache: there it would displace lines
+// that earlier kernels left to be written back, which halves its rate (470 MB after
+// a 512 MB copy: 4.3 TB/s, non-temporal 6.0).
+__device__ __forceinline__ u32x4 ld16_once(const uint16_t *p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+}
 
 __device__ __forceinline__ bf16x8 as_bf(const u32x4 &v) { return __builtin_bit_cast(bf16x8, v); }
 
@@ -337,7 +367,7 @@ __global__ __launch_bounds__(shrink_waves(RT, MT) * kWave) void k_lora_shrink(Sh
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) xr[m][i] = ld16(px[m][i] + kc);
+            for (int i = 0; i < 4; ++i) xr[m][i] = ld16_once(px[m][i] + kc);
         if (s * 128 + 128 > g.C && k >= g.C) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
@@ -406,10 +436,11 @@ __global__ __launch_bounds__(shrink_waves(RT, MT) * kWave) void k_lora_shrink(Sh
 
 // ---- expand: y += W^T h ---------------------------------------------------------
 constexpr int EX_TILES = 4;  // most tiles of a workgroup
+enum ExpandMode { EX_PLAIN, EX_PARTS, EX_ONCE };  // EX_PARTS: h in parts; EX_ONCE: y past the last-level cache
 
 struct ExpandArgs {
     const uint16_t *h;     // [place][Rp]
-    const float *partial;  // or its parts [parts][place][Rp] (PART)
+    const float *partial;  // or its parts [parts][place][Rp] (EX_PARTS)
     const uint16_t *w;     // [S][R][C]
     uint16_t *y;
     int64_t ldy;
@@ -419,11 +450,11 @@ struct ExpandArgs {
     int32_t parts;
 };
 
-// What 16 places of a tile need in expand: a lane's tokens of places 4 q + i,
-// their rows, and h of place c.
+// What 16 places of a tile need in expand: where a lane's rows of places 4 q + i
+// lie, the rows, and h of place c.
 template <int RT>
 struct ExpandRows {
-    i32x4 tok;
+    int64_t at[4];
     u32x4 y[4];
     s16x4 h[RT];
 };
@@ -439,17 +470,18 @@ struct ExpandRows {
 // so the body has no branch around either: an empty place stands for the first
 // of its 16 and a lane past the last column for the wave's first piece, and both
 // write again what that one writes.
-template <int RT, bool PART>
+template <int RT, int MODE>
 __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), c16 = l & 15, q = l >> 4;
     const int blocks = (g.C + 511) / 512;
     const int base = ((int)blockIdx.x % blocks * 4 + w) * 128, col = base + c16 * 8 < g.C ? base + c16 * 8 : base;
     const int ta = (int)blockIdx.x / blocks * g.per, tb = ta + g.per < g.max_tiles ? ta + g.per : g.max_tiles;
-    // the tiles' adapters and tokens wait in LDS: a load behind the stores of a row would wait for those too
-    __shared__ int32_t s_order[EX_TILES * LT], s_slot[EX_TILES], s_count[EX_TILES];
+    // the tiles' adapters and rows wait in LDS: a load behind the stores of a row would wait for those too
+    __shared__ int64_t s_row[EX_TILES * LT];
+    __shared__ int32_t s_slot[EX_TILES], s_count[EX_TILES];
     const int ti = (int)threadIdx.x / LT;
     if (ta + ti < tb) {
-        s_order[threadIdx.x] = g.plan.order[(int64_t)ta * LT + threadIdx.x];
+        s_row[threadIdx.x] = row_of(g.plan.order + (int64_t)ta * LT, threadIdx.x, g.T, g.ldy);
         if (l == 0) {
             s_slot[ti] = g.plan.tile_slot[ta + ti];
             s_count[ti] = g.plan.tile_count[ta + ti];
@@ -468,12 +500,12 @@ __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
         return n < 1 ? 1 : (n < LT ? n : LT);
     };
     const auto read = [&](ExpandRows<RT> &r, int tile, int sub, int count) {
-        const int32_t *const order = s_order + (tile - ta) * LT + sub * 16;
+        const int64_t *const row = s_row + (tile - ta) * LT + sub * 16 + q * 4;
         const int in = count - sub * 16;  // places of the 16 that hold a token
         const int64_t at = ((int64_t)tile * LT + sub * 16 + (c16 < in ? c16 : 0)) * (RT * 16) + q * 4;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            if constexpr (PART) {
+            if constexpr (MODE == EX_PARTS) {
                 f32x4 v = *reinterpret_cast<const f32x4 *>(g.partial + at + rt * 16);
                 for (int p = 1; p < g.parts; ++p)
                     v += *reinterpret_cast<const f32x4 *>(g.partial + p * g.places * (RT * 16) + at + rt * 16);
@@ -483,11 +515,9 @@ __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = order[q * 4 + i < in ? q * 4 + i : 0];
-            r.tok[i] = (uint32_t)t < (uint32_t)g.T ? t : 0;
-            r.y[i] = ld16(ycol + (int64_t)r.tok[i] * g.ldy);
-        }
+        for (int i = 0; i < 4; ++i) r.at[i] = row[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.y[i] = MODE == EX_ONCE ? ld16_once(ycol + r.at[i]) : ld16(ycol + r.at[i]);
     };
     int tile = ta, sub = 0, cur = -1, slot = slot_of(ta);
     if (slot < 0) return;
@@ -544,7 +574,9 @@ __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
             for (int d = 0; d < 4; ++d)
                 o[d] = cast_pair(__uint_as_float(now.y[i][d] << 16) + acc[2 * d][i],
                                  __uint_as_float(now.y[i][d] & 0xFFFF0000u) + acc[2 * d + 1][i]);
-            *reinterpret_cast<u32x4 *>(ycol + (int64_t)now.tok[i] * g.ldy) = o;
+            u32x4 *const to = reinterpret_cast<u32x4 *>(ycol + now.at[i]);
+            if constexpr (MODE == EX_ONCE) __builtin_nontemporal_store(o, to);
+            else *to = o;
         }
         tile = tile1, sub = sub1, slot = slot1, count = count1;
         return more;
@@ -563,7 +595,8 @@ struct OuterSide {
     float *out;               // [S][R][C]
     float *partial;           // [chunks][2][R][C]
     int32_t C;
-    int32_t waves;            // column blocks
+    int32_t blocks;           // column blocks, one wave each
+    int32_t q, chunks;        // tiles of a chunk
 };
 
 struct OuterArgs {
@@ -571,8 +604,12 @@ struct OuterArgs {
     LoraPlan plan;
     int64_t places;
     int32_t T, R, S, max_tiles;
-    int32_t q, chunks, accumulate, wg0;  // q: tiles of a chunk; wg0: workgroups of side 0 per chunk
+    int32_t accumulate, wg0;  // wg0: workgroups of side 0 per chunk
+    const uint16_t *w;        // FUSE: [S][R][C] what shrink multiplies z with
+    float *sums;              // FUSE: [workgroups of a chunk][32 places][512 RT] their sums, as the lanes hold them
 };
+
+constexpr int OU_TILES = 32;  // most tiles of a chunk
 
 template <int W>
 struct ZVec;
@@ -585,34 +622,67 @@ struct ZVec<4> {
     typedef u32x2 T;
 };
 
-// A wave takes 16 W columns and one chunk of q tiles, 32 places at a time: the
-// rows of the next 32 are read while these are multiplied, the places' tokens
-// one step before that.  Matrix instruction: rows = ranks, columns = columns of
-// z, 32 places.  Lane c of the column axis holds W neighbouring columns of eight
-// places, transposed in registers; instruction j takes its column j, once for
-// each part of u.  A chunk may cover several adapters and an adapter several
-// chunks: a run that lies in one chunk goes straight to the output, the others
-// to the chunk's partial sums (0: continues an earlier chunk's run, 1: begins
-// here), which k_lora_outer_sum adds in order.
-template <int RT, int W>
-__global__ __launch_bounds__(256) void k_lora_outer(OuterArgs g) {
+// What 32 places need in outer: a lane's W columns of eight rows, and u where the
+// registers hold it twice (AHEAD).
+template <int RT, int W, bool AHEAD>
+struct OuterRows {
+    typename ZVec<W>::T z[8];
+    u32x4 u[3][AHEAD ? RT : 1];
+};
+
+// A wave takes 16 W columns and one chunk of tiles, 32 places at a time; the next
+// 32 places' rows are on their way meanwhile, into the other of two buffers.
+// Matrix instruction: rows = ranks, columns = columns of z, 32 places.  Lane c of
+// the column axis holds W neighbouring columns of eight places, transposed in
+// registers; instruction j takes its column j, once for each part of u.  A chunk
+// may cover several adapters and an adapter several chunks: a run that lies in
+// one chunk goes straight to the output, the others to the chunk's partial sums
+// (0: continues an earlier chunk's run, 1: begins here), which k_lora_outer_sum
+// adds in order.
+// FUSE: z is dy, and the same read serves dh = s B dy: the rows go through LDS
+// into the order that shrink multiplies them in, the eight waves' sums over 128
+// columns each are added there, and k_lora_join adds the workgroups'.
+template <int RT, int W, bool FUSE>
+__global__ __launch_bounds__(FUSE ? 512 : 256) void k_lora_outer(OuterArgs g) {
     typedef typename ZVec<W>::T ZV;
+    constexpr int NW = FUSE ? 8 : 4;
+    constexpr bool AHEAD = FUSE ? RT == 1 : RT <= 3;
+    typedef OuterRows<RT, W, AHEAD> Rows;
+    __shared__ int64_t s_row[OU_TILES * LT];
+    __shared__ int32_t s_slot[OU_TILES], s_count[OU_TILES];
+    __shared__ u32x4 s_stage[FUSE ? NW : 1][FUSE ? 512 : 1];
+    __shared__ f32x4 s_sum[FUSE ? 2 : 1][FUSE ? NW : 1][FUSE ? 128 * RT : 1];
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), c16 = l & 15, q = l >> 4;
     const int sd = (int)blockIdx.x >= g.wg0 ? 1 : 0;
     const OuterSide &s = g.side[sd];
-    const int cb = ((int)blockIdx.x - (sd ? g.wg0 : 0)) * 4 + w, chunk = blockIdx.y;
-    if (cb >= s.waves) return;
+    const int chunk = blockIdx.y, ta = chunk * s.q;
     const int ntiles = *g.plan.ntiles < g.max_tiles ? *g.plan.ntiles : g.max_tiles;
-    const int ta = chunk * g.q, tb = ta + g.q < ntiles ? ta + g.q : ntiles;
-    if (ta >= tb) return;
-    const int col = cb * 16 * W + c16 * W;
+    const int tb = ta + s.q < ntiles ? ta + s.q : ntiles;
+    if (chunk >= s.chunks || ta >= tb) return;
+    for (int i = threadIdx.x; i < (tb - ta) * LT; i += NW * kWave) {
+        s_row[i] = row_of(g.plan.order + (int64_t)ta * LT, i, g.T, s.ldz);
+        if (i < tb - ta) {
+            s_slot[i] = g.plan.tile_slot[ta + i];
+            s_count[i] = g.plan.tile_count[ta + i];
+        }
+    }
+    __syncthreads();
+    const int cb = ((int)blockIdx.x - (sd ? g.wg0 : 0)) * NW + w, base = cb * 16 * W, col = base + c16 * W;
+    if (!FUSE && cb >= s.blocks) return;  // (FUSE: the wave still meets the others at their barriers)
     const bool colok = col < s.C;
-    const uint16_t *const zcol = s.z + (colok ? col : cb * 16 * W);
-    const int some = token_of(__builtin_amdgcn_readfirstlane(g.plan.order[(int64_t)ta * LT]), g.T);
+    const uint16_t *const zcol = s.z + (colok ? col : (base < s.C ? base : 0));
+    const auto slot_of = [&](int tile) {
+        const int v = tile < tb ? __builtin_amdgcn_readfirstlane(s_slot[tile - ta]) : -1;
+        return (uint32_t)v < (uint32_t)g.S ? v : -1;
+    };
+    const auto count_of = [&](int tile) {
+        const int n = __builtin_amdgcn_readfirstlane(s_count[tile - ta]);
+        return n < 1 ? 1 : (n < LT ? n : LT);
+    };
     f32x4 acc[RT][W];
-    auto flush = [&](int slot) {
+    const auto flush = [&](int slot) __attribute__((always_inline)) {
         const int t0 = g.plan.slot_tile[slot], t1 = g.plan.slot_tile[slot + 1];
-        const bool direct = t0 / g.q == (t1 - 1) / g.q;
+        const bool direct = t0 / s.q == (t1 - 1) / s.q;
         float *o = direct ? s.out + (int64_t)slot * g.R * s.C
                           : s.partial + ((int64_t)chunk * 2 + (t0 >= ta ? 1 : 0)) * g.R * s.C;
 #pragma unroll
@@ -631,83 +701,164 @@ __global__ __launch_bounds__(256) void k_lora_outer(OuterArgs g) {
                 }
             }
     };
-    // the eight places of lane q in the 32 from place h 32 on
-    auto order_at = [&](int h, i32x4 *o) {
-        const int32_t *p = g.plan.order + (int64_t)h * 32 + q * 8;
-        o[0] = *reinterpret_cast<const i32x4 *>(p);
-        o[1] = *reinterpret_cast<const i32x4 *>(p + 4);
-    };
-    auto rows_at = [&](const i32x4 *o, ZV *z) {
+    const auto read = [&](Rows &r, int tile, int half) __attribute__((always_inline)) {
+        const int64_t *const row = s_row + (tile - ta) * LT + half * 32 + q * 8;
+        const int64_t place = (int64_t)tile * LT + half * 32 + q * 8;
+        int64_t at[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int t = token_of(o[i >> 2][i & 3], g.T);
-            z[i] = *reinterpret_cast<const ZV *>(zcol + (int64_t)(t >= 0 ? t : (some < 0 ? 0 : some)) * s.ldz);
-        }
-    };
-    i32x4 ord[2], ord1[2];
-    ZV z[8], z1[8];
-    order_at(2 * ta, ord);
-    rows_at(ord, z);
-    order_at(2 * ta + 1, ord1);
-    int cur = -1, count = 0;
-    for (int h = 2 * ta; h < 2 * tb; ++h) {
-        if (!(h & 1)) {
-            const int slot = __builtin_amdgcn_readfirstlane(g.plan.tile_slot[h >> 1]);
-            if ((uint32_t)slot >= (uint32_t)g.S) break;
-            const int raw = __builtin_amdgcn_readfirstlane(g.plan.tile_count[h >> 1]);
-            count = raw < LT ? raw : LT;
-            if (slot != cur) {
-                if (cur >= 0) flush(cur);
-                cur = slot;
+        for (int i = 0; i < 8; ++i) at[i] = row[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.z[i] = __builtin_nontemporal_load(reinterpret_cast<const ZV *>(zcol + at[i]));
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int j = 0; j < W; ++j) acc[rt][j] = f32x4{0, 0, 0, 0};
-            }
+                    r.u[p][rt] = ld16(s.part[p] + (int64_t)(rt * 16 + c16) * g.places + place);
         }
-        const int first = (h & 1) * 32, left = count - first;
-        u32x4 u[3][RT];
-        if (left > 0) {
+    };
+    int tile = ta, half = 0, cur = -1, slot = slot_of(ta), buf = 0;
+    if (slot < 0) return;
+    int count = count_of(ta);
+    u32x4 wf[FUSE ? 4 : 1][RT];
+    // one step: the next 32 places (or, at the end, these once more) into `next`, these out of `now`
+    const auto step = [&](Rows &now, Rows &next) __attribute__((always_inline)) {
+        int tile1 = tile, half1 = 1, slot1 = slot, count1 = count;
+        if (half == 1 || count <= 32) {
+            tile1 = tile + 1;
+            half1 = 0;
+            slot1 = slot_of(tile1);
+            if (slot1 >= 0) count1 = count_of(tile1);
+        }
+        const bool more = slot1 >= 0;
+        if (slot != cur) {
+            if (cur >= 0) flush(cur);
+            cur = slot;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int p = 0; p < 3; ++p)
-                    u[p][rt] = ld16(s.part[p] + (int64_t)(rt * 16 + c16) * g.places + (int64_t)h * 32 + q * 8);
-        }
-        if (h + 1 < 2 * tb) rows_at(ord1, z1);
-        if (left > 0) {
-            if (left < 32) {  // empty places: no row, and past the last 16 that hold a token no u
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (token_of(ord[i >> 2][i & 3], g.T) < 0) z[i] = ZV{};
-                const bool none = q * 8 >= (left + 15) / 16 * 16;
+                for (int j = 0; j < W; ++j) acc[rt][j] = f32x4{0, 0, 0, 0};
+            if constexpr (FUSE) {
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                    for (int p = 0; p < 3; ++p)
-                        if (none) u[p][rt] = u32x4{0, 0, 0, 0};
-            }
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
-                u32x4 zt;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) zt[d] = __builtin_amdgcn_perm(z[2 * d + 1][j >> 1], z[2 * d][j >> 1], sel);
-#pragma unroll
-                for (int p = 2; p >= 0; --p)
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        acc[rt][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(u[p][rt]), as_bf(zt), acc[rt][j], 0,
-                                                                            0, 0);
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = rt * 16 + c16, c = base + (k * 4 + q) * 8;
+                        wf[k][rt] = u32x4{0, 0, 0, 0};
+                        if (r < g.R && c < s.C) wf[k][rt] = ld16(g.w + ((int64_t)slot * g.R + r) * s.C + c);
+                    }
             }
         }
+        u32x4 u[3][RT];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) ord[i] = ord1[i];
+        for (int p = 0; p < 3; ++p)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = z1[i];
-        if (h + 2 < 2 * tb) order_at(h + 2, ord1);
+            for (int rt = 0; rt < RT; ++rt) {
+                if constexpr (AHEAD) u[p][rt] = now.u[p][rt];
+                else u[p][rt] = ld16(s.part[p] + (int64_t)(rt * 16 + c16) * g.places + (int64_t)tile * LT + half * 32 + q * 8);
+            }
+        read(next, more ? tile1 : tile, more ? half1 : half);
+        sched_fence();
+        const int left = count - half * 32;
+        if (left < 32) {  // empty places: no row, and past the last 16 that hold a token no u
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (q * 8 + i >= left) now.z[i] = ZV{};
+            const bool none = q * 8 >= (left + 15) / 16 * 16;
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+                    if (none) u[p][rt] = u32x4{0, 0, 0, 0};
+        }
+        if constexpr (FUSE) {
+            if (base + 128 > s.C && !colok) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) now.z[i] = ZV{};
+            }
+            u32x4 *const st = s_stage[w];
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+#pragma unroll
+            for (int i = 0; i < 8; ++i) st[staged(q * 8 + i, c16)] = now.z[i];
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        }
+        u32x4 zt[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                zt[j][d] = __builtin_amdgcn_perm(now.z[2 * d + 1][j >> 1], now.z[2 * d][j >> 1],
+                                                 (j & 1) ? 0x07060302u : 0x05040100u);
+#pragma unroll
+        for (int p = 2; p >= 0; --p)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    acc[rt][j] =
+                        __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(u[p][rt]), as_bf(zt[j]), acc[rt][j], 0, 0, 0);
+        if constexpr (FUSE) {
+            u32x4 *const st = s_stage[w];
+            f32x4 sum[2][RT];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) sum[m][rt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const u32x4 zv = st[staged(m * 16 + c16, k * 4 + q)];
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        sum[m][rt] =
+                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(wf[k][rt]), as_bf(zv), sum[m][rt], 0, 0, 0);
+                }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) s_sum[buf][w][(m * RT + rt) * kWave + l] = sum[m][rt];
+            lds_barrier();  // the one barrier of a step: the other buffer's sums were read before it
+            const float *in = reinterpret_cast<const float *>(&s_sum[buf][0][0]);
+            float *out = g.sums + ((int64_t)blockIdx.x * (g.max_tiles * 2) + tile * 2 + half) * (512 * RT);
+#pragma unroll
+            for (int k = 0; k < RT; ++k) {
+                const int e = k * 512 + (int)threadIdx.x;
+                float v = in[e];
+#pragma unroll
+                for (int p = 1; p < NW; ++p) v += in[p * 512 * RT + e];
+                out[e] = v;
+            }
+            buf ^= 1;
+        }
+        tile = tile1, half = half1, slot = slot1, count = count1;
+        return more;
+    };
+    Rows even, odd;
+    read(even, tile, 0);
+    while (step(even, odd) && step(odd, even)) {
     }
-    if (cur >= 0) flush(cur);
+    flush(cur);
+}
+
+// dh of 32 places from the fused pass's sums, a workgroup's after the other.
+template <int RT>
+__global__ __launch_bounds__(128 * RT) void k_lora_join(const float *__restrict__ sums, int32_t parts,
+                                                        const float *__restrict__ scales, LoraPlan plan, LoraHidden h,
+                                                        int32_t max_tiles, int32_t S, int32_t R) {
+    const int tile = blockIdx.x >> 1, half = blockIdx.x & 1, slot = plan.tile_slot[tile];
+    if ((uint32_t)slot >= (uint32_t)S) return;
+    const int left = plan.tile_count[tile] - half * 32;
+    if (left <= 0) return;
+    const f32x4 *in = reinterpret_cast<const f32x4 *>(sums) + (int64_t)blockIdx.x * (128 * RT) + threadIdx.x;
+    const float scale = scales[slot];
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) v += in[(int64_t)p * (max_tiles * 2) * (128 * RT)];
+    const int lane = threadIdx.x & 63, c = threadIdx.x >> 6, place = c / RT * 16 + (lane & 15);
+    const int r = c % RT * 16 + (lane >> 4) * 4;
+    v = place < left && r < R ? v * scale : f32x4{0, 0, 0, 0};
+    store_hidden(h, (int64_t)blockIdx.x * 32 + place, (int64_t)max_tiles * LT, RT * 16, r, v);
 }
 
 // The gradients of adapters that lie in several chunks: their partial sums in
@@ -718,11 +869,11 @@ __global__ __launch_bounds__(256) void k_lora_outer_sum(OuterArgs g) {
     const int t0 = g.plan.slot_tile[slot], t1 = g.plan.slot_tile[slot + 1];
     const int64_t n = (int64_t)g.R * s.C;
     const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (e >= n || (t1 > t0 && t0 / g.q == (t1 - 1) / g.q) || (t1 == t0 && g.accumulate)) return;
+    if (e >= n || (t1 > t0 && t0 / s.q == (t1 - 1) / s.q) || (t1 == t0 && g.accumulate)) return;
     float *o = s.out + (int64_t)slot * n + e;
     f32x4 v = {0, 0, 0, 0};
     if (t1 > t0) {
-        const int c0 = t0 / g.q, c1 = (t1 - 1) / g.q < g.chunks ? (t1 - 1) / g.q : g.chunks - 1;
+        const int c0 = t0 / s.q, c1 = (t1 - 1) / s.q < s.chunks ? (t1 - 1) / s.q : s.chunks - 1;
         if (g.accumulate) v = *reinterpret_cast<const f32x4 *>(o);
 #pragma unroll 4
         for (int c = c0 < 0 ? 0 : c0; c <= c1; ++c)
@@ -735,26 +886,49 @@ __global__ __launch_bounds__(256) void k_lora_outer_sum(OuterArgs g) {
 // Columns of a wave in outer: 128, or 64 where 128 columns' sums leave no registers to read ahead.
 int lora_outer_width(int64_t R) { return R > 48 ? 64 : 128; }
 
-int64_t lora_outer_waves(int64_t K, int64_t N, int64_t R) {
-    const int64_t width = lora_outer_width(R);
-    return (K + width - 1) / width + (N + width - 1) / width;
+int64_t lora_outer_blocks(int64_t C, int64_t R) { return (C + lora_outer_width(R) - 1) / lora_outer_width(R); }
+
+// Tiles of a chunk in outer: about 2048 waves over the column blocks of a launch, 128 tokens or more.
+int lora_chunk(int64_t T, int64_t S, int64_t blocks) {
+    const int64_t q = lora_max_tiles(T, S) * blocks / 2048;
+    return (int)(q < 2 ? 2 : (q > OU_TILES ? OU_TILES : q));
 }
 
-// Tiles of a chunk in outer: about 2048 waves over both sides, 128 tokens or more.
-int lora_chunk(int64_t T, int64_t S, int64_t K, int64_t N, int64_t R) {
-    const int64_t q = lora_max_tiles(T, S) * lora_outer_waves(K, N, R) / 2048;
-    return (int)(q < 2 ? 2 : (q > 64 ? 64 : q));
+// The backward pass reads dy once, for dh and dB together, where that saves more
+// than it costs: from 64 MB of dy on (below, dy comes from the caches the second
+// time and the launch more is felt), and to rank 32 (two rank tiles: the sums of
+// more leave no registers to read ahead).
+bool lora_fused(int64_t T, int64_t N, int64_t R) { return R <= 32 && T * N >= (int64_t)1 << 25; }
+
+int64_t lora_fused_groups(int64_t N) { return (N + 1023) / 1024; }
+
+// Tiles of a chunk in the fused pass: one workgroup a compute unit, in one or two
+// rounds, whichever comes to fewer tiles one after the other.
+int lora_fused_chunk(int64_t T, int64_t S, int64_t N) {
+    const int64_t mt = lora_max_tiles(T, S), groups = lora_fused_groups(N);
+    int64_t best = OU_TILES, cost = INT64_MAX;
+    for (int64_t rounds = 1; rounds <= 2; ++rounds) {
+        const int64_t chunks = 256 * rounds / groups > 1 ? 256 * rounds / groups : 1, q = (mt + chunks - 1) / chunks;
+        if (q <= OU_TILES && q * rounds < cost) best = q, cost = q * rounds;
+    }
+    return (int)best;
 }
 
 int64_t lora_chunks(int64_t T, int64_t S, int q) { return (lora_max_tiles(T, S) + q - 1) / q; }
 
-// Most chunks of this T and every smaller one: a chunk has 2 tiles (and there are
-// fewer than 3 times those that make 2048 waves), or more than 3/4 of the tiles
-// that make 2048 waves, or 64 tiles.
-int64_t lora_most_chunks(int64_t T, int64_t S, int64_t K, int64_t N, int64_t R) {
-    const int64_t mt = lora_max_tiles(T, S), a = mt / 2 + 1, b = 3072 / lora_outer_waves(K, N, R) + 2, c = mt / 64 + 1;
+// Most chunks of this T and every smaller one.  Outer alone: a chunk has 2 tiles
+// (and there are fewer than 3 times those that make 2048 waves), or more than 3/4
+// of the tiles that make 2048 waves, or OU_TILES tiles.  Fused: two rounds, or
+// OU_TILES tiles.
+int64_t lora_most_chunks(int64_t T, int64_t S, int64_t blocks) {
+    const int64_t mt = lora_max_tiles(T, S), a = mt / 2 + 1, b = 3072 / blocks + 2, c = mt / OU_TILES + 1;
     const int64_t m = a < b ? a : b;
     return m > c ? m : c;
+}
+
+int64_t lora_most_fused_chunks(int64_t T, int64_t S, int64_t N) {
+    const int64_t a = 512 / lora_fused_groups(N) + 1, b = lora_max_tiles(T, S) / OU_TILES + 1;
+    return a > b ? a : b;
 }
 
 template <int MT, bool PART>
@@ -775,19 +949,19 @@ void launch_shrink(const ShrinkArgs &g, int parts, int rt, hipStream_t stream) {
     }
 }
 
-template <bool PART>
+template <int MODE>
 void launch_expand(const ExpandArgs &g, int rt, hipStream_t stream) {
     const int64_t blocks = ((int64_t)g.C + 511) / 512;
     const dim3 grid((unsigned)(blocks * g.groups)), block(256);
     switch (rt) {
-    case 1: k_lora_expand<1, PART><<<grid, block, 0, stream>>>(g); break;
-    case 2: k_lora_expand<2, PART><<<grid, block, 0, stream>>>(g); break;
-    case 3: k_lora_expand<3, PART><<<grid, block, 0, stream>>>(g); break;
-    case 4: k_lora_expand<4, PART><<<grid, block, 0, stream>>>(g); break;
-    case 5: k_lora_expand<5, PART><<<grid, block, 0, stream>>>(g); break;
-    case 6: k_lora_expand<6, PART><<<grid, block, 0, stream>>>(g); break;
-    case 7: k_lora_expand<7, PART><<<grid, block, 0, stream>>>(g); break;
-    default: k_lora_expand<8, PART><<<grid, block, 0, stream>>>(g); break;
+    case 1: k_lora_expand<1, MODE><<<grid, block, 0, stream>>>(g); break;
+    case 2: k_lora_expand<2, MODE><<<grid, block, 0, stream>>>(g); break;
+    case 3: k_lora_expand<3, MODE><<<grid, block, 0, stream>>>(g); break;
+    case 4: k_lora_expand<4, MODE><<<grid, block, 0, stream>>>(g); break;
+    case 5: k_lora_expand<5, MODE><<<grid, block, 0, stream>>>(g); break;
+    case 6: k_lora_expand<6, MODE><<<grid, block, 0, stream>>>(g); break;
+    case 7: k_lora_expand<7, MODE><<<grid, block, 0, stream>>>(g); break;
+    default: k_lora_expand<8, MODE><<<grid, block, 0, stream>>>(g); break;
     }
 }
 
@@ -803,14 +977,14 @@ int lora_parts(int64_t T, int64_t S, int64_t C, int64_t R) {
 void launch_outer(const OuterArgs &g, int rt, int64_t wgs, int64_t chunks, hipStream_t stream) {
     const dim3 grid((unsigned)wgs, (unsigned)chunks), block(256);
     switch (rt) {
-    case 1: k_lora_outer<1, 8><<<grid, block, 0, stream>>>(g); break;
-    case 2: k_lora_outer<2, 8><<<grid, block, 0, stream>>>(g); break;
-    case 3: k_lora_outer<3, 8><<<grid, block, 0, stream>>>(g); break;
-    case 4: k_lora_outer<4, 4><<<grid, block, 0, stream>>>(g); break;
-    case 5: k_lora_outer<5, 4><<<grid, block, 0, stream>>>(g); break;
-    case 6: k_lora_outer<6, 4><<<grid, block, 0, stream>>>(g); break;
-    case 7: k_lora_outer<7, 4><<<grid, block, 0, stream>>>(g); break;
-    default: k_lora_outer<8, 4><<<grid, block, 0, stream>>>(g); break;
+    case 1: k_lora_outer<1, 8, false><<<grid, block, 0, stream>>>(g); break;
+    case 2: k_lora_outer<2, 8, false><<<grid, block, 0, stream>>>(g); break;
+    case 3: k_lora_outer<3, 8, false><<<grid, block, 0, stream>>>(g); break;
+    case 4: k_lora_outer<4, 4, false><<<grid, block, 0, stream>>>(g); break;
+    case 5: k_lora_outer<5, 4, false><<<grid, block, 0, stream>>>(g); break;
+    case 6: k_lora_outer<6, 4, false><<<grid, block, 0, stream>>>(g); break;
+    case 7: k_lora_outer<7, 4, false><<<grid, block, 0, stream>>>(g); break;
+    default: k_lora_outer<8, 4, false><<<grid, block, 0, stream>>>(g); break;
     }
 }
 
@@ -832,12 +1006,33 @@ extern "C" int64_t pulse_lora_plan_size(int64_t T, int64_t S) { return lora_plan
 
 extern "C" int64_t pulse_lora_hidden_size(int64_t T, int64_t S, int64_t R) { return lora_hidden_size(T, S, R, true); }
 
-// Workspace: h of a forward pass, whole or in parts, or in a backward pass dh and the partial sums of both gradients.
+// Workspace: h of a forward pass, whole or in parts, or in a backward pass dh, the
+// partial sums of dA and dB, and of dh where it comes from the fused pass.
+struct LoraWs {
+    int64_t da, db, sums, bytes;
+};
+
+LoraWs lora_ws(int64_t T, int64_t K, int64_t N, int64_t R, int64_t S, bool train) {
+    LoraWs w{};
+    int64_t n = round256(lora_hidden_size(T, S, R, train));
+    if (n < lora_parts_size(T, S, R)) n = round256(lora_parts_size(T, S, R));
+    if (train) {
+        const bool fused = lora_fused(T, N, R);
+        const int64_t k = lora_outer_blocks(K, R), both = lora_most_chunks(T, S, k + lora_outer_blocks(N, R));
+        const int64_t da = fused ? lora_most_chunks(T, S, k) : both, db = fused ? lora_most_fused_chunks(T, S, N) : 0;
+        w.da = n;
+        n += round256(da * 2 * R * K * 4);  // (fewer column blocks, more chunks: da >= both)
+        w.db = n;
+        n += round256((both > db ? both : db) * 2 * R * N * 4);
+        w.sums = n;
+        if (fused) n += lora_fused_groups(N) * lora_max_tiles(T, S) * LT * ((R + 15) / 16 * 16) * 4;
+    }
+    w.bytes = n;
+    return w;
+}
+
 extern "C" int64_t pulse_lora_ws_size(int64_t T, int64_t K, int64_t N, int64_t R, int64_t S, int32_t train) {
-    int64_t n = round256(lora_hidden_size(T, S, R, train != 0));
-    if (n < lora_parts_size(T, S, R)) n = lora_parts_size(T, S, R);
-    if (train) n += lora_most_chunks(T, S, K, N, R) * 2 * R * (K + N) * 4;
-    return n;
+    return lora_ws(T, K, N, R, S, train != 0).bytes;
 }
 
 extern "C" int pulse_launch_lora_plan(const int32_t *ids, int64_t T, int32_t S, void *plan, uint32_t *d_status,
@@ -874,9 +1069,10 @@ void shrink(const uint16_t *x, int64_t ldx, const uint16_t *a, const float *scal
     g.C = (int32_t)C;
     g.R = (int32_t)R;
     // 32 places a workgroup, so that the adapter is read half as often, once that still fills the chip
-    // and few adapters end in the first half of a tile
+    // and few adapters end in the first half of a tile: 8192 x 5120 at rank 64 37 us with 16 places, 27
+    // with 32; at rank 16 or less the adapter weighs little (16384 x 4096 at rank 16: 35 us, 39)
     if (parts > 1) launch_shrink<1, true>(g, parts, rt, stream);
-    else if (T >= 8192 && T / S >= 128) launch_shrink<2, false>(g, 1, rt, stream);
+    else if (rt >= 2 && T >= 8192 && T / S >= 128) launch_shrink<2, false>(g, 1, rt, stream);
     else launch_shrink<1, false>(g, 1, rt, stream);
 }
 
@@ -901,8 +1097,12 @@ void expand(const uint16_t *h, const float *partial, int parts, const uint16_t *
     g.per = (int32_t)(per < 1 ? 1 : (per > EX_TILES ? EX_TILES : per));
     g.groups = (g.max_tiles + g.per - 1) / g.per;
     const int rt = (int)((R + 15) / 16);
-    if (parts > 1) launch_expand<true>(g, rt, stream);
-    else launch_expand<false>(g, rt, stream);
+    // From 128 MB on y would not be in the last-level cache any more when the next kernel reads it, and
+    // its lines would wait there to be written back: 8192 x 27648 at rank 64 173 us, past the cache 162;
+    // forward and backward of 16384 x 14336 at rank 16 446 us, 434.
+    if (parts > 1) launch_expand<EX_PARTS>(g, rt, stream);
+    else if (T * C >= (int64_t)1 << 26) launch_expand<EX_ONCE>(g, rt, stream);
+    else launch_expand<EX_PLAIN>(g, rt, stream);
 }
 
 }  // namespace
@@ -925,28 +1125,47 @@ extern "C" int pulse_launch_lora_backward(const uint16_t *x, int64_t ldx, const 
                                           uint16_t *dx, int64_t lddx, float *da, float *db, int32_t accumulate,
                                           void *ws, hipStream_t stream) {
     const LoraPlan p = lora_plan_parts(const_cast<void *>(plan), T, S);
-    char *w = static_cast<char *>(ws);
+    const LoraWs at = lora_ws(T, K, N, R, S, true);
+    char *const w = static_cast<char *>(ws);
     const LoraHidden dh = lora_hidden_parts(w, T, S, R, true), hp = lora_hidden_parts(const_cast<void *>(h), T, S, R, true);
-    shrink(dy, lddy, b, scales, p, dh, nullptr, 1, T, N, R, S, stream);
-    if (dx) expand(dh.rows, nullptr, 1, a, dx, lddx, p, T, K, R, S, stream);
-    const int rt = (int)((R + 15) / 16), width = lora_outer_width(R);
+    const int rt = (int)((R + 15) / 16);
+    const auto outer_side = [&](const LoraHidden &u, const uint16_t *z, int64_t ldz, float *out, int64_t partial, int64_t C,
+                                int q) {
+        return OuterSide{{u.part[0], u.part[1], u.part[2]}, z, ldz, out, reinterpret_cast<float *>(w + partial), (int32_t)C,
+                         (int32_t)lora_outer_blocks(C, R), q, (int32_t)lora_chunks(T, S, q)};
+    };
+    const bool fused = lora_fused(T, N, R);
+    const int64_t kb = lora_outer_blocks(K, R), nb = lora_outer_blocks(N, R);
+    const int q = lora_chunk(T, S, fused ? kb : kb + nb);
     OuterArgs g{};
     g.plan = p;
-    g.places = lora_max_tiles(T, S) * LT;
+    g.max_tiles = (int32_t)lora_max_tiles(T, S);
+    g.places = (int64_t)g.max_tiles * LT;
     g.T = (int32_t)T;
     g.R = (int32_t)R;
     g.S = (int32_t)S;
-    g.max_tiles = (int32_t)lora_max_tiles(T, S);
-    g.q = lora_chunk(T, S, K, N, R);
     g.accumulate = accumulate;
-    const int64_t chunks = lora_chunks(T, S, g.q);
-    g.chunks = (int32_t)chunks;
-    float *part = reinterpret_cast<float *>(w + round256(lora_hidden_size(T, S, R, true)));
-    g.side[0] = OuterSide{{dh.part[0], dh.part[1], dh.part[2]}, x, ldx, da, part, (int32_t)K, (int32_t)((K + width - 1) / width)};
-    g.side[1] = OuterSide{{hp.part[0], hp.part[1], hp.part[2]}, dy, lddy, db, part + chunks * 2 * R * K, (int32_t)N,
-                          (int32_t)((N + width - 1) / width)};
-    g.wg0 = (g.side[0].waves + 3) / 4;
-    launch_outer(g, rt, g.wg0 + (g.side[1].waves + 3) / 4, chunks, stream);
+    g.side[0] = outer_side(dh, x, ldx, da, at.da, K, q);
+    g.side[1] = outer_side(hp, dy, lddy, db, at.db, N, fused ? lora_fused_chunk(T, S, N) : q);
+    if (fused) {
+        g.w = b;
+        g.sums = reinterpret_cast<float *>(w + at.sums);
+        const int32_t groups = (int32_t)lora_fused_groups(N);
+        const dim3 grid((unsigned)groups, (unsigned)g.side[1].chunks), tiles((unsigned)g.max_tiles * 2);
+        if (rt == 1) {
+            k_lora_outer<1, 8, true><<<grid, dim3(512), 0, stream>>>(g);
+            k_lora_join<1><<<tiles, dim3(128), 0, stream>>>(g.sums, groups, scales, p, dh, g.max_tiles, g.S, g.R);
+        } else {
+            k_lora_outer<2, 8, true><<<grid, dim3(512), 0, stream>>>(g);
+            k_lora_join<2><<<tiles, dim3(256), 0, stream>>>(g.sums, groups, scales, p, dh, g.max_tiles, g.S, g.R);
+        }
+    } else {
+        shrink(dy, lddy, b, scales, p, dh, nullptr, 1, T, N, R, S, stream);
+    }
+    if (dx) expand(dh.rows, nullptr, 1, a, dx, lddx, p, T, K, R, S, stream);
+    g.wg0 = (g.side[0].blocks + 3) / 4;
+    const int wgs = g.wg0 + (fused ? 0 : (g.side[1].blocks + 3) / 4);
+    launch_outer(g, rt, wgs, g.side[0].chunks, stream);
     const int64_t most = R * (K > N ? K : N);
     k_lora_outer_sum<<<dim3((unsigned)((most / 4 + 255) / 256), (unsigned)S, 2), dim3(256), 0, stream>>>(g);
     return hipGetLastError() == hipSuccess ? 0 : -5;
