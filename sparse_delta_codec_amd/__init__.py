@@ -135,6 +135,8 @@ def _dev(t, name, dtype=None):
         return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
@@ -818,6 +820,7 @@ class LoraPlan:
         nbytes = _size(_lib.pulse_lora_plan_bytes(max_tokens, n_adapters), "pulse_lora_plan_bytes")
         self.max_tokens, self.n_adapters, self.n_tokens = max_tokens, n_adapters, 0
         self.buffer = torch.empty((max(nbytes, 16) + 15) // 16 * 16, dtype=torch.uint8, device=device)
+        self.pointer, self.nbytes = self.buffer.data_ptr(), self.buffer.numel()
 
 
 def lora_workspace(n_tokens, k, n, rank, n_adapters, train=False, device="cuda"):
@@ -832,66 +835,87 @@ def lora_hidden(n_tokens, rank, n_adapters, device="cuda"):
     return torch.empty((max(nbytes, 16) + 15) // 16 * 16, dtype=torch.uint8, device=device)
 
 
+# The adapter calls are made once per projection and batch, where a few microseconds
+# of checks on the host are felt: each argument's checks stand in one expression, and
+# only when it fails are they gone through one by one for the message.
 def _rows(t, rows, cols, name):
     """A BF16 matrix [rows, cols] with contiguous columns and any row stride that is
     a multiple of 8.  Returns (data pointer, row stride)."""
+    try:
+        stride = t.stride()
+        if t.shape == (rows, cols) and t.is_cuda and t.dtype in _U16 and (stride[1] == 1 or cols <= 1 or rows == 0):
+            return t.data_ptr(), stride[0] if rows > 1 else max(stride[0], cols)
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype not in _U16:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {_U16}")
     if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({rows}, {cols})")
-    if cols > 1 and rows > 0 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    raise ValueError(f"{name} must have contiguous rows")
 
 
 def _pools(a, b, scales, plan):
-    """Checks the adapter pools; returns (rank, k, n)."""
+    """Checks the adapter pools; returns (rank, k, n) and their data pointers."""
+    try:
+        (s, r, k), (s1, r1, n) = a.shape, b.shape
+        if (s == s1 == plan.n_adapters and r == r1 and a.is_cuda and b.is_cuda and scales.is_cuda and a.dtype in _U16
+                and b.dtype in _U16 and scales.dtype is torch.float32 and a.is_contiguous() and b.is_contiguous()
+                and scales.is_contiguous() and scales.numel() >= s):
+            return r, k, n, a.data_ptr(), b.data_ptr(), scales.data_ptr()
+    except (AttributeError, ValueError):
+        pass
     if a.dim() != 3 or b.dim() != 3 or a.shape[:2] != b.shape[:2] or a.shape[0] != plan.n_adapters:
         raise ValueError(f"a {tuple(a.shape)} and b {tuple(b.shape)} must be [{plan.n_adapters}, rank, ...]")
     _need(scales, 4 * plan.n_adapters, "scales")
-    return a.shape[1], a.shape[2], b.shape[2]
+    for t, name, dtype in ((a, "a", _U16), (b, "b", _U16), (scales, "scales", torch.float32)):
+        if t is None:
+            raise ValueError(f"{name} must be a GPU tensor")
+        _dev(t, name, dtype)
+    raise ValueError("a, b and scales do not belong together")
 
 
 def pulse_lora_plan(plan, ids, d_status, stream=None):
     """Groups the tokens of a batch by adapter: ids int32, -1 for no adapter."""
-    if ids.numel() > plan.max_tokens:
-        raise ValueError(f"ids holds {ids.numel()} tokens, the plan at most {plan.max_tokens}")
+    n = ids.numel()
+    if n > plan.max_tokens:
+        raise ValueError(f"ids holds {n} tokens, the plan at most {plan.max_tokens}")
     _need(d_status, 4, "d_status")
-    _check(_lib.pulse_lora_plan(_dev(ids, "ids", torch.int32), ids.numel(), plan.n_adapters, plan.buffer.data_ptr(),
-                                plan.buffer.numel(), _dev(d_status, "d_status", torch.int32), _stream(stream)),
-           "pulse_lora_plan")
-    plan.n_tokens = ids.numel()
+    _check(_lib.pulse_lora_plan(_dev(ids, "ids", torch.int32), n, plan.n_adapters, plan.pointer, plan.nbytes,
+                                _dev(d_status, "d_status", torch.int32), _stream(stream)), "pulse_lora_plan")
+    plan.n_tokens = n
 
 
 def pulse_lora_forward(x, a, b, scales, plan, y, ws, h=None, stream=None):
     """y [tokens, n] += scale B^T A x for the tokens of the plan's batch: x [tokens, k],
     a [adapters, rank, k], b [adapters, rank, n] BF16, scales float32; h keeps what the
     backward pass needs."""
-    r, k, n = _pools(a, b, scales, plan)
-    px, ldx = _rows(x, plan.n_tokens, k, "x")
-    py, ldy = _rows(y, plan.n_tokens, n, "y")
+    r, k, n, pa, pb, ps = _pools(a, b, scales, plan)
+    tokens = plan.n_tokens
+    px, ldx = _rows(x, tokens, k, "x")
+    py, ldy = _rows(y, tokens, n, "y")
     wsp, wsb = _ws(ws)
-    _check(_lib.pulse_lora_forward(
-        px, ldx, _dev(a, "a", _U16), _dev(b, "b", _U16), _dev(scales, "scales", torch.float32), plan.buffer.data_ptr(),
-        plan.buffer.numel(), plan.n_tokens, k, n, r, plan.n_adapters, py, ldy, _dev(h, "h", torch.uint8),
-        0 if h is None else h.numel(), wsp, wsb, _stream(stream)), "pulse_lora_forward")
+    ph, hb = (None, 0) if h is None else (_dev(h, "h", torch.uint8), h.numel())
+    _check(_lib.pulse_lora_forward(px, ldx, pa, pb, ps, plan.pointer, plan.nbytes, tokens, k, n, r, plan.n_adapters, py,
+                                   ldy, ph, hb, wsp, wsb, _stream(stream)), "pulse_lora_forward")
 
 
 def pulse_lora_backward(x, dy, a, b, scales, plan, h, dx, da, db, ws, accumulate=False, stream=None):
     """The gradients of pulse_lora_forward: dx [tokens, k] BF16 is added to (None: not
     wanted), da and db (float32, the pools' shapes) are written or, with accumulate,
     added to."""
-    r, k, n = _pools(a, b, scales, plan)
-    px, ldx = _rows(x, plan.n_tokens, k, "x")
-    pdy, lddy = _rows(dy, plan.n_tokens, n, "dy")
-    pdx, lddx = (None, 0) if dx is None else _rows(dx, plan.n_tokens, k, "dx")
+    r, k, n, pa, pb, ps = _pools(a, b, scales, plan)
+    tokens = plan.n_tokens
+    px, ldx = _rows(x, tokens, k, "x")
+    pdy, lddy = _rows(dy, tokens, n, "dy")
+    pdx, lddx = (None, 0) if dx is None else _rows(dx, tokens, k, "dx")
+    if h is None or da is None or db is None:
+        raise ValueError("h, da and db must be GPU tensors")
     _need(da, 4 * a.numel(), "da")
     _need(db, 4 * b.numel(), "db")
     wsp, wsb = _ws(ws)
     _check(_lib.pulse_lora_backward(
-        px, ldx, pdy, lddy, _dev(a, "a", _U16), _dev(b, "b", _U16), _dev(scales, "scales", torch.float32),
-        plan.buffer.data_ptr(), plan.buffer.numel(), plan.n_tokens, k, n, r, plan.n_adapters,
+        px, ldx, pdy, lddy, pa, pb, ps, plan.pointer, plan.nbytes, tokens, k, n, r, plan.n_adapters,
         _dev(h, "h", torch.uint8), h.numel(), pdx, lddx, _dev(da, "da", torch.float32),
         _dev(db, "db", torch.float32), int(accumulate), wsp, wsb, _stream(stream)), "pulse_lora_backward")

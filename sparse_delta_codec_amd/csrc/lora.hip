@@ -302,31 +302,52 @@ struct ShrinkArgs {
     const float *scales;
     LoraPlan plan;
     LoraHidden h;
-    float *partial;  // [gridDim.y][places][Rp] (PART)
+    float *partial;  // [gridDim.y][places][Rp] (SH_PARTS)
     int64_t places;
     int32_t T, S, C, R, max_tiles, max_groups;
+    const uint16_t *w;  // [S][R][N] (SH_APPLY)
+    uint16_t *y;
+    int64_t ldy;
+    int32_t N;
 };
 
-// A wave's piece of LDS: rows of 128 columns, sixteen 16-byte pieces each, which
-// it writes as they were loaded (four rows an instruction, 256 contiguous bytes
-// each) and reads as a matrix instruction wants them (16 rows, 64 bytes each).
-// Piece p of row r lies at p ^ r, so that neither side has two lanes in a bank.
-__device__ __forceinline__ int staged(int row, int piece) { return row * 16 + (piece ^ (row & 15)); }
+// SH_WHOLE: h in its forms; SH_PARTS: the workgroups' sums over their shares of the
+// long axis; SH_APPLY: y += W^T h too, and h in its forms where they are asked for.
+enum ShrinkMode { SH_WHOLE, SH_PARTS, SH_APPLY };
 
-// Waves of a workgroup: as many as their LDS leaves room for.
-constexpr int shrink_waves(int rt, int mt) { return rt + mt <= 2 ? 16 : (rt + mt <= 4 ? 8 : 4); }
+// A wave's piece of LDS: rows of P 16-byte pieces (128 columns, or 64), which it
+// writes as they were loaded (four rows an instruction, 256 contiguous bytes each)
+// and reads as a matrix instruction wants them (16 rows, 64 bytes each).  Piece p
+// of row r lies at p ^ r, so that neither side has two lanes in a bank.
+template <int P = 16>
+__device__ __forceinline__ int staged(int row, int piece) {
+    return row * P + (piece ^ (row & (P - 1)));
+}
 
-// A workgroup takes 16 MT places of a tile; its waves, and with PART gridDim.y
-// workgroups, share the long axis in steps of 128 columns, and the waves' sums
+// Columns of a wave's step and waves of a workgroup: two waves a SIMD or more in
+// the 160 KB of LDS, so that one loads while another turns its rows round.
+constexpr int shrink_cols(int rt, int mt) { return rt + mt <= 4 ? 128 : 64; }
+constexpr int shrink_waves(int rt, int mt) { return rt + mt <= 2 ? 16 : 8; }
+
+// A workgroup takes 16 MT places of a tile; its waves, and with SH_PARTS gridDim.y
+// workgroups, share the long axis in steps of 128 or 64 columns, and the waves' sums
 // are added through LDS, in their order.  Matrix instruction: rows = ranks,
 // columns = places, 32 elements of the long axis.  Read as the instruction wants
 // them, 64 bytes of 16 rows at once, rows came in at 10 to 15 bytes a clock and
 // compute unit; 256 bytes of 4 rows, turned round in LDS, are not held back.
 // The rows of the next step are read while these are multiplied.
-template <int RT, int MT, bool PART>
+// SH_APPLY serves small batches, which wait for launches and round trips more
+// than for bytes: gridDim.y workgroups each make the same h, keep it in LDS and go
+// through their share of y's columns as k_lora_expand does; a wave's first rows and
+// adapter columns are read before h is made.
+template <int RT, int MT, int MODE>
 __global__ __launch_bounds__(shrink_waves(RT, MT) * kWave) void k_lora_shrink(ShrinkArgs g) {
-    constexpr int NW = shrink_waves(RT, MT);
-    __shared__ u32x4 s_stage[NW][(MT + RT) * 256];
+    constexpr int NW = shrink_waves(RT, MT), COLS = shrink_cols(RT, MT), P = COLS / 8;
+    constexpr int LOADS = P / 4, ROWS = 64 / P;  // loads of 16 rows, rows of a load
+    constexpr bool APPLY = MODE == SH_APPLY, AHEAD = RT <= 4;
+    static_assert(!APPLY || MT == 1, "16 places in SH_APPLY");
+    __shared__ u32x2 s_h[APPLY ? 64 * RT : 1];  // [16 places][Rp] BF16
+    __shared__ u32x4 s_stage[NW][(MT + RT) * 16 * P];
     __shared__ int s_tok[16 * MT];
     // 16 places: from the plan's list, which leaves out the empty ones (a workgroup that finds nothing
     // to do still takes the LDS of a whole one)
@@ -338,45 +359,72 @@ __global__ __launch_bounds__(shrink_waves(RT, MT) * kWave) void k_lora_shrink(Sh
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), c16 = l & 15, q = l >> 4;
     const int64_t place0 = (int64_t)at * 16;
     const float scale = g.scales[slot];
-    const uint16_t *const pa = g.a + ((int64_t)slot * g.R + q) * g.C;
-    const uint16_t *px[MT][4];
-    int tok[MT][4];
+    const int lp = l % P, lr = l / P;  // a lane's piece and row in a load
+    const uint16_t *const pa = g.a + ((int64_t)slot * g.R + lr) * g.C;
+    const uint16_t *px[MT][LOADS];
+    int tok[MT][LOADS];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tok[m][i] = token_of(g.plan.order[place0 + m * 16 + i * 4 + q], g.T);
+        for (int i = 0; i < LOADS; ++i) tok[m][i] = token_of(g.plan.order[place0 + m * 16 + i * ROWS + lr], g.T);
     const int some = __builtin_amdgcn_readfirstlane(tok[0][0]) < 0 ? 0 : __builtin_amdgcn_readfirstlane(tok[0][0]);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (w == 0 && c16 == 0) s_tok[m * 16 + i * 4 + q] = tok[m][i];
+        for (int i = 0; i < LOADS; ++i) {
+            if (w == 0 && lp == 0) s_tok[m * 16 + i * ROWS + lr] = tok[m][i];
             px[m][i] = g.x + (int64_t)(tok[m][i] < 0 ? some : tok[m][i]) * g.ldx;  // an empty place's sums are dropped
         }
-    const int steps = (g.C + 127) / 128, stride = NW * (int)gridDim.y;
-    u32x4 xr[MT][4], ar[RT][4];
+    // SH_APPLY: where the rows of places 4 q + i lie (an empty place stands for the first), and a block
+    // of 128 columns of them and of the adapter
+    const int in = APPLY ? g.plan.tile_count[tile] - sub * 16 : 0, jstride = NW * (int)gridDim.y;
+    int jb = (int)blockIdx.y * NW + w;
+    int64_t row[4];
+    u32x4 yv[4], wv[AHEAD ? RT : 1][4];
+    const auto adapter_row = [&](int r) { return g.w + ((int64_t)slot * g.R + (r < g.R ? r : 0)) * g.N; };
+    const auto piece = [&](int b) {
+        const int base = b * 128, col = base + c16 * 8 < g.N ? base + c16 * 8 : base;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) yv[i] = ld16(g.y + row[i] + col);
+#pragma unroll
+        for (int rt = 0; rt < (AHEAD ? RT : 0); ++rt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wv[rt][i] = ld16(adapter_row(rt * 16 + q * 4 + i) + col);
+        return col;
+    };
+    int col = 0;
+    if constexpr (APPLY) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = token_of(g.plan.order[place0 + (q * 4 + i < in ? q * 4 + i : 0)], g.T);
+            row[i] = (int64_t)(t < 0 ? 0 : t) * g.ldy;
+        }
+        if (jb * 128 < g.N) col = piece(jb);
+    }
+    const int steps = (g.C + COLS - 1) / COLS, stride = NW * (MODE == SH_PARTS ? (int)gridDim.y : 1);
+    u32x4 xr[MT][LOADS], ar[RT][LOADS];
     auto load = [&](int s) {
-        const int k = s * 128 + c16 * 8, kc = k < g.C ? k : 0;
+        const int k = s * COLS + lp * 8, kc = k < g.C ? k : 0;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < LOADS; ++i) {  // (R is a multiple of 8: a load is all ranks or none)
                 ar[rt][i] = u32x4{0, 0, 0, 0};
-                if (rt * 16 + i * 4 < g.R) ar[rt][i] = ld16(pa + (int64_t)(rt * 16 + i * 4) * g.C + kc);
+                if (rt * 16 + i * ROWS < g.R) ar[rt][i] = ld16(pa + (int64_t)(rt * 16 + i * ROWS) * g.C + kc);
             }
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) xr[m][i] = ld16_once(px[m][i] + kc);
-        if (s * 128 + 128 > g.C && k >= g.C) {
+            for (int i = 0; i < LOADS; ++i) xr[m][i] = ld16_once(px[m][i] + kc);
+        if (s * COLS + COLS > g.C && k >= g.C) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ar[rt][i] = u32x4{0, 0, 0, 0};
+                for (int i = 0; i < LOADS; ++i) ar[rt][i] = u32x4{0, 0, 0, 0};
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) xr[m][i] = u32x4{0, 0, 0, 0};
+                for (int i = 0; i < LOADS; ++i) xr[m][i] = u32x4{0, 0, 0, 0};
         }
     };
     f32x4 acc[MT][RT];
@@ -385,29 +433,29 @@ __global__ __launch_bounds__(shrink_waves(RT, MT) * kWave) void k_lora_shrink(Sh
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) acc[m][rt] = f32x4{0, 0, 0, 0};
     u32x4 *const st = s_stage[w];
-    int s = (int)blockIdx.y * NW + w;
+    int s = (MODE == SH_PARTS ? (int)blockIdx.y * NW : 0) + w;
     if (s < steps) load(s);
     for (; s < steps; s += stride) {
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // the last step's reads are done
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) st[m * 256 + staged(i * 4 + q, c16)] = xr[m][i];
+            for (int i = 0; i < LOADS; ++i) st[m * 16 * P + staged<P>(i * ROWS + lr, lp)] = xr[m][i];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) st[(MT + rt) * 256 + staged(i * 4 + q, c16)] = ar[rt][i];
+            for (int i = 0; i < LOADS; ++i) st[(MT + rt) * 16 * P + staged<P>(i * ROWS + lr, lp)] = ar[rt][i];
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // the lanes' pieces are visible to the wave
         if (s + stride < steps) load(s + stride);
         sched_fence();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < COLS / 32; ++k) {
             u32x4 xv[MT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) xv[m] = st[m * 256 + staged(c16, k * 4 + q)];
+            for (int m = 0; m < MT; ++m) xv[m] = st[m * 16 * P + staged<P>(c16, k * 4 + q)];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const u32x4 av = st[(MT + rt) * 256 + staged(c16, k * 4 + q)];
+                const u32x4 av = st[(MT + rt) * 16 * P + staged<P>(c16, k * 4 + q)];
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
                     acc[m][rt] =
@@ -428,9 +476,58 @@ __global__ __launch_bounds__(shrink_waves(RT, MT) * kWave) void k_lora_shrink(Sh
         const int64_t place = place0 + m * 16 + c16;
         const bool live = s_tok[m * 16 + c16] >= 0 && r < g.R;  // R is a multiple of 8: all four ranks or none
         v = live ? v * scale : f32x4{0, 0, 0, 0};
-        if constexpr (PART)
+        if constexpr (MODE == SH_PARTS) {
             *reinterpret_cast<f32x4 *>(g.partial + ((int64_t)blockIdx.y * g.places + place) * (RT * 16) + r) = v;
-        else store_hidden(g.h, place, g.places, RT * 16, r, v);
+        } else {
+            if (!APPLY || (g.h.rows && blockIdx.y == 0)) store_hidden(g.h, place, g.places, RT * 16, r, v);
+            if constexpr (APPLY) s_h[c16 * (RT * 4) + r / 4] = u32x2{cast_pair(v[0], v[1]), cast_pair(v[2], v[3])};
+        }
+    }
+    if constexpr (APPLY) {
+        lds_barrier();
+        s16x4 hv[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+            hv[rt] = __builtin_bit_cast(s16x4, s_h[(c16 < in ? c16 : 0) * (RT * 4) + rt * 4 + q]);
+        while (jb * 128 < g.N) {
+            f32x4 out[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) out[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                u32x4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (AHEAD) v[i] = wv[rt][i];
+                    else v[i] = ld16(adapter_row(rt * 16 + q * 4 + i) + col);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (rt * 16 + q * 4 + i >= g.R) v[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const u32x2 lo = {__builtin_amdgcn_perm(v[1][d], v[0][d], 0x05040100u),
+                                      __builtin_amdgcn_perm(v[3][d], v[2][d], 0x05040100u)};
+                    const u32x2 hi = {__builtin_amdgcn_perm(v[1][d], v[0][d], 0x07060302u),
+                                      __builtin_amdgcn_perm(v[3][d], v[2][d], 0x07060302u)};
+                    out[2 * d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(hv[rt], __builtin_bit_cast(s16x4, lo),
+                                                                           out[2 * d], 0, 0, 0);
+                    out[2 * d + 1] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(hv[rt], __builtin_bit_cast(s16x4, hi),
+                                                                               out[2 * d + 1], 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u32x4 o;
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    o[d] = cast_pair(__uint_as_float(yv[i][d] << 16) + out[2 * d][i],
+                                     __uint_as_float(yv[i][d] & 0xFFFF0000u) + out[2 * d + 1][i]);
+                *reinterpret_cast<u32x4 *>(g.y + row[i] + col) = o;
+            }
+            jb += jstride;
+            if (jb * 128 < g.N) col = piece(jb);
+        }
     }
 }
 
@@ -503,16 +600,22 @@ __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
         const int64_t *const row = s_row + (tile - ta) * LT + sub * 16 + q * 4;
         const int in = count - sub * 16;  // places of the 16 that hold a token
         const int64_t at = ((int64_t)tile * LT + sub * 16 + (c16 < in ? c16 : 0)) * (RT * 16) + q * 4;
+        if constexpr (MODE == EX_PARTS) {
+            f32x4 v[RT];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            if constexpr (MODE == EX_PARTS) {
-                f32x4 v = *reinterpret_cast<const f32x4 *>(g.partial + at + rt * 16);
-                for (int p = 1; p < g.parts; ++p)
-                    v += *reinterpret_cast<const f32x4 *>(g.partial + p * g.places * (RT * 16) + at + rt * 16);
-                r.h[rt] = __builtin_bit_cast(s16x4, u32x2{cast_pair(v[0], v[1]), cast_pair(v[2], v[3])});
-            } else {
+            for (int rt = 0; rt < RT; ++rt) v[rt] = *reinterpret_cast<const f32x4 *>(g.partial + at + rt * 16);
+#pragma unroll 2
+            for (int p = 1; p < g.parts; ++p)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+                    v[rt] += *reinterpret_cast<const f32x4 *>(g.partial + p * g.places * (RT * 16) + at + rt * 16);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+                r.h[rt] = __builtin_bit_cast(s16x4, u32x2{cast_pair(v[rt][0], v[rt][1]), cast_pair(v[rt][2], v[rt][3])});
+        } else {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
                 r.h[rt] = __builtin_bit_cast(s16x4, *reinterpret_cast<const u32x2 *>(g.h + at + rt * 16));
-            }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) r.at[i] = row[i];
@@ -557,7 +660,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
                 }
             }
         }
-        read(next, more ? tile1 : tile, more ? sub1 : sub, more ? count1 : count);
+        if (MODE != EX_PARTS || more) read(next, more ? tile1 : tile, more ? sub1 : sub, more ? count1 : count);
         sched_fence();
         f32x4 acc[8];
 #pragma unroll
@@ -605,49 +708,40 @@ struct OuterArgs {
     int64_t places;
     int32_t T, R, S, max_tiles;
     int32_t accumulate, wg0;  // wg0: workgroups of side 0 per chunk
+    int32_t clear;            // set where k_lora_outer_sum does not follow: zero the adapters without tokens
+    int32_t groups;           // of a workgroup's four waves, those that share its columns: one for two rank tiles
     const uint16_t *w;        // FUSE: [S][R][C] what shrink multiplies z with
     float *sums;              // FUSE: [workgroups of a chunk][32 places][512 RT] their sums, as the lanes hold them
 };
 
 constexpr int OU_TILES = 32;  // most tiles of a chunk
 
-template <int W>
-struct ZVec;
-template <>
-struct ZVec<8> {
-    typedef u32x4 T;
-};
-template <>
-struct ZVec<4> {
-    typedef u32x2 T;
-};
-
-// What 32 places need in outer: a lane's W columns of eight rows, and u where the
-// registers hold it twice (AHEAD).
-template <int RT, int W, bool AHEAD>
+// What 32 places need in outer: a lane's eight columns of eight rows, and u where
+// the registers hold it twice (AHEAD).
+template <int RT, bool AHEAD>
 struct OuterRows {
-    typename ZVec<W>::T z[8];
+    u32x4 z[8];
     u32x4 u[3][AHEAD ? RT : 1];
 };
 
-// A wave takes 16 W columns and one chunk of tiles, 32 places at a time; the next
-// 32 places' rows are on their way meanwhile, into the other of two buffers.
-// Matrix instruction: rows = ranks, columns = columns of z, 32 places.  Lane c of
-// the column axis holds W neighbouring columns of eight places, transposed in
-// registers; instruction j takes its column j, once for each part of u.  A chunk
-// may cover several adapters and an adapter several chunks: a run that lies in
-// one chunk goes straight to the output, the others to the chunk's partial sums
-// (0: continues an earlier chunk's run, 1: begins here), which k_lora_outer_sum
-// adds in order.
+// A wave takes 128 columns, RT tiles of 16 ranks and one chunk of tiles, 32 places
+// at a time; the next 32 places' rows are on their way meanwhile, into the other of
+// two buffers.  The waves of a workgroup that differ in their ranks only read the
+// same rows, three of four times from the nearest cache.  Matrix instruction: rows
+// = ranks, columns = columns of z, 32 places.  Lane c of the column axis holds eight
+// neighbouring columns of eight places, transposed in registers; instruction j takes
+// its column j, once for each part of u.  A chunk may cover several adapters and an
+// adapter several chunks: a run that lies in one chunk goes straight to the output,
+// the others to the chunk's partial sums (0: continues an earlier chunk's run, 1:
+// begins here), which k_lora_outer_sum adds in order.
 // FUSE: z is dy, and the same read serves dh = s B dy: the rows go through LDS
 // into the order that shrink multiplies them in, the eight waves' sums over 128
 // columns each are added there, and k_lora_join adds the workgroups'.
-template <int RT, int W, bool FUSE>
-__global__ __launch_bounds__(FUSE ? 512 : 256) void k_lora_outer(OuterArgs g) {
-    typedef typename ZVec<W>::T ZV;
-    constexpr int NW = FUSE ? 8 : 4;
-    constexpr bool AHEAD = FUSE ? RT == 1 : RT <= 3;
-    typedef OuterRows<RT, W, AHEAD> Rows;
+template <int RT, bool FUSE>
+__global__ __launch_bounds__(FUSE ? 512 : 256, FUSE ? 1 : 2) void k_lora_outer(OuterArgs g) {
+    constexpr int NW = FUSE ? 8 : 4, W = 8;
+    constexpr bool AHEAD = RT == 1;
+    typedef OuterRows<RT, AHEAD> Rows;
     __shared__ int64_t s_row[OU_TILES * LT];
     __shared__ int32_t s_slot[OU_TILES], s_count[OU_TILES];
     __shared__ u32x4 s_stage[FUSE ? NW : 1][FUSE ? 512 : 1];
@@ -658,7 +752,7 @@ __global__ __launch_bounds__(FUSE ? 512 : 256) void k_lora_outer(OuterArgs g) {
     const int chunk = blockIdx.y, ta = chunk * s.q;
     const int ntiles = *g.plan.ntiles < g.max_tiles ? *g.plan.ntiles : g.max_tiles;
     const int tb = ta + s.q < ntiles ? ta + s.q : ntiles;
-    if (chunk >= s.chunks || ta >= tb) return;
+    if (chunk >= s.chunks || (ta >= tb && !g.clear)) return;
     for (int i = threadIdx.x; i < (tb - ta) * LT; i += NW * kWave) {
         s_row[i] = row_of(g.plan.order + (int64_t)ta * LT, i, g.T, s.ldz);
         if (i < tb - ta) {
@@ -667,8 +761,12 @@ __global__ __launch_bounds__(FUSE ? 512 : 256) void k_lora_outer(OuterArgs g) {
         }
     }
     __syncthreads();
-    const int cb = ((int)blockIdx.x - (sd ? g.wg0 : 0)) * NW + w, base = cb * 16 * W, col = base + c16 * W;
-    if (!FUSE && cb >= s.blocks) return;  // (FUSE: the wave still meets the others at their barriers)
+    const int groups = FUSE ? 1 : g.groups, r0 = w % groups * RT * 16;  // the wave's first rank
+    const int cb = ((int)blockIdx.x - (sd ? g.wg0 : 0)) * (NW / groups) + w / groups, base = cb * 128, col = base + c16 * 8;
+    if (!FUSE && (cb >= s.blocks || r0 >= g.R)) return;  // (FUSE: the wave still meets the others at their barriers)
+    int64_t urow[RT];  // the lane's rank of each tile in u; past u's last tile: that one's
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) urow[rt] = (int64_t)((r0 + rt * 16 < g.R ? r0 + rt * 16 : r0) + c16) * g.places;
     const bool colok = col < s.C;
     const uint16_t *const zcol = s.z + (colok ? col : (base < s.C ? base : 0));
     const auto slot_of = [&](int tile) {
@@ -679,6 +777,22 @@ __global__ __launch_bounds__(FUSE ? 512 : 256) void k_lora_outer(OuterArgs g) {
         const int n = __builtin_amdgcn_readfirstlane(s_count[tile - ta]);
         return n < 1 ? 1 : (n < LT ? n : LT);
     };
+    if (g.clear && chunk == 0) {  // one chunk only: the adapters without a token have no other launch
+        for (int a = 0; a < g.S; ++a) {
+            if (g.plan.slot_tile[a] != g.plan.slot_tile[a + 1]) continue;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + rt * 16 + q * 4 + i;
+                    float *p = s.out + ((int64_t)a * g.R + r) * s.C + col;
+                    if (r < g.R && colok) {
+                        *reinterpret_cast<f32x4 *>(p) = f32x4{0, 0, 0, 0};
+                        *reinterpret_cast<f32x4 *>(p + 4) = f32x4{0, 0, 0, 0};
+                    }
+                }
+        }
+    }
     f32x4 acc[RT][W];
     const auto flush = [&](int slot) __attribute__((always_inline)) {
         const int t0 = g.plan.slot_tile[slot], t1 = g.plan.slot_tile[slot + 1];
@@ -689,7 +803,7 @@ __global__ __launch_bounds__(FUSE ? 512 : 256) void k_lora_outer(OuterArgs g) {
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = rt * 16 + q * 4 + i;
+                const int r = r0 + rt * 16 + q * 4 + i;
                 if (r < g.R && colok) {
                     float *p = o + (int64_t)r * s.C + col;
 #pragma unroll
@@ -708,15 +822,16 @@ __global__ __launch_bounds__(FUSE ? 512 : 256) void k_lora_outer(OuterArgs g) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) at[i] = row[i];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r.z[i] = __builtin_nontemporal_load(reinterpret_cast<const ZV *>(zcol + at[i]));
+        for (int i = 0; i < 8; ++i) r.z[i] = ld16_once(zcol + at[i]);
         if constexpr (AHEAD) {
 #pragma unroll
             for (int p = 0; p < 3; ++p)
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
-                    r.u[p][rt] = ld16(s.part[p] + (int64_t)(rt * 16 + c16) * g.places + place);
+                    r.u[p][rt] = ld16(s.part[p] + urow[rt] + place);
         }
     };
+    if (ta >= tb) return;
     int tile = ta, half = 0, cur = -1, slot = slot_of(ta), buf = 0;
     if (slot < 0) return;
     int count = count_of(ta);
@@ -755,7 +870,7 @@ __global__ __launch_bounds__(FUSE ? 512 : 256) void k_lora_outer(OuterArgs g) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 if constexpr (AHEAD) u[p][rt] = now.u[p][rt];
-                else u[p][rt] = ld16(s.part[p] + (int64_t)(rt * 16 + c16) * g.places + (int64_t)tile * LT + half * 32 + q * 8);
+                else u[p][rt] = ld16(s.part[p] + urow[rt] + (int64_t)tile * LT + half * 32 + q * 8);
             }
         read(next, more ? tile1 : tile, more ? half1 : half);
         sched_fence();
@@ -763,7 +878,7 @@ __global__ __launch_bounds__(FUSE ? 512 : 256) void k_lora_outer(OuterArgs g) {
         if (left < 32) {  // empty places: no row, and past the last 16 that hold a token no u
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (q * 8 + i >= left) now.z[i] = ZV{};
+                if (q * 8 + i >= left) now.z[i] = u32x4{0, 0, 0, 0};
             const bool none = q * 8 >= (left + 15) / 16 * 16;
 #pragma unroll
             for (int p = 0; p < 3; ++p)
@@ -774,7 +889,7 @@ __global__ __launch_bounds__(FUSE ? 512 : 256) void k_lora_outer(OuterArgs g) {
         if constexpr (FUSE) {
             if (base + 128 > s.C && !colok) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) now.z[i] = ZV{};
+                for (int i = 0; i < 8; ++i) now.z[i] = u32x4{0, 0, 0, 0};
             }
             u32x4 *const st = s_stage[w];
             __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
@@ -883,15 +998,17 @@ __global__ __launch_bounds__(256) void k_lora_outer_sum(OuterArgs g) {
 }
 
 // ---- launches ---------------------------------------------------------------------
-// Columns of a wave in outer: 128, or 64 where 128 columns' sums leave no registers to read ahead.
-int lora_outer_width(int64_t R) { return R > 48 ? 64 : 128; }
+int64_t lora_outer_blocks(int64_t C) { return (C + 127) / 128; }
 
-int64_t lora_outer_blocks(int64_t C, int64_t R) { return (C + lora_outer_width(R) - 1) / lora_outer_width(R); }
+// Waves that share a column block: one for each two rank tiles (three: a fourth stays idle).
+int lora_outer_groups(int64_t R) { return R <= 32 ? 1 : (R <= 64 ? 2 : 4); }
 
-// Tiles of a chunk in outer: about 2048 waves over the column blocks of a launch, 128 tokens or more.
-int lora_chunk(int64_t T, int64_t S, int64_t blocks) {
-    const int64_t q = lora_max_tiles(T, S) * blocks / 2048;
-    return (int)(q < 2 ? 2 : (q > OU_TILES ? OU_TILES : q));
+// Tiles of a chunk in outer: about 2048 waves over a launch's waves for one chunk,
+// and enough tokens that the partial sums, 4 R bytes a column, weigh no more than
+// the rows, 2 bytes a token and column; up to 6 tiles one chunk, which needs no sum.
+int lora_chunk(int64_t T, int64_t S, int64_t R, int64_t waves) {
+    const int64_t mt = lora_max_tiles(T, S), q = mt * waves / 2048, least = mt <= 6 ? 6 : (R > 64 ? R / 32 : 2);
+    return (int)(q < least ? least : (q > OU_TILES ? OU_TILES : q));
 }
 
 // The backward pass reads dy once, for dh and dB together, where that saves more
@@ -920,8 +1037,8 @@ int64_t lora_chunks(int64_t T, int64_t S, int q) { return (lora_max_tiles(T, S) 
 // (and there are fewer than 3 times those that make 2048 waves), or more than 3/4
 // of the tiles that make 2048 waves, or OU_TILES tiles.  Fused: two rounds, or
 // OU_TILES tiles.
-int64_t lora_most_chunks(int64_t T, int64_t S, int64_t blocks) {
-    const int64_t mt = lora_max_tiles(T, S), a = mt / 2 + 1, b = 3072 / blocks + 2, c = mt / OU_TILES + 1;
+int64_t lora_most_chunks(int64_t T, int64_t S, int64_t waves) {
+    const int64_t mt = lora_max_tiles(T, S), a = mt / 2 + 1, b = 3072 / waves + 2, c = mt / OU_TILES + 1;
     const int64_t m = a < b ? a : b;
     return m > c ? m : c;
 }
@@ -931,20 +1048,20 @@ int64_t lora_most_fused_chunks(int64_t T, int64_t S, int64_t N) {
     return a > b ? a : b;
 }
 
-template <int MT, bool PART>
+template <int MT, int MODE>
 void launch_shrink(const ShrinkArgs &g, int parts, int rt, hipStream_t stream) {
     const dim3 grid((unsigned)(MT == 1 ? g.max_groups : g.max_tiles * (4 / MT)), (unsigned)parts);
     const auto block = [](int r) { return dim3(shrink_waves(r, MT) * kWave); };
     switch (rt) {
-    case 1: k_lora_shrink<1, MT, PART><<<grid, block(1), 0, stream>>>(g); break;
-    case 2: k_lora_shrink<2, MT, PART><<<grid, block(2), 0, stream>>>(g); break;
-    case 3: k_lora_shrink<3, MT, PART><<<grid, block(3), 0, stream>>>(g); break;
-    case 4: k_lora_shrink<4, MT, PART><<<grid, block(4), 0, stream>>>(g); break;
-    case 5: k_lora_shrink<5, MT, PART><<<grid, block(5), 0, stream>>>(g); break;
-    case 6: k_lora_shrink<6, MT, PART><<<grid, block(6), 0, stream>>>(g); break;
-    case 7: k_lora_shrink<7, MT, PART><<<grid, block(7), 0, stream>>>(g); break;
+    case 1: k_lora_shrink<1, MT, MODE><<<grid, block(1), 0, stream>>>(g); break;
+    case 2: k_lora_shrink<2, MT, MODE><<<grid, block(2), 0, stream>>>(g); break;
+    case 3: k_lora_shrink<3, MT, MODE><<<grid, block(3), 0, stream>>>(g); break;
+    case 4: k_lora_shrink<4, MT, MODE><<<grid, block(4), 0, stream>>>(g); break;
+    case 5: k_lora_shrink<5, MT, MODE><<<grid, block(5), 0, stream>>>(g); break;
+    case 6: k_lora_shrink<6, MT, MODE><<<grid, block(6), 0, stream>>>(g); break;
+    case 7: k_lora_shrink<7, MT, MODE><<<grid, block(7), 0, stream>>>(g); break;
     default:  // eight rank tiles leave room for 16 places only
-        k_lora_shrink<8, 1, PART><<<dim3((unsigned)g.max_groups, (unsigned)parts), dim3(shrink_waves(8, 1) * kWave), 0,
+        k_lora_shrink<8, 1, MODE><<<dim3((unsigned)g.max_groups, (unsigned)parts), dim3(shrink_waves(8, 1) * kWave), 0,
                                     stream>>>(g);
     }
 }
@@ -969,23 +1086,16 @@ void launch_expand(const ExpandArgs &g, int rt, hipStream_t stream) {
 // as bring the groups of 16 places that hold a token to about 256, one step a wave
 // or more.  Each writes its own part of h, which expand adds up.
 int lora_parts(int64_t T, int64_t S, int64_t C, int64_t R) {
-    const int64_t groups = (T + 15) / 16 + (S < T ? S : T), waves = shrink_waves((int)((R + 15) / 16), 1);
-    const int64_t most = (C + 127) / 128 / waves, parts = 256 / groups < most ? 256 / groups : most;
+    const int64_t groups = (T + 15) / 16 + (S < T ? S : T);
+    const int64_t waves = shrink_waves((int)((R + 15) / 16), 1), cols = shrink_cols((int)((R + 15) / 16), 1);
+    const int64_t most = (C + cols - 1) / cols / waves, parts = 256 / groups < most ? 256 / groups : most;
     return (int)(parts < 1 ? 1 : (parts > 8 ? 8 : parts));
 }
 
-void launch_outer(const OuterArgs &g, int rt, int64_t wgs, int64_t chunks, hipStream_t stream) {
+void launch_outer(const OuterArgs &g, int64_t wgs, int64_t chunks, hipStream_t stream) {
     const dim3 grid((unsigned)wgs, (unsigned)chunks), block(256);
-    switch (rt) {
-    case 1: k_lora_outer<1, 8, false><<<grid, block, 0, stream>>>(g); break;
-    case 2: k_lora_outer<2, 8, false><<<grid, block, 0, stream>>>(g); break;
-    case 3: k_lora_outer<3, 8, false><<<grid, block, 0, stream>>>(g); break;
-    case 4: k_lora_outer<4, 4, false><<<grid, block, 0, stream>>>(g); break;
-    case 5: k_lora_outer<5, 4, false><<<grid, block, 0, stream>>>(g); break;
-    case 6: k_lora_outer<6, 4, false><<<grid, block, 0, stream>>>(g); break;
-    case 7: k_lora_outer<7, 4, false><<<grid, block, 0, stream>>>(g); break;
-    default: k_lora_outer<8, 4, false><<<grid, block, 0, stream>>>(g); break;
-    }
+    if (g.R <= 16) k_lora_outer<1, false><<<grid, block, 0, stream>>>(g);
+    else k_lora_outer<2, false><<<grid, block, 0, stream>>>(g);
 }
 
 // Bytes of h's parts, for this T and every smaller one.  Parts are made where the
@@ -1018,7 +1128,8 @@ LoraWs lora_ws(int64_t T, int64_t K, int64_t N, int64_t R, int64_t S, bool train
     if (n < lora_parts_size(T, S, R)) n = round256(lora_parts_size(T, S, R));
     if (train) {
         const bool fused = lora_fused(T, N, R);
-        const int64_t k = lora_outer_blocks(K, R), both = lora_most_chunks(T, S, k + lora_outer_blocks(N, R));
+        const int64_t each = lora_outer_groups(R), k = lora_outer_blocks(K) * each;
+        const int64_t both = lora_most_chunks(T, S, k + lora_outer_blocks(N) * each);
         const int64_t da = fused ? lora_most_chunks(T, S, k) : both, db = fused ? lora_most_fused_chunks(T, S, N) : 0;
         w.da = n;
         n += round256(da * 2 * R * K * 4);  // (fewer column blocks, more chunks: da >= both)
@@ -1048,11 +1159,8 @@ extern "C" int pulse_launch_lora_plan(const int32_t *ids, int64_t T, int32_t S, 
 
 namespace {
 
-// h goes to its forms, or with parts > 1 to `partial`
-void shrink(const uint16_t *x, int64_t ldx, const uint16_t *a, const float *scales, const LoraPlan &plan,
-            const LoraHidden &h, float *partial, int parts, int64_t T, int64_t C, int64_t R, int64_t S,
-            hipStream_t stream) {
-    const int rt = (int)((R + 15) / 16);
+ShrinkArgs shrink_args(const uint16_t *x, int64_t ldx, const uint16_t *a, const float *scales, const LoraPlan &plan,
+                       const LoraHidden &h, int64_t T, int64_t C, int64_t R, int64_t S) {
     ShrinkArgs g{};
     g.max_tiles = (int32_t)lora_max_tiles(T, S);
     g.max_groups = (int32_t)lora_max_groups(T, S);
@@ -1062,18 +1170,54 @@ void shrink(const uint16_t *x, int64_t ldx, const uint16_t *a, const float *scal
     g.scales = scales;
     g.plan = plan;
     g.h = h;
-    g.partial = partial;
     g.places = (int64_t)g.max_tiles * LT;
     g.T = (int32_t)T;
     g.S = (int32_t)S;
     g.C = (int32_t)C;
     g.R = (int32_t)R;
+    return g;
+}
+
+// h goes to its forms, or with parts > 1 to `partial`
+void shrink(const uint16_t *x, int64_t ldx, const uint16_t *a, const float *scales, const LoraPlan &plan,
+            const LoraHidden &h, float *partial, int parts, int64_t T, int64_t C, int64_t R, int64_t S,
+            hipStream_t stream) {
+    const int rt = (int)((R + 15) / 16);
+    ShrinkArgs g = shrink_args(x, ldx, a, scales, plan, h, T, C, R, S);
+    g.partial = partial;
     // 32 places a workgroup, so that the adapter is read half as often, once that still fills the chip
     // and few adapters end in the first half of a tile: 8192 x 5120 at rank 64 37 us with 16 places, 27
     // with 32; at rank 16 or less the adapter weighs little (16384 x 4096 at rank 16: 35 us, 39)
-    if (parts > 1) launch_shrink<1, true>(g, parts, rt, stream);
-    else if (rt >= 2 && T >= 8192 && T / S >= 128) launch_shrink<2, false>(g, 1, rt, stream);
-    else launch_shrink<1, false>(g, 1, rt, stream);
+    if (parts > 1) launch_shrink<1, SH_PARTS>(g, parts, rt, stream);
+    else if (rt >= 2 && T >= 8192 && T / S >= 128) launch_shrink<2, SH_WHOLE>(g, 1, rt, stream);
+    else launch_shrink<1, SH_WHOLE>(g, 1, rt, stream);
+}
+
+// Workgroups of 16 places in SH_APPLY, or 0 where h and y take a launch each: for
+// more than 256 groups or 4 blocks of 128 columns a wave (the second launch then
+// spreads over more of the chip), where the adapter, which every workgroup reads,
+// comes to more than 48 MB in all (96 tokens of 64 adapters, 5120 to 7168, rank 32:
+// 69 MB, 16.4 us against 14.6; 64 tokens, 4096 to 4096, rank 16: 18 MB, 9.1 us
+// against 9.8 and one launch less), and where h's long axis can be shared and one
+// workgroup would read long (4 tokens, 4096 to 4096, rank 128: 1 MB, 22 us against 14).
+int64_t lora_apply_groups(int64_t T, int64_t S, int64_t C, int64_t N, int64_t R, bool shared) {
+    const int64_t groups = lora_max_groups(T, S), waves = shrink_waves((int)((R + 15) / 16), 1);
+    if (groups > 256 || (shared && R * C * 2 > 384 << 10)) return 0;
+    const int64_t blocks = (N + 127) / 128, most = (blocks + waves - 1) / waves;
+    const int64_t n = 256 / groups < most ? 256 / groups : most;
+    return blocks <= n * waves * 4 && groups * n * R * C * 2 <= 48 << 20 ? n : 0;
+}
+
+// h and y += W^T h in one launch
+void apply(const uint16_t *x, int64_t ldx, const uint16_t *a, const float *scales, const LoraPlan &plan,
+           const LoraHidden &h, const uint16_t *w, uint16_t *y, int64_t ldy, int64_t groups, int64_t T, int64_t C,
+           int64_t N, int64_t R, int64_t S, hipStream_t stream) {
+    ShrinkArgs g = shrink_args(x, ldx, a, scales, plan, h, T, C, R, S);
+    g.w = w;
+    g.y = y;
+    g.ldy = ldy;
+    g.N = (int32_t)N;
+    launch_shrink<1, SH_APPLY>(g, (int)groups, (int)((R + 15) / 16), stream);
 }
 
 void expand(const uint16_t *h, const float *partial, int parts, const uint16_t *w, uint16_t *y, int64_t ldy,
@@ -1113,6 +1257,11 @@ extern "C" int pulse_launch_lora_forward(const uint16_t *x, int64_t ldx, const u
     const LoraPlan p = lora_plan_parts(const_cast<void *>(plan), T, S);
     const LoraHidden hp = lora_hidden_parts(h ? h : ws, T, S, R, h != nullptr);
     const int parts = h ? 1 : lora_parts(T, S, K, R);
+    if (const int64_t groups = lora_apply_groups(T, S, K, N, R, parts > 1)) {
+        const LoraHidden keep = h ? hp : LoraHidden{};
+        apply(x, ldx, a, scales, p, keep, b, y, ldy, groups, T, K, N, R, S, stream);
+        return hipGetLastError() == hipSuccess ? 0 : -5;
+    }
     float *partial = static_cast<float *>(ws);
     shrink(x, ldx, a, scales, p, hp, partial, parts, T, K, R, S, stream);
     expand(hp.rows, partial, parts, b, y, ldy, p, T, N, R, S, stream);
@@ -1132,11 +1281,12 @@ extern "C" int pulse_launch_lora_backward(const uint16_t *x, int64_t ldx, const 
     const auto outer_side = [&](const LoraHidden &u, const uint16_t *z, int64_t ldz, float *out, int64_t partial, int64_t C,
                                 int q) {
         return OuterSide{{u.part[0], u.part[1], u.part[2]}, z, ldz, out, reinterpret_cast<float *>(w + partial), (int32_t)C,
-                         (int32_t)lora_outer_blocks(C, R), q, (int32_t)lora_chunks(T, S, q)};
+                         (int32_t)lora_outer_blocks(C), q, (int32_t)lora_chunks(T, S, q)};
     };
     const bool fused = lora_fused(T, N, R);
-    const int64_t kb = lora_outer_blocks(K, R), nb = lora_outer_blocks(N, R);
-    const int q = lora_chunk(T, S, fused ? kb : kb + nb);
+    const int64_t kb = lora_outer_blocks(K), nb = lora_outer_blocks(N);
+    const int groups = lora_outer_groups(R), per = 4 / groups;  // column blocks of a workgroup
+    const int q = lora_chunk(T, S, R, (fused ? kb : kb + nb) * groups);
     OuterArgs g{};
     g.plan = p;
     g.max_tiles = (int32_t)lora_max_tiles(T, S);
@@ -1150,22 +1300,30 @@ extern "C" int pulse_launch_lora_backward(const uint16_t *x, int64_t ldx, const 
     if (fused) {
         g.w = b;
         g.sums = reinterpret_cast<float *>(w + at.sums);
-        const int32_t groups = (int32_t)lora_fused_groups(N);
-        const dim3 grid((unsigned)groups, (unsigned)g.side[1].chunks), tiles((unsigned)g.max_tiles * 2);
+        const int32_t parts = (int32_t)lora_fused_groups(N);
+        const dim3 grid((unsigned)parts, (unsigned)g.side[1].chunks), tiles((unsigned)g.max_tiles * 2);
         if (rt == 1) {
-            k_lora_outer<1, 8, true><<<grid, dim3(512), 0, stream>>>(g);
-            k_lora_join<1><<<tiles, dim3(128), 0, stream>>>(g.sums, groups, scales, p, dh, g.max_tiles, g.S, g.R);
+            k_lora_outer<1, true><<<grid, dim3(512), 0, stream>>>(g);
+            k_lora_join<1><<<tiles, dim3(128), 0, stream>>>(g.sums, parts, scales, p, dh, g.max_tiles, g.S, g.R);
         } else {
-            k_lora_outer<2, 8, true><<<grid, dim3(512), 0, stream>>>(g);
-            k_lora_join<2><<<tiles, dim3(256), 0, stream>>>(g.sums, groups, scales, p, dh, g.max_tiles, g.S, g.R);
+            k_lora_outer<2, true><<<grid, dim3(512), 0, stream>>>(g);
+            k_lora_join<2><<<tiles, dim3(256), 0, stream>>>(g.sums, parts, scales, p, dh, g.max_tiles, g.S, g.R);
         }
+    } else if (const int64_t n = dx ? lora_apply_groups(T, S, N, K, R, false) : 0) {
+        apply(dy, lddy, b, scales, p, dh, a, dx, lddx, n, T, N, K, R, S, stream);
+        dx = nullptr;
     } else {
         shrink(dy, lddy, b, scales, p, dh, nullptr, 1, T, N, R, S, stream);
     }
     if (dx) expand(dh.rows, nullptr, 1, a, dx, lddx, p, T, K, R, S, stream);
-    g.wg0 = (g.side[0].blocks + 3) / 4;
-    const int wgs = g.wg0 + (fused ? 0 : (g.side[1].blocks + 3) / 4);
-    launch_outer(g, rt, wgs, g.side[0].chunks, stream);
+    g.groups = groups;
+    g.wg0 = (g.side[0].blocks + per - 1) / per;
+    const int wgs = g.wg0 + (fused ? 0 : (g.side[1].blocks + per - 1) / per);
+    // one chunk of a few adapters: every sum is whole, and the launch that would add parts is left out
+    const bool whole = !fused && g.side[0].chunks == 1 && S <= 64;
+    g.clear = whole && !accumulate;
+    launch_outer(g, wgs, g.side[0].chunks, stream);
+    if (whole) return hipGetLastError() == hipSuccess ? 0 : -5;
     const int64_t most = R * (K > N ? K : N);
     k_lora_outer_sum<<<dim3((unsigned)((most / 4 + 255) / 256), (unsigned)S, 2), dim3(256), 0, stream>>>(g);
     return hipGetLastError() == hipSuccess ? 0 : -5;
