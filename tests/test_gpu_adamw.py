@@ -308,3 +308,36 @@ def test_clip_and_step_in_a_replayed_graph():
         n = int(host(outs[0]["offs"])[2])
         assert n == int(host(outs[1]["offs"])[2]) > 0
         assert torch.equal(outs[0]["s"], outs[1]["s"]) and torch.equal(outs[0]["idx"][:n], outs[1]["idx"][:n])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_patch_of_a_long_list_on_a_used_workspace(bits):
+    """More pieces than the patch kernel has workgroups, tensors of every length
+    between, and a workspace that holds anything: the patch lists exactly the elements
+    whose view changed, in order, tensor by tensor."""
+    sizes = [1, 2, 3, 1023, 1025, 16384, 16383, 5] * 20 + [2080 * 16384 + 13, 7]
+    g = torch.Generator(device="cuda").manual_seed(4)
+    total = sum(sizes)
+    p = [torch.empty(n, device="cuda").normal_(0.0, 0.02, generator=g) for n in sizes]
+    grads = [torch.empty(n, device="cuda").normal_(0.0, 1e-3, generator=g) for n in sizes]
+    b = [x.bfloat16() for x in p]
+    before = [x.clone() for x in b]
+    dtype = torch.uint8 if bits == 8 else torch.float32
+    m, v = ([torch.zeros(n, dtype=dtype, device="cuda") for n in sizes] for _ in "mv")
+    scales = {}
+    if bits == 8:
+        scales = {k: [torch.zeros((n + 255) // 256, device="cuda") for n in sizes] for k in ("m_scale", "v_scale")}
+    table, st = pulse.AdamWTable(p, grads, m, v, b=b, **scales), zeros(1, torch.int32)
+    ws = pulse.workspace(pulse.PULSE_OP_ADAMW, table.ntiles)
+    ws.fill_(255)
+    idx, val = zeros(total, torch.int32), zeros(total, torch.bfloat16)
+    offs = torch.full((len(sizes) + 1,), -1, dtype=torch.int64, device="cuda")
+    pulse.pulse_adamw_step(table, 1, 1e-5, seed=1, d_status=st, ws=ws, patch_idx=idx, patch_val=val, seg_offsets=offs)
+    torch.cuda.synchronize()
+    assert int(host(st)[0]) == 0
+    want = [(x.view(torch.int16) != y.view(torch.int16)).nonzero()[:, 0] for x, y in zip(before, b)]
+    counts = torch.tensor([0] + [w.numel() for w in want]).cumsum(0)
+    assert torch.equal(offs.cpu(), counts) and 0 < int(counts[-1]) < total
+    n = int(counts[-1])
+    assert torch.equal(idx[:n].long(), torch.cat(want))
+    assert torch.equal(val[:n].view(torch.int16), torch.cat([x[w].view(torch.int16) for x, w in zip(b, want)]))

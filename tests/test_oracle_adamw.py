@@ -166,3 +166,12 @@ def test_binding_refuses_host_tensors_and_uneven_lists():
         pulse.AdamWTable([t], [t], [t], [t], m_scale=[t])
     with pytest.raises(ValueError):
         pulse.AdamWTable([t], [t], [t], [t])
+
+
+def test_adamw_refuses_an_unaligned_workspace(lib):  # noqa: F811
+    from tests.test_abi import EALIGN
+
+    f = lib.pulse_adamw_step
+    f.argtypes = [V, I32, V, I64, V, V, V, V, I64, V, V, V, ctypes.c_size_t, V]
+    al, p = V(0x10000), ctypes.byref(Params(**good()))
+    assert f(al, 1, al, 1, p, None, al, al, 10, al, al, V(0x10008), 1 << 20, None) == EALIGN
