@@ -182,7 +182,6 @@ __global__ __launch_bounds__(NW *kWave) void k_lora_plan(const int32_t *__restri
         *p.ntiles = total;
     }
     __syncthreads();
-    volatile int32_t *mine = sh + w * S;
     for (int tb = t0; tb < t1; tb += LP_AHEAD * kWave) {
         if (t0 + LP_AHEAD * kWave < t1) read_ids(ids, tb + l, t1, id);
 #pragma unroll
@@ -191,13 +190,14 @@ __global__ __launch_bounds__(NW *kWave) void k_lora_plan(const int32_t *__restri
             const int a = id[k] >= 0 && id[k] < S ? id[k] : -1;
             const uint64_t same = equal_lanes(a, bits);
             if (a >= 0) {
-                const int place = mine[a] + (int)lanes_below(same);
+                const int place = sh[w * S + a] + (int)lanes_below(same);
                 p.order[place] = tb + k * kWave + l;
-                // the last of the equal lanes moves the adapter's next place on (all have read it:
-                // a wave's LDS accesses are in order)
-                if ((same >> l) == 1ull) mine[a] = place + 1;
+                // the last of the equal lanes moves the adapter's next place on (all have read it: a
+                // wave's LDS accesses are in order; a volatile pointer would make them flat ones, which
+                // wait for the stores of the tokens)
+                if ((same >> l) == 1ull) sh[w * S + a] = place + 1;
             }
-            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+            asm volatile("" ::: "memory");  // the next 64 tokens read what these wrote
         }
     }
     // the places past an adapter's last token are empty
