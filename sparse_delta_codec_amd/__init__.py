@@ -690,6 +690,14 @@ def _aligned(t, name):
         raise ValueError(f"{name} must be 16-byte aligned")
 
 
+def _to_device(tab, tile_seg, device):
+    """A table's rows and its tiles' numbers on the device, in one copy."""
+    import numpy as np
+
+    raw = torch.from_numpy(np.concatenate([tab.view(np.uint8).ravel(), tile_seg.view(np.uint8)])).to(device)
+    return raw[:tab.nbytes].view(torch.int64).view(tab.shape), raw[tab.nbytes:].view(torch.int32)
+
+
 class GradTable:
     """Device tables of pulse_grad_norm for a list of gradients (GPU tensors, all
     float32 or all bfloat16), prepared once and reused every step."""
@@ -706,8 +714,7 @@ class GradTable:
         self.ntiles, tile0, tile_seg = pulse_segment_tiles([t.numel() for t in g])
         tab = np.array([[t.data_ptr(), t.numel(), t0] for t, t0 in zip(g, tile0)], np.int64)
         self.nseg = len(g)
-        self.segs = torch.from_numpy(tab).to(device)
-        self.tile_seg = torch.from_numpy(tile_seg.view(np.int32)).to(device)
+        self.segs, self.tile_seg = _to_device(tab, tile_seg, device)
         self._keep = list(g)
 
 
@@ -776,8 +783,7 @@ class AdamWTable:
         tab[:, 9] = np.stack([np.array(lr_mult, np.float32), np.array(weight_decay, np.float32)],
                              1).view(np.int64)[:, 0]
         self.nseg = nseg
-        self.segs = torch.from_numpy(tab).to(device)
-        self.tile_seg = torch.from_numpy(tile_seg.view(np.int32)).to(device)
+        self.segs, self.tile_seg = _to_device(tab, tile_seg, device)
         self._keep = [None if x is None else list(x) for x in (p, g, m, v, b, m_scale, v_scale)]
 
 

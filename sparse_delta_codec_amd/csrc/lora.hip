@@ -1003,11 +1003,13 @@ int64_t lora_outer_blocks(int64_t C) { return (C + 127) / 128; }
 // Waves that share a column block: one for each two rank tiles (three: a fourth stays idle).
 int lora_outer_groups(int64_t R) { return R <= 32 ? 1 : (R <= 64 ? 2 : 4); }
 
-// Tiles of a chunk in outer: about 2048 waves over a launch's waves for one chunk,
+// Tiles of a chunk in outer: up to 1024 waves in all, one workgroup a compute unit
+// (16384 x 4096 at rank 16: 29 us with 232 workgroups, 40 with 296, 41 with 512),
 // and enough tokens that the partial sums, 4 R bytes a column, weigh no more than
 // the rows, 2 bytes a token and column; up to 6 tiles one chunk, which needs no sum.
 int lora_chunk(int64_t T, int64_t S, int64_t R, int64_t waves) {
-    const int64_t mt = lora_max_tiles(T, S), q = mt * waves / 2048, least = mt <= 6 ? 6 : (R > 64 ? R / 32 : 2);
+    const int64_t mt = lora_max_tiles(T, S), q = (mt * waves + 1023) / 1024;
+    const int64_t least = mt <= 6 ? 6 : (R > 64 ? R / 32 : 2);
     return (int)(q < least ? least : (q > OU_TILES ? OU_TILES : q));
 }
 
@@ -1033,12 +1035,10 @@ int lora_fused_chunk(int64_t T, int64_t S, int64_t N) {
 
 int64_t lora_chunks(int64_t T, int64_t S, int q) { return (lora_max_tiles(T, S) + q - 1) / q; }
 
-// Most chunks of this T and every smaller one.  Outer alone: a chunk has 2 tiles
-// (and there are fewer than 3 times those that make 2048 waves), or more than 3/4
-// of the tiles that make 2048 waves, or OU_TILES tiles.  Fused: two rounds, or
-// OU_TILES tiles.
+// Most chunks of this T and every smaller one.  Outer alone: 2 tiles each, and what
+// makes 1024 waves, or OU_TILES tiles each.  Fused: two rounds, or OU_TILES tiles.
 int64_t lora_most_chunks(int64_t T, int64_t S, int64_t waves) {
-    const int64_t mt = lora_max_tiles(T, S), a = mt / 2 + 1, b = 3072 / waves + 2, c = mt / OU_TILES + 1;
+    const int64_t mt = lora_max_tiles(T, S), a = mt / 2 + 1, b = 1024 / waves + 2, c = mt / OU_TILES + 1;
     const int64_t m = a < b ? a : b;
     return m > c ? m : c;
 }
