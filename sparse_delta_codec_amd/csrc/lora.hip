@@ -10,12 +10,14 @@
 //   shrink  [tokens, C] by [R, C]   -> [tokens, R]   contracted over the long axis
 //   expand  [tokens, R] by [R, C]   -> added to [tokens, C]
 //   outer   [tokens, R] by [tokens, C] -> [R, C]     contracted over tokens
-// All of them are bound by reading or writing the [tokens, C] matrices (an
+// Large batches are bound by reading or writing the [tokens, C] matrices (an
 // element takes 2 R multiplications for 2 to 4 bytes), so the work is to touch
-// those once, with wide loads, and to keep the matrix instructions fed from
-// registers: the two operands that a matrix instruction wants along the other
-// axis (expand's adapter, outer's tokens) are transposed in registers, one
-// v_perm_b32 per pair of values, without a trip through LDS.
+// those once, in rows of 256 contiguous bytes that are on their way while the
+// last ones are multiplied: shrink turns its rows round in LDS, and the two
+// operands that a matrix instruction wants along the other axis (expand's
+// adapter, outer's tokens) are transposed in registers, one v_perm_b32 per pair
+// of values.  Small batches are bound by launches and round trips to memory: they
+// make h and y in one launch, and need no sum over chunks.
 //
 // A plan groups a batch's tokens by adapter: tiles of 64 places, each of one
 // adapter, whose places hold token numbers in ascending order (-1: empty).
@@ -335,7 +337,9 @@ constexpr int shrink_waves(int rt, int mt) { return rt + mt <= 2 ? 16 : 8; }
 // columns = places, 32 elements of the long axis.  Read as the instruction wants
 // them, 64 bytes of 16 rows at once, rows came in at 10 to 15 bytes a clock and
 // compute unit; 256 bytes of 4 rows, turned round in LDS, are not held back.
-// The rows of the next step are read while these are multiplied.
+// The rows of the next step are read while these are multiplied.  Measured:
+// 8192 x 5120 at rank 64 27 us (3.2 TB/s of x), 16384 x 4096 at rank 16 35 us
+// (3.8); of the reads of x alone, in any order, 16384 x 4096 took 25 to 34 us.
 // SH_APPLY serves small batches, which wait for launches and round trips more
 // than for bytes: gridDim.y workgroups each make the same h, keep it in LDS and go
 // through their share of y's columns as k_lora_expand does; a wave's first rows and
@@ -566,7 +570,9 @@ struct ExpandRows {
 // other of two buffers.  Loads and stores count down one counter in their order,
 // so the body has no branch around either: an empty place stands for the first
 // of its 16 and a lane past the last column for the wave's first piece, and both
-// write again what that one writes.
+// write again what that one writes.  Bound by reading and writing y: 8192 x 27648 at
+// rank 64 161 us (5.6 TB/s; with the branches 206), 16384 x 14336 at rank 16 183 us
+// (5.1; a large copy 5.2).
 template <int RT, int MODE>
 __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), c16 = l & 15, q = l >> 4;
@@ -734,9 +740,12 @@ struct OuterRows {
 // adapter several chunks: a run that lies in one chunk goes straight to the output,
 // the others to the chunk's partial sums (0: continues an earlier chunk's run, 1:
 // begins here), which k_lora_outer_sum adds in order.
+// 16384 x 4096 at rank 16: 29 us, 4.6 TB/s.
 // FUSE: z is dy, and the same read serves dh = s B dy: the rows go through LDS
 // into the order that shrink multiplies them in, the eight waves' sums over 128
-// columns each are added there, and k_lora_join adds the workgroups'.
+// columns each are added there, and k_lora_join adds the workgroups'.  16384 x 14336
+// at rank 16: 102 us, 4.6 TB/s, and 6 us for the join (dy read twice: 137 + 105 us);
+// leaving out either product changes nothing, it waits for the rows.
 template <int RT, bool FUSE>
 __global__ __launch_bounds__(FUSE ? 512 : 256, FUSE ? 1 : 2) void k_lora_outer(OuterArgs g) {
     constexpr int NW = FUSE ? 8 : 4, W = 8;
@@ -1048,21 +1057,24 @@ int64_t lora_most_fused_chunks(int64_t T, int64_t S, int64_t N) {
     return a > b ? a : b;
 }
 
+template <int RT, int MT, int MODE>
+void launch_shrink_rt(const ShrinkArgs &g, int parts, hipStream_t stream) {
+    const dim3 grid((unsigned)(MT == 1 ? g.max_groups : g.max_tiles * (4 / MT)), (unsigned)parts);
+    k_lora_shrink<RT, MT, MODE><<<grid, dim3(shrink_waves(RT, MT) * kWave), 0, stream>>>(g);
+}
+
+// (one rank tile always takes 16 places, and eight leave room in LDS for no more)
 template <int MT, int MODE>
 void launch_shrink(const ShrinkArgs &g, int parts, int rt, hipStream_t stream) {
-    const dim3 grid((unsigned)(MT == 1 ? g.max_groups : g.max_tiles * (4 / MT)), (unsigned)parts);
-    const auto block = [](int r) { return dim3(shrink_waves(r, MT) * kWave); };
     switch (rt) {
-    case 1: k_lora_shrink<1, MT, MODE><<<grid, block(1), 0, stream>>>(g); break;
-    case 2: k_lora_shrink<2, MT, MODE><<<grid, block(2), 0, stream>>>(g); break;
-    case 3: k_lora_shrink<3, MT, MODE><<<grid, block(3), 0, stream>>>(g); break;
-    case 4: k_lora_shrink<4, MT, MODE><<<grid, block(4), 0, stream>>>(g); break;
-    case 5: k_lora_shrink<5, MT, MODE><<<grid, block(5), 0, stream>>>(g); break;
-    case 6: k_lora_shrink<6, MT, MODE><<<grid, block(6), 0, stream>>>(g); break;
-    case 7: k_lora_shrink<7, MT, MODE><<<grid, block(7), 0, stream>>>(g); break;
-    default:  // eight rank tiles leave room for 16 places only
-        k_lora_shrink<8, 1, MODE><<<dim3((unsigned)g.max_groups, (unsigned)parts), dim3(shrink_waves(8, 1) * kWave), 0,
-                                    stream>>>(g);
+    case 1: launch_shrink_rt<1, 1, MODE>(g, parts, stream); break;
+    case 2: launch_shrink_rt<2, MT, MODE>(g, parts, stream); break;
+    case 3: launch_shrink_rt<3, MT, MODE>(g, parts, stream); break;
+    case 4: launch_shrink_rt<4, MT, MODE>(g, parts, stream); break;
+    case 5: launch_shrink_rt<5, MT, MODE>(g, parts, stream); break;
+    case 6: launch_shrink_rt<6, MT, MODE>(g, parts, stream); break;
+    case 7: launch_shrink_rt<7, MT, MODE>(g, parts, stream); break;
+    default: launch_shrink_rt<8, 1, MODE>(g, parts, stream);
     }
 }
 
