@@ -150,12 +150,13 @@ def _need(t, nbytes, name):
         raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, needs {nbytes}")
 
 
+_raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream):
     """The handle of a stream; None: the current device's current stream (asked for
     directly, 0.3 us: torch.cuda.current_stream() builds a Stream object in 2.7 us)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
+    return _raw_stream(_get_device()) if stream is None else stream.cuda_stream
 
 
 _U16 = (torch.uint16, torch.int16, torch.bfloat16)
@@ -888,8 +889,11 @@ def pulse_lora_plan(plan, ids, d_status, stream=None):
     if n > plan.max_tokens:
         raise ValueError(f"ids holds {n} tokens, the plan at most {plan.max_tokens}")
     _need(d_status, 4, "d_status")
-    _check(_lib.pulse_lora_plan(_dev(ids, "ids", torch.int32), n, plan.n_adapters, plan.pointer, plan.nbytes,
-                                _dev(d_status, "d_status", torch.int32), _stream(stream)), "pulse_lora_plan")
+    rc = _lib.pulse_lora_plan(_dev(ids, "ids", torch.int32), n, plan.n_adapters, plan.pointer, plan.nbytes,
+                              _dev(d_status, "d_status", torch.int32),
+                              _raw_stream(_get_device()) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "pulse_lora_plan")
     plan.n_tokens = n
 
 
@@ -901,10 +905,12 @@ def pulse_lora_forward(x, a, b, scales, plan, y, ws, h=None, stream=None):
     tokens = plan.n_tokens
     px, ldx = _rows(x, tokens, k, "x")
     py, ldy = _rows(y, tokens, n, "y")
-    wsp, wsb = _ws(ws)
     ph, hb = (None, 0) if h is None else (_dev(h, "h", torch.uint8), h.numel())
-    _check(_lib.pulse_lora_forward(px, ldx, pa, pb, ps, plan.pointer, plan.nbytes, tokens, k, n, r, plan.n_adapters, py,
-                                   ldy, ph, hb, wsp, wsb, _stream(stream)), "pulse_lora_forward")
+    rc = _lib.pulse_lora_forward(px, ldx, pa, pb, ps, plan.pointer, plan.nbytes, tokens, k, n, r, plan.n_adapters, py, ldy,
+                                 ph, hb, _dev(ws, "ws", torch.uint8), 0 if ws is None else ws.numel(),
+                                 _raw_stream(_get_device()) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "pulse_lora_forward")
 
 
 def pulse_lora_backward(x, dy, a, b, scales, plan, h, dx, da, db, ws, accumulate=False, stream=None):
