@@ -8,6 +8,7 @@ fallback: if the library is not built, importing this package fails.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -723,16 +724,16 @@ def pulse_grad_norm(table, out, ws, max_norm=float("inf"), grad_mul=1.0, stream=
     """out (float32[2]) = the clip factor and the norm of the table's gradients."""
     _need(out, 8, "out")
     wsp, wsb = _ws(ws)
-    _check(_lib.pulse_grad_norm(
+    rc = _lib.pulse_grad_norm(
         table.segs.data_ptr(), table.nseg, table.tile_seg.data_ptr(), table.ntiles, table.grad_bf16, grad_mul,
-        max_norm, _dev(out, "out", torch.float32), wsp, wsb, _stream(stream)), "pulse_grad_norm")
+        max_norm, _dev(out, "out", torch.float32), wsp, wsb,
+        _raw_stream(_get_device()) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "pulse_grad_norm")
 
 
-class _AdamWParams(ctypes.Structure):
-    """The layout of pulse_adamw_params."""
-    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
-                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("seed", ctypes.c_uint32),
-                ("grad_bf16", ctypes.c_int32), ("state_bits", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+# pulse_adamw_params: lr, beta1, beta2, eps, step, seed, grad_bf16, state_bits, reserved
+_pack_adamw = struct.Struct("=ddddqIiii").pack
 
 
 class AdamWTable:
@@ -793,19 +794,24 @@ def pulse_adamw_step(table, step, lr, betas=(0.9, 0.999), eps=1e-8, d_scale=None
     """One AdamW step over the table's tensors, with their served views and, when
     patch_idx, patch_val and seg_offsets are given, the patch of the views'
     changed elements (as pulse_cast_diff_segments writes it)."""
-    cap = 0 if patch_idx is None else patch_idx.numel()
-    if patch_idx is not None and not table.has_view:
-        raise ValueError("a patch needs the table's views (b)")
-    _need(patch_val, 2 * cap, "patch_val")
-    _need(seg_offsets, 8 * (table.nseg + 1), "seg_offsets")
+    cap = 0
+    if patch_idx is not None:
+        cap = patch_idx.numel()
+        if not table.has_view:
+            raise ValueError("a patch needs the table's views (b)")
+        _need(patch_val, 2 * cap, "patch_val")
+        _need(seg_offsets, 8 * (table.nseg + 1), "seg_offsets")
     _need(d_scale, 4, "d_scale")
-    params = _AdamWParams(lr, betas[0], betas[1], eps, step, seed & 0xFFFFFFFF, table.grad_bf16, table.state_bits, 0)
+    params = _pack_adamw(lr, betas[0], betas[1], eps, step, seed & 0xFFFFFFFF, table.grad_bf16, table.state_bits, 0)
     wsp, wsb = _ws(ws)
-    _check(_lib.pulse_adamw_step(
-        table.segs.data_ptr(), table.nseg, table.tile_seg.data_ptr(), table.ntiles, ctypes.byref(params),
+    rc = _lib.pulse_adamw_step(
+        table.segs.data_ptr(), table.nseg, table.tile_seg.data_ptr(), table.ntiles, params,
         _dev(d_scale, "d_scale", torch.float32), _dev(patch_idx, "patch_idx", torch.int32),
         _dev(patch_val, "patch_val", _U16), cap, _dev(seg_offsets, "seg_offsets", torch.int64),
-        _dev(d_status, "d_status", torch.int32), wsp, wsb, _stream(stream)), "pulse_adamw_step")
+        _dev(d_status, "d_status", torch.int32), wsp, wsb,
+        _raw_stream(_get_device()) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "pulse_adamw_step")
 
 
 PULSE_LORA_MAX_RANK = 128
