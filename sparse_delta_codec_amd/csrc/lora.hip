@@ -326,10 +326,12 @@ __device__ __forceinline__ int staged(int row, int piece) {
     return row * P + (piece ^ (row & (P - 1)));
 }
 
-// Columns of a wave's step and waves of a workgroup: two waves a SIMD or more in
-// the 160 KB of LDS, so that one loads while another turns its rows round.
+// Columns of a wave's step, and waves of a workgroup: two waves a SIMD or more in
+// the 160 KB of LDS, so that one loads while another turns its rows round, and at
+// low ranks two workgroups a compute unit, so that one begins while another adds up
+// (16384 x 4096 at rank 16: 29 us, with sixteen waves and one workgroup 35).
 constexpr int shrink_cols(int rt, int mt) { return rt + mt <= 4 ? 128 : 64; }
-constexpr int shrink_waves(int rt, int mt) { return rt + mt <= 2 ? 16 : 8; }
+constexpr int SH_WAVES = 8;
 
 // A workgroup takes 16 MT places of a tile; its waves, and with SH_PARTS gridDim.y
 // workgroups, share the long axis in steps of 128 or 64 columns, and the waves' sums
@@ -338,15 +340,15 @@ constexpr int shrink_waves(int rt, int mt) { return rt + mt <= 2 ? 16 : 8; }
 // them, 64 bytes of 16 rows at once, rows came in at 10 to 15 bytes a clock and
 // compute unit; 256 bytes of 4 rows, turned round in LDS, are not held back.
 // The rows of the next step are read while these are multiplied.  Measured:
-// 8192 x 5120 at rank 64 27 us (3.2 TB/s of x), 16384 x 4096 at rank 16 35 us
-// (3.8); of the reads of x alone, in any order, 16384 x 4096 took 25 to 34 us.
+// 8192 x 5120 at rank 64 26 us (3.2 TB/s of x), 16384 x 4096 at rank 16 29 us
+// (4.6); of the reads of x alone, in any order, 16384 x 4096 took 25 to 34 us.
 // SH_APPLY serves small batches, which wait for launches and round trips more
 // than for bytes: gridDim.y workgroups each make the same h, keep it in LDS and go
 // through their share of y's columns as k_lora_expand does; a wave's first rows and
 // adapter columns are read before h is made.
 template <int RT, int MT, int MODE>
-__global__ __launch_bounds__(shrink_waves(RT, MT) * kWave) void k_lora_shrink(ShrinkArgs g) {
-    constexpr int NW = shrink_waves(RT, MT), COLS = shrink_cols(RT, MT), P = COLS / 8;
+__global__ __launch_bounds__(SH_WAVES * kWave) void k_lora_shrink(ShrinkArgs g) {
+    constexpr int NW = SH_WAVES, COLS = shrink_cols(RT, MT), P = COLS / 8;
     constexpr int LOADS = P / 4, ROWS = 64 / P;  // loads of 16 rows, rows of a load
     constexpr bool APPLY = MODE == SH_APPLY, AHEAD = RT <= 4;
     static_assert(!APPLY || MT == 1, "16 places in SH_APPLY");
@@ -1060,7 +1062,7 @@ int64_t lora_most_fused_chunks(int64_t T, int64_t S, int64_t N) {
 template <int RT, int MT, int MODE>
 void launch_shrink_rt(const ShrinkArgs &g, int parts, hipStream_t stream) {
     const dim3 grid((unsigned)(MT == 1 ? g.max_groups : g.max_tiles * (4 / MT)), (unsigned)parts);
-    k_lora_shrink<RT, MT, MODE><<<grid, dim3(shrink_waves(RT, MT) * kWave), 0, stream>>>(g);
+    k_lora_shrink<RT, MT, MODE><<<grid, dim3(SH_WAVES * kWave), 0, stream>>>(g);
 }
 
 // (one rank tile always takes 16 places, and eight leave room in LDS for no more)
@@ -1099,7 +1101,7 @@ void launch_expand(const ExpandArgs &g, int rt, hipStream_t stream) {
 // or more.  Each writes its own part of h, which expand adds up.
 int lora_parts(int64_t T, int64_t S, int64_t C, int64_t R) {
     const int64_t groups = (T + 15) / 16 + (S < T ? S : T);
-    const int64_t waves = shrink_waves((int)((R + 15) / 16), 1), cols = shrink_cols((int)((R + 15) / 16), 1);
+    const int64_t waves = SH_WAVES, cols = shrink_cols((int)((R + 15) / 16), 1);
     const int64_t most = (C + cols - 1) / cols / waves, parts = 256 / groups < most ? 256 / groups : most;
     return (int)(parts < 1 ? 1 : (parts > 8 ? 8 : parts));
 }
@@ -1199,7 +1201,7 @@ void shrink(const uint16_t *x, int64_t ldx, const uint16_t *a, const float *scal
     g.partial = partial;
     // 32 places a workgroup, so that the adapter is read half as often, once that still fills the chip
     // and few adapters end in the first half of a tile: 8192 x 5120 at rank 64 37 us with 16 places, 27
-    // with 32; at rank 16 or less the adapter weighs little (16384 x 4096 at rank 16: 35 us, 39)
+    // with 32; at rank 16 or less the adapter weighs little (16384 x 4096 at rank 16: 29 us, 39)
     if (parts > 1) launch_shrink<1, SH_PARTS>(g, parts, rt, stream);
     else if (rt >= 2 && T >= 8192 && T / S >= 128) launch_shrink<2, SH_WHOLE>(g, 1, rt, stream);
     else launch_shrink<1, SH_WHOLE>(g, 1, rt, stream);
@@ -1213,7 +1215,7 @@ void shrink(const uint16_t *x, int64_t ldx, const uint16_t *a, const float *scal
 // against 9.8 and one launch less), and where h's long axis can be shared and one
 // workgroup would read long (4 tokens, 4096 to 4096, rank 128: 1 MB, 22 us against 14).
 int64_t lora_apply_groups(int64_t T, int64_t S, int64_t C, int64_t N, int64_t R, bool shared) {
-    const int64_t groups = lora_max_groups(T, S), waves = shrink_waves((int)((R + 15) / 16), 1);
+    const int64_t groups = lora_max_groups(T, S), waves = SH_WAVES;
     if (groups > 256 || (shared && R * C * 2 > 384 << 10)) return 0;
     const int64_t blocks = (N + 127) / 128, most = (blocks + waves - 1) / waves;
     const int64_t n = 256 / groups < most ? 256 / groups : most;
