@@ -59,7 +59,7 @@ struct AdamArgs {
     int64_t *seg_offsets;
     uint32_t *d_status;
     uint32_t *counts;  // [step's waves] changed elements
-    uint16_t *flags;   // [step's waves][64][CH] a lane's changed flags, bit 4 g + k of each 1024 elements
+    uint32_t *flags;   // [tiles][512] a bit per element of a tile, in order
 };
 
 constexpr int AW_BLOCK = 256;  // elements of a state block: one group of a wave
@@ -297,6 +297,24 @@ __device__ __forceinline__ uint32_t aw_chunk(const AdamArgs &a, const AdamTensor
     return flags;
 }
 
+// A wave's changed flags of 1024 elements (lane l: bit 4 g + k for element 256 g +
+// 4 l + k) as 32 words in element order: lane 8 j + g, g < 4, gets word 8 g + j.
+__device__ __forceinline__ uint32_t pack_flags(uint32_t f) {
+    using namespace dppc;
+    uint32_t word[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {  // the nibbles of eight lanes, in the first of them
+        uint32_t v = (f >> (4 * g)) & 0xFu;
+        v |= dpp_mov<kRowShl1, 0xf, 0xf>(0u, v) << 4;
+        v |= dpp_mov<kRowShl2, 0xf, 0xf>(0u, v) << 8;
+        word[g] = v | dpp_mov<kRowShl4, 0xf, 0xf>(0u, v) << 16;
+    }
+    const uint32_t w1 = dpp_mov<kRowShr1, 0xf, 0xf>(0u, word[1]), w2 = dpp_mov<kRowShr2, 0xf, 0xf>(0u, word[2]);
+    const uint32_t w3 = dpp_mov<0x113 /*row shift right by 3*/, 0xf, 0xf>(0u, word[3]);
+    const int g = lane_id() & 3;
+    return g == 0 ? word[0] : (g == 1 ? w1 : (g == 2 ? w2 : w3));
+}
+
 // One workgroup of four waves per piece, 1024 CH elements a wave (CH = 4: a whole
 // tile, CH = 1: a quarter).  With a patch each wave leaves its changed flags and
 // their number for k_adamw_patch.  Bound by HBM: 487.6M elements with 32-bit states,
@@ -345,81 +363,103 @@ __global__ __launch_bounds__(CD_THREADS) void k_adamw(AdamArgs a) {
         const int64_t wave = (int64_t)piece * 4 + w;
         const uint32_t count = wave_reduce_sum((uint32_t)__builtin_popcountll(flags));
         if (l == 0) a.counts[wave] = count;
-        if (count != 0) {
-            if constexpr (CH == 4) reinterpret_cast<uint64_t *>(a.flags)[wave * kWave + l] = flags;
-            else a.flags[wave * kWave + l] = (uint16_t)flags;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const uint32_t word = pack_flags((uint32_t)(flags >> (16 * c)));
+            if ((l & 7) < 4) a.flags[(wave * CH + c) * 32 + (l & 7) * 8 + (l >> 3)] = word;
         }
     }
     if (!ok && threadIdx.x == 0) or_agent32(a.d_status, 0x10u /*PULSE_DS_BADSEGMENT*/);
 }
 
-// The patch: a workgroup takes a run of the step's waves, whose first entry is
-// the sum of the counts before it; each of its waves goes through its share,
-// reads the changed elements' new view and writes their entries.  The step has
-// no place in the patch to wait for: placing a piece's entries by a ticket and
-// a look-back within the step itself cost 23 ns a piece, one after the other,
-// and 41 us before the first 1800 pieces had begun (5.2M elements: 57 us, with
-// this kernel 29 + 7; 218M with 8-bit states: 895 us, 700 + 105).
+// The patch: a workgroup takes a run of units of 4096 elements, whose first entry
+// is the sum of the counts before it; each of its waves goes through its share, 64
+// consecutive elements a lane, so that one scan ranks a unit's entries and a lane
+// picks its own bit by bit.  The step has no place in the patch to wait for:
+// placing a piece's entries by a ticket and a look-back within the step itself cost
+// 23 ns a piece, one after the other, and 41 us before the first 1800 pieces had
+// begun (5.2M elements: 57 us, with this kernel 29 + 6; 218M with 8-bit states: 895
+// us, 700 + 48).  Ranked with ballots, four for every 256 elements as in the codec's
+// passes, it was bound by its instructions: 85 to 119 us.
 template <int CH>
 __global__ __launch_bounds__(CD_THREADS) void k_adamw_patch(AdamArgs a) {
-    constexpr int kPerTile = 16 / CH;  // the step's waves of a tile
-    __shared__ int32_t s_idx[CD_THREADS / kWave][CD_SB];
-    __shared__ uint16_t s_val[CD_THREADS / kWave][CD_SB];
+    constexpr int kCounts = 4 / CH;  // the step's waves of a unit
+    constexpr int kAtOnce = 4;       // entries whose values are on their way together
     __shared__ uint64_t s_sum[CD_THREADS / kWave];
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
-    const int64_t nw = (int64_t)a.npieces * 4;
-    const int64_t w0 = nw * blockIdx.x / gridDim.x, w1 = nw * (blockIdx.x + 1) / gridDim.x;
-    const int64_t first = w0 + (w1 - w0) * w / 4, last = w0 + (w1 - w0) * (w + 1) / 4;
+    const int64_t nu = (int64_t)a.npieces * CH;
+    const int64_t u0 = nu * blockIdx.x / gridDim.x, u1 = nu * (blockIdx.x + 1) / gridDim.x;
+    const int64_t first = u0 + (u1 - u0) * w / 4, last = u0 + (u1 - u0) * (w + 1) / 4;
+    const uint64_t *const flags = reinterpret_cast<const uint64_t *>(a.flags) + l;
+    uint64_t next = first < last ? flags[first * kWave] : 0;
     uint64_t sum = 0;
     const u32x4 *c4 = reinterpret_cast<const u32x4 *>(a.counts);
-    for (int64_t i = threadIdx.x; i < w0 / 4; i += CD_THREADS) {
+    const int64_t before = u0 * kCounts;
+    for (int64_t i = threadIdx.x; i < before / 4; i += CD_THREADS) {
         const u32x4 c = c4[i];
         sum += (uint64_t)c.x + c.y + ((uint64_t)c.z + c.w);
     }
-    if (threadIdx.x < (w0 & 3)) sum += a.counts[w0 / 4 * 4 + threadIdx.x];
+    if (threadIdx.x < (before & 3)) sum += a.counts[before / 4 * 4 + threadIdx.x];
     sum = wave_reduce_sum(sum);
     if (l == 0) s_sum[w] = sum;
     __syncthreads();
     uint64_t run = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
     uint32_t mine = 0;
-    for (int64_t i = w0 + l; i < first; i += kWave) mine += a.counts[i];
+    for (int64_t i = before + l; i < first * kCounts; i += kWave) mine += a.counts[i];
     run += wave_reduce_sum(mine);
+    // the tensor of the current unit, and the tiles it has
+    const uint16_t *b = nullptr;
+    int64_t tile0 = 0, tile1 = 0;
     for (int64_t i = first; i < last; ++i) {
-        const uint32_t count = (uint32_t)__builtin_amdgcn_readfirstlane((int)a.counts[i]);
-        const uint32_t tile = (uint32_t)(i / kPerTile);
-        const uint32_t s = (uint32_t)__builtin_amdgcn_readfirstlane((int)a.tile_seg[tile]);
-        if (s < (uint32_t)a.nseg) {
-            const int64_t lt = (int64_t)tile - a.segs[s].tile0;
-            if (l == 0 && lt == 0 && i % kPerTile == 0) a.seg_offsets[s] = (int64_t)run;
-            if (count != 0) {
-                const int64_t wbase = lt * CD_TILE + (i % kPerTile) * (CH * 1024);
-                uint64_t flags;
-                if constexpr (CH == 4) flags = reinterpret_cast<const uint64_t *>(a.flags)[i * kWave + l];
-                else flags = a.flags[i * kWave + l];
-                const uint16_t *b = a.segs[s].b + wbase + 4 * l;
-                const int64_t left = a.segs[s].n - wbase - 4 * l;
-                uint32_t nvp[CH * 8];
-#pragma unroll
-                for (int g = 0; g < CH * 4; ++g) {
-                    const uint32_t f = (uint32_t)(flags >> (4 * g)) & 0xFu;
-                    u32x2 v = {0, 0};
-                    if (f) {
-                        if (left >= g * 256 + 4) v = *reinterpret_cast<const u32x2 *>(b + g * 256);
-                        else {  // the tensor's last one to three elements
-                            v.x = b[g * 256];
-                            if (f & 2u) v.x |= (uint32_t)b[g * 256 + 1] << 16;
-                            if (f & 4u) v.y = b[g * 256 + 2];
-                        }
-                    }
-                    nvp[2 * g] = v.x;
-                    nvp[2 * g + 1] = v.y;
+        uint64_t bits = next;
+        if (i + 1 < last) next = flags[(i + 1) * kWave];
+        const int64_t tile = i / 4;
+        if (tile >= tile1) {
+            const uint32_t s = (uint32_t)__builtin_amdgcn_readfirstlane((int)a.tile_seg[tile]);
+            b = nullptr;
+            tile0 = tile;
+            tile1 = tile + 1;
+            if (s < (uint32_t)a.nseg) {
+                const AdamSeg &seg = a.segs[s];
+                const int64_t t1 = seg.tile0 + (seg.n + CD_TILE - 1) / CD_TILE;
+                if (tile >= seg.tile0 && tile < t1) {
+                    b = seg.b;
+                    tile0 = seg.tile0;
+                    tile1 = t1;
                 }
-                cd_pass2<4 * CH>(a, flags, nvp, wbase, 4 * l, (int64_t)run, s_idx[w], s_val[w]);
+                if (l == 0 && i % 4 == 0 && tile == seg.tile0) a.seg_offsets[s] = (int64_t)run;
             }
         }
-        run += count;
+        const uint32_t count = (uint32_t)__builtin_popcountll(bits), incl = wave_incl_sum(count);
+        const uint32_t total = (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
+        int64_t at = (int64_t)(run + incl - count);
+        run += total;
+        if (total == 0 || !b) continue;
+        const int32_t e0 = (int32_t)((i - tile0 * 4) * 4096) + l * 64;
+        while (__ballot(bits != 0)) {
+            int32_t e[kAtOnce];
+            uint16_t v[kAtOnce];
+            int n = 0;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                e[k] = -1;
+                if (bits) {
+                    e[k] = e0 + __builtin_ctzll(bits);
+                    v[k] = b[e[k]];
+                    bits &= bits - 1;
+                    n = k + 1;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                if (e[k] >= 0 && at + k < a.cap) {
+                    a.idx[at + k] = e[k];
+                    a.val[at + k] = v[k];
+                }
+            at += n;
+        }
     }
-    if (last == nw && first < last && l == 0) {
+    if (last == nu && first < last && l == 0) {
         a.seg_offsets[a.nseg] = (int64_t)run;
         if ((int64_t)run > a.cap) or_agent32(a.d_status, 1u /*PULSE_DS_CAPACITY*/);
     }
@@ -623,7 +663,7 @@ extern "C" int pulse_launch_adamw(const void *segs, int32_t nseg, const uint32_t
     a.cap = cap;
     a.seg_offsets = seg_offsets;
     a.d_status = d_status;
-    a.flags = static_cast<uint16_t *>(ws);
+    a.flags = static_cast<uint32_t *>(ws);
     a.counts = ws ? reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + ntiles * (CD_TILE / 8)) : nullptr;
     if (ntiles >= kWholeTiles) {
         a.npieces = (uint32_t)ntiles;

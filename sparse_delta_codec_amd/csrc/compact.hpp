@@ -1,7 +1,8 @@
-// compact.hpp -- the compaction stage shared by the kernels that write a sparse
-// patch: a wave's changed elements, known as one flag bit per element and the
-// new values in registers, are ranked with ballots, staged in LDS and written
-// as one contiguous, ascending stretch of (int32 index, BF16 value) entries.
+// compact.hpp -- the tiling of the calls over lists of tensors, and the compaction
+// stage of the kernels that write a sparse patch in their own pass: a wave's
+// changed elements, known as one flag bit per element and the new values in
+// registers, are ranked with ballots, staged in LDS and written as one contiguous,
+// ascending stretch of (int32 index, BF16 value) entries.
 // A: any struct with the patch's idx, val and cap.
 #pragma once
 
@@ -45,12 +46,12 @@ __device__ __forceinline__ void cd_flush(const A &a, const int32_t *sbi, const u
 // in the wave's LDS buffer at its rank; the buffer goes out with coalesced
 // stores (the wave's entries are one contiguous stretch of the patch, the
 // first at position run).
-template <int GROUPS = CD_GROUPS, typename A>
+template <typename A>
 __device__ __forceinline__ void cd_pass2(const A &a, uint64_t flags, const uint32_t nvp[], int64_t wbase,
                                          int lo, int64_t run, int32_t *sbi, uint16_t *sbv) {
     uint32_t nb = 0;
 #pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
+    for (int g = 0; g < CD_GROUPS; ++g) {
         const uint32_t f = (uint32_t)(flags >> (4 * g)) & 0xFu;
         const uint64_t m0 = __ballot(f & 1u), m1 = __ballot(f & 2u), m2 = __ballot(f & 4u), m3 = __ballot(f & 8u);
         const uint32_t gtot = __builtin_popcountll(m0) + __builtin_popcountll(m1) + __builtin_popcountll(m2) +
