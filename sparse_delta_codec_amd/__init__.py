@@ -853,11 +853,11 @@ def lora_hidden(n_tokens, rank, n_adapters, device="cuda"):
 # only when it fails are they gone through one by one for the message.
 def _rows(t, rows, cols, name):
     """A BF16 matrix [rows, cols] with contiguous columns and any row stride that is
-    a multiple of 8.  Returns (data pointer, row stride)."""
+    a multiple of 8 (of a single row: any at all).  Returns (data pointer, row stride)."""
     try:
         stride = t.stride()
         if t.shape == (rows, cols) and t.is_cuda and t.dtype in _U16 and (stride[1] == 1 or cols <= 1 or rows == 0):
-            return t.data_ptr(), stride[0] if rows > 1 else max(stride[0], cols)
+            return t.data_ptr(), stride[0] if rows > 1 else cols
     except AttributeError:
         pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:

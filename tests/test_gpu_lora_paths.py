@@ -158,3 +158,16 @@ def test_plan_lists_the_places_in_use(t, s, shape):
     want = [(first[a] * 4 + i) for a in range(s) for i in range((int((ids == a).sum()) + 15) // 16)]
     assert np.array_equal(group[:len(want)], want) and np.all(group[len(want):] == -1)
     assert first[s] == w[0] == sum((int((ids == a).sum()) + 63) // 64 for a in range(s))
+
+
+def test_one_row_of_any_stride():
+    """A single token's rows may be cut from wider ones of any length."""
+    c = Batch(1, 64, 40, 16, 2, ids=[1], seed=2)
+    c.gpu_plan()
+    x, y = torch.zeros(2, 1001, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 333, dtype=torch.bfloat16, device="cuda")
+    x[:1, :64], y[:1, :40] = c.X, c.Y
+    c.Y = y[:1, :40]
+    pulse.pulse_lora_forward(x[:1, :64], c.A, c.B, c.SC, c.plan, c.Y, pulse.lora_workspace(1, 64, 40, 16, 2))
+    torch.cuda.synchronize()
+    c.check_forward()
+    assert not y[0, 40:].any() and not y[1].any()
