@@ -161,21 +161,21 @@ struct AdamTensor {
     uint32_t key;
 };
 
-// Four groups of 256 elements of one wave (lane l: elements 4l .. 4l+3 of each
+// G groups of 256 elements of one wave (lane l: elements 4l .. 4l+3 of each
 // group, the first group at element e0 of the tensor): the step, its stores,
 // and the changed flags (bit 4g+k) for the patch.
-template <bool FULL, bool BF16G, bool EIGHT, bool PATCH>
+template <int G, bool FULL, bool BF16G, bool EIGHT, bool PATCH>
 __device__ __forceinline__ uint32_t aw_chunk(const AdamArgs &a, const AdamTensor &t, int64_t e0) {
     typedef typename GradVec<BF16G>::T GV;
     const int64_t n = t.s.n;
     const int64_t el = e0 + 4 * lane_id();
-    u32x4 pv[4];
-    GV gv[4];
-    u32x4 mv[4], vv[4];
-    uint32_t mc[4], vc[4];
-    u32x2 ov[4];
+    u32x4 pv[G];
+    GV gv[G];
+    u32x4 mv[G], vv[G];
+    uint32_t mc[G], vc[G];
+    u32x2 ov[G];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < G; ++g) {
         const int64_t e = el + g * 256;
         pv[g] = load4<FULL, u32x4>(t.s.p, e, n);
         gv[g] = load4<FULL, GV>(t.s.g, e, n);
@@ -191,15 +191,15 @@ __device__ __forceinline__ uint32_t aw_chunk(const AdamArgs &a, const AdamTensor
     // the blocks' scales: lane g of the wave holds block e0 / 256 + g
     float ms = 0.0f, vs = 0.0f;
     if constexpr (EIGHT) {
-        const int64_t blk = e0 / AW_BLOCK + (lane_id() & 3);
+        const int64_t blk = e0 / AW_BLOCK + (lane_id() & (G - 1));
         if (FULL || blk * AW_BLOCK < n) {
             ms = t.s.m_scale[blk];
             vs = t.s.v_scale[blk];
         }
     }
-    uint32_t flags = 0, mmax[4], umax[4];
+    uint32_t flags = 0, mmax[G], umax[G];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < G; ++g) {
         float m4[4], v4[4];
         if constexpr (EIGHT) {
             const float sm = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(ms), g));
@@ -264,7 +264,7 @@ __device__ __forceinline__ uint32_t aw_chunk(const AdamArgs &a, const AdamTensor
         const int q = lane_id() & 7;
         uint32_t ab = 0;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < G; ++g) {
             ab = q == 2 * g ? mmax[g] : ab;
             ab = q == 2 * g + 1 ? umax[g] : ab;
         }
@@ -273,9 +273,9 @@ __device__ __forceinline__ uint32_t aw_chunk(const AdamArgs &a, const AdamTensor
         const float scale = live ? amax / 448.0f : 0.0f;
         const float inv = live ? 448.0f / amax : 0.0f;
         const int64_t blk = e0 / AW_BLOCK + (q >> 1);
-        if (lane_id() < 8 && (FULL || blk * AW_BLOCK < n)) ((q & 1) ? t.s.v_scale : t.s.m_scale)[blk] = scale;
+        if (lane_id() < 2 * G && (FULL || blk * AW_BLOCK < n)) ((q & 1) ? t.s.v_scale : t.s.m_scale)[blk] = scale;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < G; ++g) {
             const int64_t e = el + g * 256;
             const float im = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(inv), 2 * g));
             const float iu = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(inv), 2 * g + 1));
@@ -315,14 +315,14 @@ __device__ __forceinline__ uint32_t pack_flags(uint32_t f) {
     return g == 0 ? word[0] : (g == 1 ? w1 : (g == 2 ? w2 : w3));
 }
 
-// One workgroup of four waves per piece, 1024 CH elements a wave (CH = 4: a whole
-// tile, CH = 1: a quarter).  With a patch each wave leaves its changed flags and
+// One workgroup of four waves per piece, E elements a wave (4096: a piece is a whole
+// tile; 1024 and 256: a quarter and a sixteenth).  With a patch each wave leaves its changed flags and
 // their number for k_adamw_patch.  Bound by HBM: 487.6M elements with 32-bit states,
 // 28 bytes each, 2.60 ms (5.2 TB/s, as a large copy); 218M with 8-bit states and the
-// flags, 20 bytes each, 0.70 ms (6.2 TB/s); 475K elements 5.7 us.
-template <int CH, bool BF16G, bool EIGHT, bool PATCH>
+// flags, 20 bytes each, 0.70 ms (6.2 TB/s); 475K elements 4.4 us.
+template <int E, bool BF16G, bool EIGHT, bool PATCH>
 __global__ __launch_bounds__(CD_THREADS) void k_adamw(AdamArgs a) {
-    constexpr int kPerTile = 4 / CH;
+    constexpr int kPerTile = CD_TILE / (4 * E), G = E < 1024 ? E / 256 : 4, CH = E / (256 * G);
     const uint32_t piece = blockIdx.x, tile = piece / kPerTile;
     const uint32_t s = (uint32_t)__builtin_amdgcn_readfirstlane((int)a.tile_seg[tile]);
     AdamTensor t{};
@@ -341,20 +341,20 @@ __global__ __launch_bounds__(CD_THREADS) void k_adamw(AdamArgs a) {
     t.key = aw_mix(a.seed + (s + 1u) * 0x9E3779B1u);
     const bool skip = !(__builtin_fabsf(t.scale) <= 3.402823466e38f);  // NaN or infinite: no step
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
-    const int64_t wbase = lt * CD_TILE + (int64_t)(piece % kPerTile) * (CH * 4096) + (int64_t)w * (CH * 1024);
+    const int64_t wbase = lt * CD_TILE + (int64_t)(piece % kPerTile) * (4 * E) + (int64_t)w * E;
     uint64_t flags = 0;
     if (ok && !skip && wbase < t.s.n) {
-        if (wbase + CH * 1024 <= t.s.n) {
+        if (wbase + E <= t.s.n) {
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
-                flags |= (uint64_t)aw_chunk<true, BF16G, EIGHT, PATCH>(a, t, wbase + c * 1024) << (16 * c);
+                flags |= (uint64_t)aw_chunk<G, true, BF16G, EIGHT, PATCH>(a, t, wbase + c * 1024) << (16 * c);
                 sched_fence();
             }
         } else {
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 if (wbase + c * 1024 < t.s.n)
-                    flags |= (uint64_t)aw_chunk<false, BF16G, EIGHT, PATCH>(a, t, wbase + c * 1024) << (16 * c);
+                    flags |= (uint64_t)aw_chunk<G, false, BF16G, EIGHT, PATCH>(a, t, wbase + c * 1024) << (16 * c);
                 sched_fence();
             }
         }
@@ -366,7 +366,7 @@ __global__ __launch_bounds__(CD_THREADS) void k_adamw(AdamArgs a) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const uint32_t word = pack_flags((uint32_t)(flags >> (16 * c)));
-            if ((l & 7) < 4) a.flags[(wave * CH + c) * 32 + (l & 7) * 8 + (l >> 3)] = word;
+            if ((l & 7) < G) a.flags[(wave * CH + c) * (8 * G) + (l & 7) * 8 + (l >> 3)] = word;
         }
     }
     if (!ok && threadIdx.x == 0) or_agent32(a.d_status, 0x10u /*PULSE_DS_BADSEGMENT*/);
@@ -381,13 +381,13 @@ __global__ __launch_bounds__(CD_THREADS) void k_adamw(AdamArgs a) {
 // begun (5.2M elements: 57 us, with this kernel 29 + 6; 218M with 8-bit states: 895
 // us, 700 + 48).  Ranked with ballots, four for every 256 elements as in the codec's
 // passes, it was bound by its instructions: 85 to 119 us.
-template <int CH>
+template <int E>
 __global__ __launch_bounds__(CD_THREADS) void k_adamw_patch(AdamArgs a) {
-    constexpr int kCounts = 4 / CH;  // the step's waves of a unit
+    constexpr int kCounts = 4096 / E;  // the step's waves of a unit
     constexpr int kAtOnce = 4;       // entries whose values are on their way together
     __shared__ uint64_t s_sum[CD_THREADS / kWave];
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id();
-    const int64_t nu = (int64_t)a.npieces * CH;
+    const int64_t nu = (int64_t)a.npieces * E / 1024;
     const int64_t u0 = nu * blockIdx.x / gridDim.x, u1 = nu * (blockIdx.x + 1) / gridDim.x;
     const int64_t first = u0 + (u1 - u0) * w / 4, last = u0 + (u1 - u0) * (w + 1) / 4;
     const uint64_t *const flags = reinterpret_cast<const uint64_t *>(a.flags) + l;
@@ -601,40 +601,43 @@ __global__ __launch_bounds__(GN_THREADS) void k_grad_norm(NormArgs a) {
 
 using namespace pulse;
 
-// A bit per element and a 4-byte count per wave of the step (4 or 16 of a tile).
+// A bit per element and a 4-byte count per wave of the step (4, 16 or 64 of a tile).
 extern "C" size_t pulse_adamw_ws_bytes(int64_t ntiles) {
-    return (size_t)(ntiles > 0 ? ntiles : 1) * (CD_TILE / 8 + 16 * sizeof(uint32_t));
+    return (size_t)(ntiles > 0 ? ntiles : 1) * (CD_TILE / 8 + 64 * sizeof(uint32_t));
 }
 
 extern "C" size_t pulse_grad_norm_ws_bytes(void) { return 256 + GN_MAX_BLOCKS * sizeof(double); }
 
 namespace {
 
-// Lists of fewer tiles than 4 per compute unit are cut into quarter tiles, so
-// that they spread over the chip.
-constexpr int64_t kWholeTiles = 1024;
+// Lists of fewer tiles than 4 per compute unit are cut into sixteenths of a tile, so
+// that they spread over the chip (5.2M float32 elements: 23.8 us, in quarters 27.5;
+// 0.48M with 8-bit states: 5.8 us, in quarters 8.5, for a wave's 1024 elements are
+// 4 us of instructions).  With a patch only short lists are: every piece's counts
+// are added up again by every workgroup of the patch (5.2M elements with 8-bit
+// states: 32.7 us, in quarters 27.9; 1M: 12.4 and 12.7).
+constexpr int64_t kWholeTiles = 1024, kPatchQuarterTiles = 64;
+constexpr int64_t kPatchBlocks = 2048;
 
-constexpr unsigned kPatchBlocks = 2048;
-
-template <int CH, bool BF16G, bool EIGHT>
-void launch_adamw(const AdamArgs &a, hipStream_t stream) {
-    const dim3 grid(a.npieces), block(CD_THREADS);
-    if (a.idx) {
-        k_adamw<CH, BF16G, EIGHT, true><<<grid, block, 0, stream>>>(a);
-        k_adamw_patch<CH><<<dim3(a.npieces < kPatchBlocks ? a.npieces : kPatchBlocks), block, 0, stream>>>(a);
-    } else {
-        k_adamw<CH, BF16G, EIGHT, false><<<grid, block, 0, stream>>>(a);
+template <int E, bool BF16G, bool EIGHT, bool PATCH>
+void launch_adamw(AdamArgs a, int64_t ntiles, hipStream_t stream) {
+    a.npieces = (uint32_t)(ntiles * (CD_TILE / (4 * E)));
+    k_adamw<E, BF16G, EIGHT, PATCH><<<dim3(a.npieces), dim3(CD_THREADS), 0, stream>>>(a);
+    if constexpr (PATCH) {
+        const int64_t units = ntiles * 4;
+        k_adamw_patch<E><<<dim3((unsigned)(units < kPatchBlocks ? units : kPatchBlocks)), dim3(CD_THREADS), 0, stream>>>(a);
     }
 }
 
-template <int CH>
-void launch_adamw_types(const AdamArgs &a, bool bf16, bool eight, hipStream_t stream) {
-    if (bf16) {
-        if (eight) launch_adamw<CH, true, true>(a, stream);
-        else launch_adamw<CH, true, false>(a, stream);
+template <bool BF16G, bool EIGHT>
+void launch_adamw_sizes(const AdamArgs &a, int64_t ntiles, hipStream_t stream) {
+    if (a.idx) {
+        if (ntiles >= kWholeTiles) launch_adamw<4096, BF16G, EIGHT, true>(a, ntiles, stream);
+        else if (ntiles >= kPatchQuarterTiles) launch_adamw<1024, BF16G, EIGHT, true>(a, ntiles, stream);
+        else launch_adamw<256, BF16G, EIGHT, true>(a, ntiles, stream);
     } else {
-        if (eight) launch_adamw<CH, false, true>(a, stream);
-        else launch_adamw<CH, false, false>(a, stream);
+        if (ntiles >= kWholeTiles) launch_adamw<4096, BF16G, EIGHT, false>(a, ntiles, stream);
+        else launch_adamw<256, BF16G, EIGHT, false>(a, ntiles, stream);
     }
 }
 
@@ -665,13 +668,11 @@ extern "C" int pulse_launch_adamw(const void *segs, int32_t nseg, const uint32_t
     a.d_status = d_status;
     a.flags = static_cast<uint32_t *>(ws);
     a.counts = ws ? reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + ntiles * (CD_TILE / 8)) : nullptr;
-    if (ntiles >= kWholeTiles) {
-        a.npieces = (uint32_t)ntiles;
-        launch_adamw_types<4>(a, grad_bf16 != 0, state_bits == 8, stream);
-    } else {
-        a.npieces = (uint32_t)(ntiles * 4);
-        launch_adamw_types<1>(a, grad_bf16 != 0, state_bits == 8, stream);
-    }
+    const bool bf16 = grad_bf16 != 0, eight = state_bits == 8;
+    if (bf16 && eight) launch_adamw_sizes<true, true>(a, ntiles, stream);
+    else if (bf16) launch_adamw_sizes<true, false>(a, ntiles, stream);
+    else if (eight) launch_adamw_sizes<false, true>(a, ntiles, stream);
+    else launch_adamw_sizes<false, false>(a, ntiles, stream);
     return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 

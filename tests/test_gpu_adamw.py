@@ -341,3 +341,24 @@ def test_patch_of_a_long_list_on_a_used_workspace(bits):
     n = int(counts[-1])
     assert torch.equal(idx[:n].long(), torch.cat(want))
     assert torch.equal(val[:n].view(torch.int16), torch.cat([x[w].view(torch.int16) for x, w in zip(b, want)]))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("grad", ["float32", "bfloat16"])
+@pytest.mark.parametrize("tiles", [63, 64, 130])
+def test_patch_around_the_sizes_of_a_piece(bits, grad, tiles):
+    """Lists of just under and over the lengths at which a tile is cut otherwise."""
+    sizes = [300, 257, 16384 * 2 + 1, 16384 * (tiles - 6), 255]
+    c = Case(sizes, tiles, grad, bits)
+    assert c.table.ntiles == tiles
+    before, total = [b.copy() for b in c.b], sum(sizes)
+    idx, val = zeros(total, torch.int32), zeros(total, torch.int16)
+    offs = zeros(len(sizes) + 1, torch.int64)
+    c.step_host(3, 1e-5, seed=9)
+    c.step_gpu(3, 1e-5, seed=9, patch_idx=idx, patch_val=val, seg_offsets=offs)
+    c.check()
+    want = [np.flatnonzero(a != b) for a, b in zip(before, c.b)]
+    assert np.array_equal(host(offs), np.cumsum([0] + [w.size for w in want]))
+    n = sum(w.size for w in want)
+    assert 0 < n < total and np.array_equal(host(idx)[:n], np.concatenate(want))
+    assert np.array_equal(host(val, np.uint16)[:n], np.concatenate([b[w] for b, w in zip(c.b, want)]))
