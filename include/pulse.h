@@ -681,9 +681,10 @@ int pulse_adamw_step(const pulse_adamw_segment *segs, int32_t nseg, const uint32
  * row of the projection's output [N]:
  *   h = scale_i A_i x,   y += B_i^T h                                 (forward)
  *   dh = scale_i B_i dy, dx += A_i^T dh, dA_i = sum dh x^T, dB_i = sum h dy^T
- * Sums are held in float32.  h and dh are rounded to BF16 for the products with
- * B and A, once; in dA and dB they enter as float32 (the sum of three BF16).  y
- * and dx are rounded once, after the addition.
+ * Sums are held in float32.  In the products with B and A, h and dh enter as the
+ * sum of two BF16 (2^-16 of themselves is left out; y and dx keep 2^-8); in dA and
+ * dB as float32 (the sum of three BF16).  y and dx are rounded once, after the
+ * addition.
  *
  * Layouts: x [T][ldx], y [T][ldy], dy, dx BF16 rows with any row stride that is
  * a multiple of 8 elements; a [S][R][K] and b [S][R][N] BF16 (b is stored with

@@ -232,8 +232,9 @@ __global__ __launch_bounds__(NW *kWave) void k_lora_plan(const int32_t *__restri
 }
 
 // ---- what the kernels share -----------------------------------------------------
-// h (or dh) of every place, in the forms its readers want: BF16 [place][Rp] for
-// expand; for outer, whose sums over tokens go out in float32, the float32 value
+// h (or dh) of every place, in the forms its readers want: for expand, whose sums go
+// out with 8 bits of mantissa, two BF16 (16 bits) in the order of its matrix operand
+// (put_row); for outer, whose sums over tokens go out in float32, the float32 value
 // as the exact sum of three BF16 (8 bits of mantissa each), each [Rp][place].
 struct LoraHidden {
     uint16_t *rows;
@@ -242,14 +243,14 @@ struct LoraHidden {
 
 inline int64_t lora_hidden_size(int64_t T, int64_t S, int64_t R, bool train) {
     const int64_t rp = (R + 15) / 16 * 16, places = lora_max_tiles(T, S) * LT;
-    return places * rp * 2 * (train ? 4 : 1);
+    return places * rp * 2 * (train ? 5 : 2);
 }
 
 inline LoraHidden lora_hidden_parts(void *h, int64_t T, int64_t S, int64_t R, bool train) {
     const int64_t rp = (R + 15) / 16 * 16, places = lora_max_tiles(T, S) * LT;
     LoraHidden p;
     p.rows = static_cast<uint16_t *>(h);
-    for (int i = 0; i < 3; ++i) p.part[i] = train ? p.rows + (i + 1) * places * rp : nullptr;
+    for (int i = 0; i < 3; ++i) p.part[i] = train ? p.rows + (i + 2) * places * rp : nullptr;
     return p;
 }
 
@@ -277,12 +278,148 @@ __device__ __forceinline__ u32x4 ld16_once(const uint16_t *p) {
 
 __device__ __forceinline__ bf16x8 as_bf(const u32x4 &v) { return __builtin_bit_cast(bf16x8, v); }
 
+// Four float32 values as two BF16 each: the nearest one, at most the largest, and what
+// is left with its infinities and NaN (an infinity in the first part would leave no
+// number for the second).
+struct Split {
+    u32x2 top, rest;
+};
+
+__device__ __forceinline__ Split split4(const f32x4 &v) {
+    constexpr float kMost = 0x1.FEp127f;  // the largest BF16
+    Split s;
+    s.top = u32x2{cast_pair(__builtin_amdgcn_fmed3f(v[0], -kMost, kMost), __builtin_amdgcn_fmed3f(v[1], -kMost, kMost)),
+                  cast_pair(__builtin_amdgcn_fmed3f(v[2], -kMost, kMost), __builtin_amdgcn_fmed3f(v[3], -kMost, kMost))};
+    float left[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        left[i] = v[i] - __uint_as_float((i & 1) ? (s.top[i >> 1] & 0xFFFF0000u) : (s.top[i >> 1] << 16));
+    s.rest = u32x2{cast_pair(left[0], left[1]), cast_pair(left[2], left[3])};
+    return s;
+}
+
+// h's four values of ranks 16 rt + 4 q .. + 3 at one place of `rows`.  Expand's matrix
+// instruction takes 32 products, two rank tiles with their first parts, and once more
+// with their second ones; a tile that is left over takes two instructions of 16.
+// Operand i of a place's RT, for the lanes of quarter q, is the 16 bytes at
+// (place * RT + i) * 4 + q; of the tile left over, both its parts.
+__device__ __forceinline__ void put_row(u32x2 *rows, int64_t place, int RT, int rt, int q, const Split &s) {
+    const bool alone = rt == RT - 1 && (RT & 1);
+    u32x2 *const to = rows + ((place * RT + (alone ? rt : rt & ~1)) * 4 + q) * 2 + (alone ? 0 : rt & 1);
+    to[0] = s.top;
+    to[alone ? 1 : 8] = s.rest;
+}
+
+// the same operands in registers, from the values of all tiles
+template <int RT>
+__device__ __forceinline__ void row_operands(const f32x4 (&v)[RT], u32x4 (&h)[RT]) {
+#pragma unroll
+    for (int rt = 0; rt < RT; rt += 2) {
+        const Split a = split4(v[rt]);
+        if (rt + 1 < RT) {
+            const Split b = split4(v[rt + 1 < RT ? rt + 1 : rt]);
+            h[rt] = u32x4{a.top.x, a.top.y, b.top.x, b.top.y};
+            h[rt + 1 < RT ? rt + 1 : rt] = u32x4{a.rest.x, a.rest.y, b.rest.x, b.rest.y};
+        } else {
+            h[rt] = u32x4{a.top.x, a.top.y, a.rest.x, a.rest.y};
+        }
+    }
+}
+
+// A part of h below the first may be zero or of the other sign, and would make a NaN of
+// an infinity that its first part has multiplied into the sum already: there the lower
+// parts are multiplied with one of its sign instead.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t ones_for_infinities(uint32_t pair) {
+    if ((pair & 0x7F80u) == 0x7F80u) pair = (pair & 0xFFFF8000u) | 0x3F80u;
+    if ((pair & 0x7F800000u) == 0x7F800000u) pair = (pair & 0x8000FFFFu) | 0x3F800000u;
+    return pair;
+}
+
+// the larger magnitudes of two pairs, and whether a pair of magnitudes holds one that is not finite
+__device__ __forceinline__ uint32_t most_of(uint32_t m, uint32_t pair) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m),
+                                                                  __builtin_bit_cast(u16x2, pair & 0x7FFF7FFFu)));
+}
+
+__device__ __forceinline__ bool not_finite(uint32_t m) { return m >= 0x7F800000u || (m & 0xFFFFu) >= 0x7F80u; }
+
+// The adapter's operands beside h's: of each column of a lane's eight, the values of ranks
+// 4 q .. 4 q + 3 of two rank tiles, or of the one that is left over.
+template <int RT>
+struct Columns {
+    u32x4 pair[RT > 1 ? RT / 2 : 1][8];
+    u32x2 last[RT & 1 ? 8 : 1];
+};
+
+// rows(rt, v): the four ranks' rows, eight columns each.  Returns whether the columns are all finite.
+template <int RT, typename F>
+__device__ __forceinline__ bool read_columns(Columns<RT> &f, F &&rows) {
+    const auto low = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_perm(y, x, 0x05040100u); };
+    const auto high = [](uint32_t x, uint32_t y) { return __builtin_amdgcn_perm(y, x, 0x07060302u); };
+    uint32_t most = 0;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        u32x4 v[4];
+        rows(rt, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int d = j / 2;
+            const u32x2 c = (j & 1) ? u32x2{high(v[0][d], v[1][d]), high(v[2][d], v[3][d])}
+                                    : u32x2{low(v[0][d], v[1][d]), low(v[2][d], v[3][d])};
+            if (rt == RT - 1 && (RT & 1)) f.last[RT & 1 ? j : 0] = c;
+            else f.pair[rt / 2][j][2 * (rt & 1)] = c.x, f.pair[rt / 2][j][2 * (rt & 1) + 1] = c.y;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) most = most_of(most, v[i][d]);
+    }
+    return __ballot(not_finite(most)) == 0;
+}
+
+// out += h times eight columns.  Where these are not all finite, they are not the
+// adapter's any more afterwards.
+template <int RT>
+__device__ __forceinline__ void multiply_rows(const u32x4 *h, Columns<RT> &f, bool finite, f32x4 (&out)[8]) {
+    const auto last = [&](int half) {
+        const s16x4 a = __builtin_bit_cast(s16x4, u32x2{h[RT - 1][half * 2], h[RT - 1][half * 2 + 1]});
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            out[j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, __builtin_bit_cast(s16x4, f.last[RT & 1 ? j : 0]), out[j], 0,
+                                                               0, 0);
+    };
+#pragma unroll
+    for (int i = 0; i < RT / 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            out[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(h[2 * i]), as_bf(f.pair[i][j]), out[j], 0, 0, 0);
+    if constexpr (RT & 1) last(0);
+    if (!finite) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+            for (int i = 0; i < RT / 2; ++i)
+#pragma unroll
+                for (int d = 0; d < 4; ++d) f.pair[i][j][d] = ones_for_infinities(f.pair[i][j][d]);
+            if constexpr (RT & 1) f.last[j] = u32x2{ones_for_infinities(f.last[j].x), ones_for_infinities(f.last[j].y)};
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RT / 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            out[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(h[2 * i + 1]), as_bf(f.pair[i][j]), out[j], 0, 0, 0);
+    if constexpr (RT & 1) last(1);
+}
+
 // h's four values of ranks r .. r+3 at one place, in its forms
 __device__ __forceinline__ void store_hidden(const LoraHidden &h, int64_t place, int64_t places, int rp, int r,
                                              const f32x4 &v) {
-    const uint32_t p0 = cast_pair(v[0], v[1]), p1 = cast_pair(v[2], v[3]);
-    *reinterpret_cast<u32x2 *>(h.rows + place * rp + r) = u32x2{p0, p1};
+    put_row(reinterpret_cast<u32x2 *>(h.rows), place, rp / 16, r / 16, r % 16 / 4, split4(v));
     if (h.part[0]) {
+        const uint32_t p0 = cast_pair(v[0], v[1]), p1 = cast_pair(v[2], v[3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t top = (i < 2 ? p0 : p1) >> (16 * (i & 1)) & 0xFFFFu;
@@ -352,7 +489,7 @@ __global__ __launch_bounds__(SH_WAVES * kWave) void k_lora_shrink(ShrinkArgs g) 
     constexpr int LOADS = P / 4, ROWS = 64 / P;  // loads of 16 rows, rows of a load
     constexpr bool APPLY = MODE == SH_APPLY, AHEAD = RT <= 4;
     static_assert(!APPLY || MT == 1, "16 places in SH_APPLY");
-    __shared__ u32x2 s_h[APPLY ? 64 * RT : 1];  // [16 places][Rp] BF16
+    __shared__ u32x4 s_h[APPLY ? 64 * RT : 1];  // h of 16 places as put_row lays it out
     __shared__ u32x4 s_stage[NW][(MT + RT) * 16 * P];
     __shared__ int s_tok[16 * MT];
     // 16 places: from the plan's list, which leaves out the empty ones (a workgroup that finds nothing
@@ -486,22 +623,19 @@ __global__ __launch_bounds__(SH_WAVES * kWave) void k_lora_shrink(ShrinkArgs g) 
             *reinterpret_cast<f32x4 *>(g.partial + ((int64_t)blockIdx.y * g.places + place) * (RT * 16) + r) = v;
         } else {
             if (!APPLY || (g.h.rows && blockIdx.y == 0)) store_hidden(g.h, place, g.places, RT * 16, r, v);
-            if constexpr (APPLY) s_h[c16 * (RT * 4) + r / 4] = u32x2{cast_pair(v[0], v[1]), cast_pair(v[2], v[3])};
+            if constexpr (APPLY) put_row(reinterpret_cast<u32x2 *>(s_h), c16, RT, c % RT, q, split4(v));
         }
     }
     if constexpr (APPLY) {
         lds_barrier();
-        s16x4 hv[RT];
+        u32x4 hv[RT];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-            hv[rt] = __builtin_bit_cast(s16x4, s_h[(c16 < in ? c16 : 0) * (RT * 4) + rt * 4 + q]);
+        for (int i = 0; i < RT; ++i) hv[i] = s_h[((c16 < in ? c16 : 0) * RT + i) * 4 + q];
         while (jb * 128 < g.N) {
             f32x4 out[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) out[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                u32x4 v[4];
+            const auto rows_of = [&](int rt, u32x4 (&v)[4]) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if constexpr (AHEAD) v[i] = wv[rt][i];
@@ -510,16 +644,18 @@ __global__ __launch_bounds__(SH_WAVES * kWave) void k_lora_shrink(ShrinkArgs g) 
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (rt * 16 + q * 4 + i >= g.R) v[i] = u32x4{0, 0, 0, 0};
+            };
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const u32x2 lo = {__builtin_amdgcn_perm(v[1][d], v[0][d], 0x05040100u),
-                                      __builtin_amdgcn_perm(v[3][d], v[2][d], 0x05040100u)};
-                    const u32x2 hi = {__builtin_amdgcn_perm(v[1][d], v[0][d], 0x07060302u),
-                                      __builtin_amdgcn_perm(v[3][d], v[2][d], 0x07060302u)};
-                    out[2 * d] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(hv[rt], __builtin_bit_cast(s16x4, lo),
-                                                                           out[2 * d], 0, 0, 0);
-                    out[2 * d + 1] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(hv[rt], __builtin_bit_cast(s16x4, hi),
-                                                                               out[2 * d + 1], 0, 0, 0);
+            for (int rt = 0; rt < RT; rt += 2) {  // two tiles at a time
+                constexpr int kOne = RT & 1;
+                if (rt + 1 < RT) {
+                    Columns<2> f;
+                    const bool finite = read_columns<2>(f, [&](int i, u32x4(&v)[4]) { rows_of(rt + i, v); });
+                    multiply_rows<2>(hv + rt, f, finite, out);
+                } else if constexpr (kOne) {
+                    Columns<1> f;
+                    const bool finite = read_columns<1>(f, [&](int, u32x4(&v)[4]) { rows_of(RT - 1, v); });
+                    multiply_rows<1>(hv + RT - 1, f, finite, out);
                 }
             }
 #pragma unroll
@@ -542,7 +678,7 @@ constexpr int EX_TILES = 4;  // most tiles of a workgroup
 enum ExpandMode { EX_PLAIN, EX_PARTS, EX_ONCE };  // EX_PARTS: h in parts; EX_ONCE: y past the last-level cache
 
 struct ExpandArgs {
-    const uint16_t *h;     // [place][Rp]
+    const uint16_t *h;     // rows of put_row
     const float *partial;  // or its parts [parts][place][Rp] (EX_PARTS)
     const uint16_t *w;     // [S][R][C]
     uint16_t *y;
@@ -559,11 +695,12 @@ template <int RT>
 struct ExpandRows {
     int64_t at[4];
     u32x4 y[4];
-    s16x4 h[RT];
+    u32x4 h[RT];
 };
 
 // A wave takes 128 columns of the 64 places of each of its tiles.  Matrix
-// instruction: rows = places, columns = columns of y, 16 ranks.  Lane c of the
+// instruction: rows = places, columns = columns of y, the ranks of two tiles (of the
+// one left over, 16), once for each part of h.  Lane c of the
 // column axis holds the 8-column piece c, instruction j its column j: then the
 // lane's results i = 0..3 are, for j = 0..7, one 16-byte piece of the row of
 // place 4 q + i, and sixteen lanes touch 256 contiguous bytes; neighbouring
@@ -576,7 +713,7 @@ struct ExpandRows {
 // rank 64 161 us (5.6 TB/s; with the branches 206), 16384 x 14336 at rank 16 183 us
 // (5.1; a large copy 5.2).
 template <int RT, int MODE>
-__global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
+__global__ __launch_bounds__(256, RT <= 2 ? 3 : (RT <= 4 ? 2 : 1)) void k_lora_expand(ExpandArgs g) {
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), c16 = l & 15, q = l >> 4;
     const int blocks = (g.C + 511) / 512;
     const int base = ((int)blockIdx.x % blocks * 4 + w) * 128, col = base + c16 * 8 < g.C ? base + c16 * 8 : base;
@@ -607,23 +744,22 @@ __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
     const auto read = [&](ExpandRows<RT> &r, int tile, int sub, int count) {
         const int64_t *const row = s_row + (tile - ta) * LT + sub * 16 + q * 4;
         const int in = count - sub * 16;  // places of the 16 that hold a token
-        const int64_t at = ((int64_t)tile * LT + sub * 16 + (c16 < in ? c16 : 0)) * (RT * 16) + q * 4;
+        const int64_t place = (int64_t)tile * LT + sub * 16 + (c16 < in ? c16 : 0);
         if constexpr (MODE == EX_PARTS) {
+            const float *const at = g.partial + place * (RT * 16) + q * 4;
             f32x4 v[RT];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) v[rt] = *reinterpret_cast<const f32x4 *>(g.partial + at + rt * 16);
+            for (int rt = 0; rt < RT; ++rt) v[rt] = *reinterpret_cast<const f32x4 *>(at + rt * 16);
 #pragma unroll 2
             for (int p = 1; p < g.parts; ++p)
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
-                    v[rt] += *reinterpret_cast<const f32x4 *>(g.partial + p * g.places * (RT * 16) + at + rt * 16);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-                r.h[rt] = __builtin_bit_cast(s16x4, u32x2{cast_pair(v[rt][0], v[rt][1]), cast_pair(v[rt][2], v[rt][3])});
+                    v[rt] += *reinterpret_cast<const f32x4 *>(at + p * g.places * (RT * 16) + rt * 16);
+            row_operands<RT>(v, r.h);
         } else {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-                r.h[rt] = __builtin_bit_cast(s16x4, *reinterpret_cast<const u32x2 *>(g.h + at + rt * 16));
+            for (int i = 0; i < RT; ++i)
+                r.h[i] = reinterpret_cast<const u32x4 *>(g.h)[(place * RT + i) * 4 + q];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) r.at[i] = row[i];
@@ -633,7 +769,8 @@ __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
     int tile = ta, sub = 0, cur = -1, slot = slot_of(ta);
     if (slot < 0) return;
     int count = count_of(ta);
-    s16x4 frag[RT][8];
+    Columns<RT> w_cols;
+    bool finite = true;
     // one step: the next 16 places (or, at the end, these once more) into `next`, these out of `now`
     const auto step = [&](ExpandRows<RT> &now, ExpandRows<RT> &next) {
         int tile1 = tile, sub1 = sub + 1, slot1 = slot, count1 = count;
@@ -646,9 +783,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
         const bool more = slot1 >= 0;
         if (slot != cur) {
             cur = slot;
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                u32x4 v[4];
+            const auto rows_of = [&](int rt, u32x4 (&v)[4]) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = rt * 16 + q * 4 + i;
@@ -657,27 +792,16 @@ __global__ __launch_bounds__(256) void k_lora_expand(ExpandArgs g) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (rt * 16 + q * 4 + i >= g.R) v[i] = u32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const u32x2 lo = {__builtin_amdgcn_perm(v[1][d], v[0][d], 0x05040100u),
-                                      __builtin_amdgcn_perm(v[3][d], v[2][d], 0x05040100u)};
-                    const u32x2 hi = {__builtin_amdgcn_perm(v[1][d], v[0][d], 0x07060302u),
-                                      __builtin_amdgcn_perm(v[3][d], v[2][d], 0x07060302u)};
-                    frag[rt][2 * d] = __builtin_bit_cast(s16x4, lo);
-                    frag[rt][2 * d + 1] = __builtin_bit_cast(s16x4, hi);
-                }
-            }
+            };
+            finite = read_columns<RT>(w_cols, rows_of);
         }
         if (MODE != EX_PARTS || more) read(next, more ? tile1 : tile, more ? sub1 : sub, more ? count1 : count);
         sched_fence();
         f32x4 acc[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                acc[j] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(now.h[rt], frag[rt][j], acc[j], 0, 0, 0);
+        multiply_rows<RT>(now.h, w_cols, finite, acc);
+        if (!finite) cur = -1;  // read the adapter anew
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             u32x4 o;
