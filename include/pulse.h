@@ -684,7 +684,7 @@ int pulse_adamw_step(const pulse_adamw_segment *segs, int32_t nseg, const uint32
  * Sums are held in float32.  In the products with B and A, h and dh enter as the
  * sum of two BF16 (2^-16 of themselves is left out; y and dx keep 2^-8); in dA and
  * dB as float32 (the sum of three BF16).  y and dx are rounded once, after the
- * addition.
+ * addition.  Infinities and NaN are where the formulas have them.
  *
  * Layouts: x [T][ldx], y [T][ldy], dy, dx BF16 rows with any row stride that is
  * a multiple of 8 elements; a [S][R][K] and b [S][R][N] BF16 (b is stored with

@@ -283,6 +283,7 @@ __device__ __forceinline__ bf16x8 as_bf(const u32x4 &v) { return __builtin_bit_c
 // number for the second).
 struct Split {
     u32x2 top, rest;
+    f32x4 left;  // of which rest is the nearest BF16
 };
 
 __device__ __forceinline__ Split split4(const f32x4 &v) {
@@ -290,11 +291,10 @@ __device__ __forceinline__ Split split4(const f32x4 &v) {
     Split s;
     s.top = u32x2{cast_pair(__builtin_amdgcn_fmed3f(v[0], -kMost, kMost), __builtin_amdgcn_fmed3f(v[1], -kMost, kMost)),
                   cast_pair(__builtin_amdgcn_fmed3f(v[2], -kMost, kMost), __builtin_amdgcn_fmed3f(v[3], -kMost, kMost))};
-    float left[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        left[i] = v[i] - __uint_as_float((i & 1) ? (s.top[i >> 1] & 0xFFFF0000u) : (s.top[i >> 1] << 16));
-    s.rest = u32x2{cast_pair(left[0], left[1]), cast_pair(left[2], left[3])};
+        s.left[i] = v[i] - __uint_as_float((i & 1) ? (s.top[i >> 1] & 0xFFFF0000u) : (s.top[i >> 1] << 16));
+    s.rest = u32x2{cast_pair(s.left[0], s.left[1]), cast_pair(s.left[2], s.left[3])};
     return s;
 }
 
@@ -417,18 +417,16 @@ __device__ __forceinline__ void multiply_rows(const u32x4 *h, Columns<RT> &f, bo
 // h's four values of ranks r .. r+3 at one place, in its forms
 __device__ __forceinline__ void store_hidden(const LoraHidden &h, int64_t place, int64_t places, int rp, int r,
                                              const f32x4 &v) {
-    put_row(reinterpret_cast<u32x2 *>(h.rows), place, rp / 16, r / 16, r % 16 / 4, split4(v));
+    const Split s = split4(v);
+    put_row(reinterpret_cast<u32x2 *>(h.rows), place, rp / 16, r / 16, r % 16 / 4, s);
     if (h.part[0]) {
-        const uint32_t p0 = cast_pair(v[0], v[1]), p1 = cast_pair(v[2], v[3]);
+        const Split t = split4(s.left);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t top = (i < 2 ? p0 : p1) >> (16 * (i & 1)) & 0xFFFFu;
-            const float rest = v[i] - __uint_as_float(top << 16);
-            const uint32_t mid = cast_pair(rest, 0.0f);
             const int64_t at = (r + i) * places + place;
-            h.part[0][at] = (uint16_t)top;
-            h.part[1][at] = (uint16_t)mid;
-            h.part[2][at] = (uint16_t)cast_pair(rest - __uint_as_float(mid << 16), 0.0f);
+            h.part[0][at] = (uint16_t)(s.top[i >> 1] >> (16 * (i & 1)));
+            h.part[1][at] = (uint16_t)(t.top[i >> 1] >> (16 * (i & 1)));
+            h.part[2][at] = (uint16_t)(t.rest[i >> 1] >> (16 * (i & 1)));
         }
     }
 }
@@ -862,7 +860,9 @@ struct OuterRows {
 // same rows, three of four times from the nearest cache.  Matrix instruction: rows
 // = ranks, columns = columns of z, 32 places.  Lane c of the column axis holds eight
 // neighbouring columns of eight places, transposed in registers; instruction j takes
-// its column j, once for each part of u.  A chunk may cover several adapters and an
+// its column j, once for each part of u (rows that are not all finite: the lower parts
+// with ones for infinities; finding that out is 64 vector instructions of a step, which
+// waits for its rows).  A chunk may cover several adapters and an
 // adapter several chunks: a run that lies in one chunk goes straight to the output,
 // the others to the chunk's partial sums (0: continues an earlier chunk's run, 1:
 // begins here), which k_lora_outer_sum adds in order.
@@ -1039,14 +1039,28 @@ __global__ __launch_bounds__(FUSE ? 512 : 256, FUSE ? 1 : 2) void k_lora_outer(O
             for (int d = 0; d < 4; ++d)
                 zt[j][d] = __builtin_amdgcn_perm(now.z[2 * d + 1][j >> 1], now.z[2 * d][j >> 1],
                                                  (j & 1) ? 0x07060302u : 0x05040100u);
-#pragma unroll
-        for (int p = 2; p >= 0; --p)
+        const auto part = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                 for (int j = 0; j < W; ++j)
                     acc[rt][j] =
                         __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf(u[p][rt]), as_bf(zt[j]), acc[rt][j], 0, 0, 0);
+        };
+        part(0);
+        uint32_t most = 0;
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) most = most_of(most, zt[j][d]);
+        if (__ballot(not_finite(most))) {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+#pragma unroll
+                for (int d = 0; d < 4; ++d) zt[j][d] = ones_for_infinities(zt[j][d]);
+        }
+        part(1);
+        part(2);
         if constexpr (FUSE) {
             u32x4 *const st = s_stage[w];
             f32x4 sum[2][RT];
