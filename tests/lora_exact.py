@@ -42,3 +42,23 @@ def whole_rows(t, k, n, r, s, ids, seed=0):
     live = np.abs(want[ids >= 0])
     assert live.max() <= 256 and (live > 0).mean() > 0.5
     return x, a, b, y, want
+
+
+def whole_sums(t, cols, k, r, s, ids, seed=1):
+    """(z [t, cols], u [t, r], x [t, k], a [s, r, k], sum of u z^T per adapter): u = A x are
+    whole numbers of up to 24 bits, and a column of z is not zero for one token of an adapter."""
+    rng = np.random.default_rng(seed)
+    x = rng.integers(1, 128, (t, k)).astype(np.float64)
+    a = np.zeros((s, r, k))
+    a[:, :, 0] = rng.integers(64, 128, (s, r)) * 512.0
+    a[:, :, 1] = rng.integers(64, 128, (s, r))
+    z, u, want = np.zeros((t, cols)), np.zeros((t, r)), np.zeros((s, r, cols))
+    for i in set(ids.tolist()) - {-1}:
+        rows = np.flatnonzero(ids == i)
+        u[rows] = x[rows] @ a[i].T
+        mine = rows[:cols]
+        at = rng.permutation(cols)[:mine.size]
+        z[mine, at] = rng.choice([-1.0, 1.0], mine.size)
+        want[i] = u[rows].T @ z[rows]
+    assert np.abs(u).max() < 2 ** 24
+    return z, u, x, a, want

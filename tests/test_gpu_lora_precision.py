@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.lora_exact import spread_ids, whole_rows
+from tests.lora_exact import bf16_round, spread_ids, whole_rows, whole_sums
 
 try:
     import sparse_delta_codec_amd as pulse
@@ -73,3 +73,39 @@ def test_dx_takes_sixteen_bits_of_dh(t, k, n, r, s):
     ids = spread_ids(t, s)
     dy, b, a, dx, want = whole_rows(t, n, k, r, s, ids)
     assert np.array_equal(run(np.ones((t, k)), a, b, np.ones(s), ids, np.zeros((t, n)), dy, dx)[1], want)
+
+
+SUMS = [(1, 64, 136, 8, 1), (900, 264, 520, 24, 3), (300, 72, 136, 128, 2), (1500, 136, 264, 96, 3), (5, 40, 24, 8, 65),
+        (3000, 520, 200, 16, 1), (4200, 64, 8200, 16, 1), (4200, 64, 8200, 32, 900), (33_000, 40, 1032, 8, 700)]
+
+
+@pytest.mark.parametrize("t,k,n,r,s", SUMS)
+@pytest.mark.parametrize("drop", [1, 2])
+def test_the_sums_data_needs_all_three_parts(t, k, n, r, s, drop):
+    """On the CPU: without the second or the third part of h the sums are others."""
+    ids = spread_ids(t, s)
+    for cols in (k, n):
+        z, u, _, _, want = whole_sums(t, cols, n if cols == k else k, r, s, ids)
+        top = bf16_round(u)
+        mid = bf16_round(u - top)
+        low = bf16_round(u - top - mid)
+        assert np.array_equal(top + mid + low, u)
+        less = top + (0 if drop == 1 else mid) + (0 if drop == 2 else low)
+        got = np.zeros(want.shape)
+        for i in range(s):
+            rows = np.flatnonzero(ids == i)
+            got[i] = less[rows].T @ z[rows]
+        assert not np.array_equal(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,k,n,r,s", SUMS)
+def test_weight_gradients_take_all_bits_of_h_and_dh(t, k, n, r, s):
+    """Each column of z belongs to one token of an adapter, so a sum is one product: exact."""
+    ids = spread_ids(t, s)
+    dy, _, x, a, db = whole_sums(t, n, k, r, s, ids)
+    got = run(x, a, np.ones((s, r, n)), np.ones(s), ids, np.zeros((t, n)), dy, np.zeros((t, k)))
+    assert np.array_equal(got[3], db)
+    x, _, dy, b, da = whole_sums(t, k, n, r, s, ids)
+    got = run(x, np.ones((s, r, k)), b, np.ones(s), ids, np.zeros((t, n)), dy, np.zeros((t, k)))
+    assert np.array_equal(got[2], da)
