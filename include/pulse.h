@@ -647,6 +647,9 @@ typedef struct pulse_adamw_params {
  *   g  = grad * scale                       (scale = *d_scale, or 1)
  *   m' = b1 m + (1 - b1) g;  v' = b2 v + (1 - b2) (g g)
  *   p' = p (1 - lr' wd) - (lr' / (1 - b1^t)) (m' / (sqrt(v') / sqrt(1 - b2^t) + eps))
+ *      = p - ((lr' / (1 - b1^t)) (...) + p (lr' wd))  where |lr' wd| < 2^-23: below,
+ *        the float32 factor 1 - lr' wd may be off by a third of lr' wd or more
+ *        (above, by a fifth at most, from 2^-20 on by 3%)
  * with lr' = lr lr_mult and the constants (1 - b1, 1 / (1 - b1^t) and the like)
  * computed in float64 and rounded; then b' = bf16(p') as pulse_cast_diff casts.
  * 8-bit states: per block of 256 elements of a tensor, code = E4M3(x 448 / amax)

@@ -10,6 +10,9 @@
 //   m' = b1 m + (1 - b1) g          v' = b2 v + (1 - b2) (g g)
 //   u  = sqrt(v')
 //   p' = p (1 - lr wd) - (lr / (1 - b1^t)) (m' / (u / sqrt(1 - b2^t) + eps))
+//   with lr wd below 2^-23: p' = p - ((lr / (1 - b1^t)) (...) + p (lr wd)), for the
+//   float32 numbers below 1 are 2^-24 apart, and 1 - lr wd would be off by a third of
+//   lr wd or more: at lr = 2e-6 and wd = 0.01 it is 1 and nothing ever decays
 //   b' = bf16(p')                   patch: the elements where b' != b
 // States in 8 bits: m and u, in blocks of 256 elements of one tensor, as
 // E4M3 codes times amax / 448.  u rather than v is kept because a square root
@@ -63,6 +66,7 @@ struct AdamArgs {
 };
 
 constexpr int AW_BLOCK = 256;  // elements of a state block: one group of a wave
+constexpr float kLargest = 0x1.FFFFFEp127f;
 constexpr float kTinyBlock = 0x1p-96f;  // blocks below are stored as zero (448 / amax would overflow)
 
 // 32 well-mixed bits of x: xor-shifts and products with odd constants (the
@@ -157,7 +161,7 @@ __device__ __forceinline__ void store4v(void *p, int64_t e, int64_t n, V v) {
 // What one wave needs of its tensor.
 struct AdamTensor {
     AdamSeg s;
-    float scale, decay, size;
+    float scale, decay, rate, size;  // decay: the factor, or 1 and the rate apart
     uint32_t key;
 };
 
@@ -225,7 +229,10 @@ __device__ __forceinline__ uint32_t aw_chunk(const AdamArgs &a, const AdamTensor
             v4[k] = v4[k] * a.b2 + (gr * gr) * a.omb2;
             u4[k] = sqrtf(v4[k]);
             const float upd = m4[k] / (u4[k] * a.inv_sqrt_bc2 + a.eps);
-            p4[k] = __uint_as_float(pv[g][k]) * t.decay - upd * t.size;
+            const float p = __uint_as_float(pv[g][k]), step = upd * t.size;
+            // one of decay = 1 and rate = 0 holds: a zero added to the step changes nothing (a master that is
+            // infinite stays so, as the largest number stands for it in the product)
+            p4[k] = p * t.decay - (step + __builtin_amdgcn_fmed3f(p, -kLargest, kLargest) * t.rate);
             if constexpr (EIGHT) {
                 const uint32_t mb = __float_as_uint(m4[k]) & 0x7FFFFFFFu, ub = __float_as_uint(u4[k]) & 0x7FFFFFFFu;
                 mm = mb > mm ? mb : mm;
@@ -335,8 +342,10 @@ __global__ __launch_bounds__(CD_THREADS) void k_adamw(AdamArgs a) {
                     (all & 15u) == 0 && t.s.p && t.s.g && t.s.m && t.s.v && (!PATCH || t.s.b) &&
                     (!EIGHT || (t.s.m_scale && t.s.v_scale));
     t.scale = a.d_scale ? *a.d_scale : 1.0f;
-    const float lr = a.lr * t.s.lr_mult;
-    t.decay = 1.0f - lr * t.s.weight_decay;
+    const float lr = a.lr * t.s.lr_mult, rate = lr * t.s.weight_decay;
+    const bool apart = __builtin_fabsf(rate) < 0x1p-23f;
+    t.decay = apart ? 1.0f : 1.0f - rate;
+    t.rate = apart ? rate : 0.0f;
     t.size = lr * a.inv_bc1;
     t.key = aw_mix(a.seed + (s + 1u) * 0x9E3779B1u);
     const bool skip = !(__builtin_fabsf(t.scale) <= 3.402823466e38f);  // NaN or infinite: no step

@@ -49,3 +49,19 @@ def test_small_decays_add_up(bits, lr, wd):
     want = steps * lr * wd
     noise = 6 * 2.0 ** -24 * np.sqrt(2 * steps / n)
     assert abs(got - want) <= noise + want * (12 * steps * lr / (0.02 * np.sqrt(n)) + want + 2.0 ** -22)
+
+
+@pytest.mark.parametrize("lr,wd", [(2e-6, 0.01), (1e-3, 0.1), (1e-3, 0.0)])
+def test_extreme_masters(lr, wd):
+    """Infinite, NaN, zero and largest masters with and without a step of the gradient."""
+    values = torch.tensor([float("inf"), -float("inf"), float("nan"), 0.0, -0.0, 3.4e38, -3.4e38, 1.0], device="cuda")
+    p = values.repeat(2).contiguous()
+    g = torch.cat([torch.zeros(8, device="cuda"), torch.full((8,), 1e-3, device="cuda")])
+    m, v = torch.zeros(16, device="cuda"), torch.zeros(16, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pulse.pulse_adamw_step(pulse.AdamWTable([p], [g], [m], [v], weight_decay=wd), 1, lr, d_status=st)
+    got = p.cpu()
+    for half in (got[:8], got[8:]):
+        assert torch.equal(half[:2], values[:2].cpu()) and bool(torch.isnan(half[2]))
+        assert bool(torch.isfinite(half[3:]).all())
+    assert not got[3:5].any()  # zero masters without a gradient stay zero
