@@ -634,7 +634,8 @@ typedef struct pulse_adamw_segment {
 } pulse_adamw_segment;
 
 typedef struct pulse_adamw_params {
-    double lr, beta1, beta2, eps; /* lr >= 0, 0 <= beta < 1, eps > 0            */
+    double lr, beta1, beta2, eps; /* lr >= 0, 0 <= beta < 1, eps > 0, all so as
+                                     float32 too                                */
     int64_t step;                 /* t >= 1, for the bias corrections           */
     uint32_t seed;                /* 8-bit states: seed of the random rounding,
                                      another one every step                     */

@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <limits>
 #include <cstdint>
 
 extern "C" {
@@ -550,8 +551,11 @@ int pulse_adamw_step(const pulse_adamw_segment *segs, int32_t nseg, const uint32
                      size_t ws_bytes, hipStream_t stream) {
     if (!segs || !tile_seg || !params || !d_status || nseg < 1 || ntiles < nseg || patch_cap < 0) return PULSE_EINVAL;
     const pulse_adamw_params &q = *params;
-    if (!(q.lr >= 0.0) || !std::isfinite(q.lr) || !(q.beta1 >= 0.0 && q.beta1 < 1.0) ||
-        !(q.beta2 >= 0.0 && q.beta2 < 1.0) || !(q.eps > 0.0) || !std::isfinite(q.eps) || q.step < 1 ||
+    // also in float32, which the step computes with: an eps of 1e-50 would be zero there, and 0 / 0 where
+    // nothing ever moved
+    constexpr double kMost = std::numeric_limits<float>::max();
+    if (!(q.lr >= 0.0 && q.lr <= kMost) || !(q.beta1 >= 0.0 && (float)q.beta1 < 1.0f) ||
+        !(q.beta2 >= 0.0 && (float)q.beta2 < 1.0f) || !(q.eps <= kMost && (float)q.eps > 0.0f) || q.step < 1 ||
         (q.grad_bf16 != 0 && q.grad_bf16 != 1) || (q.state_bits != 32 && q.state_bits != 8) || q.reserved != 0)
         return PULSE_EINVAL;
     const bool patch = patch_idx || patch_val || seg_offsets;
