@@ -608,8 +608,8 @@ typedef struct pulse_grad_segment {
  *   grad_mul   a positive factor on every gradient (1 / the loss scale or the
  *              number of micro-batches); max_norm > 0, infinity for no clip.
  *   d_out      (device) float32[2]: scale, norm (written).
- *   ws         pulse_workspace_bytes(PULSE_OP_GRAD_NORM, ntiles, 0), zeroed
- *              before its first use (pulse_workspace_init).
+ *   ws         8-byte aligned, pulse_workspace_bytes(PULSE_OP_GRAD_NORM, ntiles, 0),
+ *              zeroed before its first use (pulse_workspace_init).
  * The result does not depend on the order in which workgroups run. */
 int pulse_grad_norm(const pulse_grad_segment *segs, int32_t nseg, const uint32_t *tile_seg, int64_t ntiles,
                     int32_t grad_bf16, double grad_mul, double max_norm, float *d_out, void *ws, size_t ws_bytes,

@@ -541,6 +541,7 @@ int pulse_grad_norm(const pulse_grad_segment *segs, int32_t nseg, const uint32_t
         return PULSE_EINVAL;
     if (!(grad_mul > 0.0) || !std::isfinite(grad_mul) || !(max_norm > 0.0)) return PULSE_EINVAL;
     if (ntiles > kMaxTiles) return PULSE_ERANGE;
+    if (reinterpret_cast<uintptr_t>(ws) & 7u) return PULSE_EALIGN;  // float64 sums, accessed as atomics
     if (!ws || ws_bytes < pulse_grad_norm_ws_bytes()) return PULSE_EWORKSPACE;
     return pulse_launch_grad_norm(segs, nseg, tile_seg, ntiles, grad_bf16, grad_mul, max_norm, d_out, ws, stream);
 }

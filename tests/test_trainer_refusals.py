@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from tests.test_abi import EINVAL, lib  # noqa: F401  (the library fixture)
+from tests.test_abi import EALIGN, EINVAL, lib  # noqa: F401  (the library fixture)
 from tests.test_oracle_adamw import I32, I64, Params, V, good
 
 
@@ -18,3 +18,12 @@ def test_adamw_refuses_what_float32_does_not_hold(lib, bad):  # noqa: F811
     f.argtypes = [V, I32, V, I64, V, V, V, V, I64, V, V, V, ctypes.c_size_t, V]
     al, q = V(0x10000), Params(**(good() | bad))
     assert f(al, 1, al, 1, ctypes.byref(q), None, None, None, 0, None, al, None, 0, None) == EINVAL
+
+
+def test_grad_norm_refuses_an_unaligned_workspace(lib):  # noqa: F811
+    """It holds float64 partial sums and a counter."""
+    f = lib.pulse_grad_norm
+    f.argtypes = [V, I32, V, I64, I32, ctypes.c_double, ctypes.c_double, V, V, ctypes.c_size_t, V]
+    al = V(0x10000)
+    for off in (1, 2, 4):
+        assert f(al, 1, al, 1, 0, 1.0, 1.0, al, V(0x10000 + off), 1 << 20, None) == EALIGN
