@@ -700,9 +700,36 @@ def _to_device(tab, tile_seg, device):
     return raw[:tab.nbytes].view(torch.int64).view(tab.shape), raw[tab.nbytes:].view(torch.int32)
 
 
+def _new_gradients(table, column, g, old, ns, stream):
+    """Checks gradients that take the place of a table's and writes their addresses into
+    its rows, behind what the stream holds and without waiting for it."""
+    dtype = torch.bfloat16 if table.grad_bf16 else torch.float32
+    if g is None or len(g) != len(ns):
+        raise ValueError(f"g must be a list of {len(ns)} tensors")
+    at = []
+    for i, (t, n) in enumerate(zip(g, ns)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or not t.is_contiguous():
+            raise ValueError(f"g[{i}] must be a contiguous GPU tensor of {dtype}")
+        if t.numel() != n:
+            raise ValueError(f"g[{i}] holds {t.numel()} elements, the table's {n}")
+        at.append(t.data_ptr())
+    if any(a % 16 for a in at):
+        raise ValueError("g: every tensor must be 16-byte aligned")
+    if at != table._g_at:
+        stream = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(stream):
+            host = torch.tensor(at, dtype=torch.int64, pin_memory=True)
+            table.segs[:, column].copy_(host, non_blocking=True)
+        for t in old:  # the stream may still have to read them
+            t.record_stream(stream)
+        table._g_at = at
+
+
 class GradTable:
     """Device tables of pulse_grad_norm for a list of gradients (GPU tensors, all
-    float32 or all bfloat16), prepared once and reused every step."""
+    float32 or all bfloat16), prepared once and reused every step.  The table holds the
+    gradients' addresses and keeps them alive: where a step's gradients are other tensors
+    (autograd's after zero_grad(set_to_none=True)), set_gradients names them."""
 
     def __init__(self, g, device="cuda"):
         import numpy as np
@@ -717,6 +744,12 @@ class GradTable:
         tab = np.array([[t.data_ptr(), t.numel(), t0] for t, t0 in zip(g, tile0)], np.int64)
         self.nseg = len(g)
         self.segs, self.tile_seg = _to_device(tab, tile_seg, device)
+        self._keep, self._ns, self._g_at = list(g), tab[:, 1].tolist(), tab[:, 0].tolist()
+
+    def set_gradients(self, g, stream=None):
+        """Other tensors of the same sizes and type from here on: calls enqueued on this
+        stream (None: the current one) from now on read them."""
+        _new_gradients(self, 0, g, self._keep, self._ns, stream)
         self._keep = list(g)
 
 
@@ -745,7 +778,10 @@ class AdamWTable:
                float32 [ceil(n/256)] block scales (zeroed codes and scales are the
                state before the first step)
       b        BF16/uint16 served views, or None
-    lr_mult and weight_decay: one number, or one per tensor."""
+    lr_mult and weight_decay: one number, or one per tensor.
+    The table holds the tensors' addresses and keeps them alive: where a step's gradients
+    are other tensors (autograd's after zero_grad(set_to_none=True)), set_gradients names
+    them."""
 
     def __init__(self, p, g, m, v, b=None, m_scale=None, v_scale=None, lr_mult=1.0, weight_decay=0.0, device="cuda"):
         import numpy as np
@@ -787,6 +823,13 @@ class AdamWTable:
         self.nseg = nseg
         self.segs, self.tile_seg = _to_device(tab, tile_seg, device)
         self._keep = [None if x is None else list(x) for x in (p, g, m, v, b, m_scale, v_scale)]
+        self._ns, self._g_at = [t.numel() for t in g], tab[:, 1].tolist()
+
+    def set_gradients(self, g, stream=None):
+        """Other tensors of the same sizes and type as gradients from here on: steps enqueued
+        on this stream (None: the current one) from now on read them."""
+        _new_gradients(self, 1, g, self._keep[1], self._ns, stream)
+        self._keep[1] = list(g)
 
 
 def pulse_adamw_step(table, step, lr, betas=(0.9, 0.999), eps=1e-8, d_scale=None, seed=0, d_status=None, ws=None,
