@@ -151,7 +151,14 @@ def _need(t, nbytes, name):
         raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, needs {nbytes}")
 
 
-_raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+try:
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _get_device
+except ImportError:  # another torch: the public way, where a call needs a stream at all
+    def _get_device():
+        return None
+
+    def _raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
 
 
 def _stream(stream):
