@@ -23,7 +23,7 @@
 // bits are a mix of the element's place, its tensor's number and the caller's
 // seed.  A u above zero gets at least the smallest code: a zero would divide
 // the next update by eps alone.
-#include "compact.hpp"
+#include "tiles.hpp"
 
 namespace pulse {
 
