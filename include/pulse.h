@@ -666,7 +666,12 @@ typedef struct pulse_adamw_params {
  *   patch_idx, patch_val, patch_cap, seg_offsets  the patch of the view's
  *              changed elements as pulse_cast_diff_segments writes it (b is
  *              both the old and the new view), or all NULL.
- *   d_status   PULSE_DS_CAPACITY, PULSE_DS_BADSEGMENT.
+ *   d_status   PULSE_DS_CAPACITY, PULSE_DS_BADSEGMENT.  After PULSE_DS_CAPACITY
+ *              the masters, states and views are those of the step and
+ *              seg_offsets counts every changed element, but the entries from
+ *              patch_cap on cannot be had any more (the old view is gone): the
+ *              receiver needs the whole views.  A buffer of as many entries as
+ *              the list has elements cannot overflow.
  *   ws         16-byte aligned, pulse_workspace_bytes(PULSE_OP_ADAMW, ntiles, 0)
  *              when a patch is asked for (it may hold anything before a call, and
  *              nothing is kept there after it); ignored otherwise. */
@@ -695,7 +700,8 @@ int pulse_adamw_step(const pulse_adamw_segment *segs, int32_t nseg, const uint32
  * the output axis last), adapters of a smaller rank padded with zero rows;
  * scales [S] float32.  K and N are multiples of 8 up to 2^24, R a multiple of 8
  * up to PULSE_LORA_MAX_RANK, S up to PULSE_LORA_MAX_ADAPTERS, T up to 2^24.
- * Every pointer but ids and scales is 16-byte aligned. */
+ * Every pointer but ids and scales is 16-byte aligned.  y, dx, da and db overlap
+ * no other buffer of their call. */
 #define PULSE_LORA_MAX_RANK 128
 #define PULSE_LORA_MAX_ADAPTERS 1024
 

@@ -843,7 +843,8 @@ def pulse_adamw_step(table, step, lr, betas=(0.9, 0.999), eps=1e-8, d_scale=None
                      patch_idx=None, patch_val=None, seg_offsets=None, stream=None):
     """One AdamW step over the table's tensors, with their served views and, when
     patch_idx, patch_val and seg_offsets are given, the patch of the views'
-    changed elements (as pulse_cast_diff_segments writes it)."""
+    changed elements (as pulse_cast_diff_segments writes it).  Where the patch does not
+    fit (PULSE_DS_CAPACITY), the receiver needs the whole views: the old ones are gone."""
     cap = 0
     if patch_idx is not None:
         cap = patch_idx.numel()
