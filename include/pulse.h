@@ -589,8 +589,9 @@ int pulse_apply_patch_segments(const pulse_view *views, int32_t nseg, const int3
  * The masters that the codec casts and compares come from an Adam step whose
  * size is about the learning rate ([Jiang talk] 07:17-10:37; [PULSE summary]
  * "Osservazione Centrale").  These calls run that step over a whole list of
- * tensors in one launch, with the tiling metadata of pulse_segment_tiles, and
- * write the served BF16 view and the sparse patch in the same pass.
+ * tensors, with the tiling metadata of pulse_segment_tiles: one launch for masters,
+ * states and the served BF16 view, and where asked a second one that writes the
+ * sparse patch from the changes that the first one found.
  *
  * One gradient of the list (device table of nseg entries, 24 bytes each). */
 typedef struct pulse_grad_segment {

@@ -18,8 +18,8 @@
 // E4M3 codes times amax / 448.  u rather than v is kept because a square root
 // halves the exponents: 18 binades of u are 36 of v.  Codes are rounded up or
 // down at random, with the chance that makes the expectation exact: at
-// b2 = 0.999 a step moves u by at most 0.05%, far below half a code's spacing
-// (3% to 6%), so rounding to nearest would never let a code follow.  The random
+// b2 = 0.999 a step lowers u by at most 0.05%, far below half a code's spacing
+// (3% to 6%), so rounding to nearest would never let a code come down.  The random
 // bits are a mix of the element's place, its tensor's number and the caller's
 // seed.  A u above zero gets at least the smallest code: a zero would divide
 // the next update by eps alone.

@@ -91,7 +91,7 @@ constexpr int64_t kMaxIndexed = 2147483647;    // int32 patch indices
 constexpr int64_t kMaxPayload = (1ll << 39) - 2; // look-back value field
 
 constexpr int64_t kMaxLora = 1 << 24;          // tokens and widths of the adapter calls
-constexpr int64_t kMaxTiles = 0x1FFFFFFF;  // list calls that cut a tile into four pieces count them in 31 bits
+constexpr int64_t kMaxTiles = 0x1FFFFFFF;  // of list calls: the pieces of a long list, two a tile at most, count in 31 bits
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -21,8 +21,10 @@
 //
 // A plan groups a batch's tokens by adapter: tiles of 64 places, each of one
 // adapter, whose places hold token numbers in ascending order (-1: empty).
-// Every kernel works on tiles, so a token is found by its place and sums over
-// tokens have one order whatever the launch.
+// Every kernel works on tiles, so a token is found by its place, and no atomic's
+// order reaches a result: the same call gives the same bits.  Another batch may not:
+// how many tiles a partial sum covers, and how many workgroups share the long axis,
+// go by the batch's size.
 #include "device.hpp"
 
 namespace pulse {
@@ -1337,11 +1339,12 @@ void shrink(const uint16_t *x, int64_t ldx, const uint16_t *a, const float *scal
     const int rt = (int)((R + 15) / 16);
     ShrinkArgs g = shrink_args(x, ldx, a, scales, plan, h, T, C, R, S);
     g.partial = partial;
-    // 32 places a workgroup, so that the adapter is read half as often, once that still fills the chip
-    // and few adapters end in the first half of a tile: 8192 x 5120 at rank 64 37 us with 16 places, 27
-    // with 32; at rank 16 or less the adapter weighs little (16384 x 4096 at rank 16: 29 us, 39)
+    // 32 places a workgroup, so that the adapter is read half as often, once that still makes a workgroup
+    // for each of the 256 compute units and few adapters end in the first half of a tile: 8192 x 5120 at
+    // rank 64 37 us with 16 places, 27 with 32; at rank 16 or less the adapter weighs little (16384 x 4096
+    // at rank 16: 29 us, 39)
     if (parts > 1) launch_shrink<1, SH_PARTS>(g, parts, rt, stream);
-    else if (rt >= 2 && T >= 8192 && T / S >= 128) launch_shrink<2, SH_WHOLE>(g, 1, rt, stream);
+    else if (rt >= 2 && T / 32 >= 256 && T / S >= 128) launch_shrink<2, SH_WHOLE>(g, 1, rt, stream);
     else launch_shrink<1, SH_WHOLE>(g, 1, rt, stream);
 }
 
