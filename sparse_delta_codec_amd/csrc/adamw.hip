@@ -325,8 +325,8 @@ __device__ __forceinline__ uint32_t pack_flags(uint32_t f) {
 // One workgroup of four waves per piece, E elements a wave (4096: a piece is a whole
 // tile; 1024 and 256: a quarter and a sixteenth).  With a patch each wave leaves its changed flags and
 // their number for k_adamw_patch.  Bound by HBM: 487.6M elements with 32-bit states,
-// 28 bytes each, 2.60 ms (5.2 TB/s, as a large copy); 218M with 8-bit states and the
-// flags, 20 bytes each, 0.70 ms (6.2 TB/s); 475K elements 4.4 us.
+// 28 bytes each, 2.56 ms (5.3 TB/s, as a large copy); 218M with 8-bit states and the
+// flags, 20 bytes each, 0.74 ms (5.9 TB/s); 475K elements 4.4 us.
 template <int E, bool BF16G, bool EIGHT, bool PATCH>
 __global__ __launch_bounds__(CD_THREADS) void k_adamw(AdamArgs a) {
     constexpr int kPerTile = CD_TILE / (4 * E), G = E < 1024 ? E / 256 : 4, CH = E / (256 * G);
@@ -387,8 +387,8 @@ __global__ __launch_bounds__(CD_THREADS) void k_adamw(AdamArgs a) {
 // picks its own bit by bit.  The step has no place in the patch to wait for:
 // placing a piece's entries by a ticket and a look-back within the step itself cost
 // 23 ns a piece, one after the other, and 41 us before the first 1800 pieces had
-// begun (5.2M elements: 57 us, with this kernel 29 + 6; 218M with 8-bit states: 895
-// us, 700 + 48).  Ranked with ballots, four for every 256 elements as in the codec's
+// begun (5.2M elements: 57 us, with this kernel 28 + 6; 218M with 8-bit states: 895
+// us, 741 + 47).  Ranked with ballots, four for every 256 elements as in the codec's
 // passes, it was bound by its instructions: 85 to 119 us.
 template <int E>
 __global__ __launch_bounds__(CD_THREADS) void k_adamw_patch(AdamArgs a) {

@@ -477,8 +477,8 @@ constexpr int SH_WAVES = 8;
 // them, 64 bytes of 16 rows at once, rows came in at 10 to 15 bytes a clock and
 // compute unit; 256 bytes of 4 rows, turned round in LDS, are not held back.
 // The rows of the next step are read while these are multiplied.  Measured:
-// 8192 x 5120 at rank 64 26 us (3.2 TB/s of x), 16384 x 4096 at rank 16 29 us
-// (4.6); of the reads of x alone, in any order, 16384 x 4096 took 25 to 34 us.
+// 8192 x 5120 at rank 64 27 us (3.1 TB/s of x), 16384 x 4096 at rank 16 30 us
+// (4.5); of the reads of x alone, in any order, 16384 x 4096 took 25 to 34 us.
 // SH_APPLY serves small batches, which wait for launches and round trips more
 // than for bytes: gridDim.y workgroups each make the same h, keep it in LDS and go
 // through their share of y's columns as k_lora_expand does; a wave's first rows and
@@ -710,8 +710,8 @@ struct ExpandRows {
 // so the body has no branch around either: an empty place stands for the first
 // of its 16 and a lane past the last column for the wave's first piece, and both
 // write again what that one writes.  Bound by reading and writing y: 8192 x 27648 at
-// rank 64 161 us (5.6 TB/s; with the branches 206), 16384 x 14336 at rank 16 183 us
-// (5.1; a large copy 5.2).
+// rank 64 170 us (5.3 TB/s; with one part of h 161, with the branches 206 then), 16384 x
+// 14336 at rank 16 184 us (5.1; a large copy 5.2).
 template <int RT, int MODE>
 __global__ __launch_bounds__(256, RT <= 2 ? 3 : (RT <= 4 ? 2 : 1)) void k_lora_expand(ExpandArgs g) {
     const int w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), c16 = l & 15, q = l >> 4;
@@ -868,11 +868,11 @@ struct OuterRows {
 // adapter several chunks: a run that lies in one chunk goes straight to the output,
 // the others to the chunk's partial sums (0: continues an earlier chunk's run, 1:
 // begins here), which k_lora_outer_sum adds in order.
-// 16384 x 4096 at rank 16: 29 us, 4.6 TB/s.
+// 16384 x 4096 at rank 16: 31 us, 4.3 TB/s.
 // FUSE: z is dy, and the same read serves dh = s B dy: the rows go through LDS
 // into the order that shrink multiplies them in, the eight waves' sums over 128
 // columns each are added there, and k_lora_join adds the workgroups'.  16384 x 14336
-// at rank 16: 102 us, 4.6 TB/s, and 6 us for the join (dy read twice: 137 + 105 us);
+// at rank 16: 106 us, 4.4 TB/s, and 5.5 us for the join (dy read twice: 137 + 105 us);
 // leaving out either product changes nothing, it waits for the rows.
 template <int RT, bool FUSE>
 __global__ __launch_bounds__(FUSE ? 512 : 256, FUSE ? 1 : 2) void k_lora_outer(OuterArgs g) {
@@ -1167,7 +1167,11 @@ int lora_chunk(int64_t T, int64_t S, int64_t R, int64_t waves) {
 // The backward pass reads dy once, for dh and dB together, where that saves more
 // than it costs: from 64 MB of dy on (below, dy comes from the caches the second
 // time and the launch more is felt), and to rank 32 (two rank tiles: the sums of
-// more leave no registers to read ahead).
+// more leave no registers to read ahead).  Backward with it and without, ranks 16 and
+// 32: 16384 tokens, 4096 to 14336, 204 us and 303, 236 and 345; 4096 tokens of 4
+// adapters, 14336 to 8200, 101 and 125, 129 and 152; 2100 tokens, 4096 to 16392, 56 and
+// 63, 69 and 81; at 64 MB, 8192 tokens, 4096 to 4096, 79 and 77, 96 and 94 for one
+// adapter, 79 and 84, 106 and 105 for 16.
 bool lora_fused(int64_t T, int64_t N, int64_t R) { return R <= 32 && T * N >= (int64_t)1 << 25; }
 
 int64_t lora_fused_groups(int64_t N) { return (N + 1023) / 1024; }
