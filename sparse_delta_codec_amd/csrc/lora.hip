@@ -1359,6 +1359,10 @@ void shrink(const uint16_t *x, int64_t ldx, const uint16_t *a, const float *scal
 // 69 MB, 16.4 us against 14.6; 64 tokens, 4096 to 4096, rank 16: 18 MB, 9.1 us
 // against 9.8 and one launch less), and where h's long axis can be shared and one
 // workgroup would read long (4 tokens, 4096 to 4096, rank 128: 1 MB, 22 us against 14).
+// Both ways at 190 sizes (1 to 600 tokens of 8 to 64 adapters, ranks 8 to 128, five pairs
+// of widths): the rule's choice is within an eighth of the better one but for 17, the
+// largest of them 14336 to 4096 at rank 8 (224 KB; 12 us against 9, 600 tokens 23 against
+// 14) and 64 adapters of rank 128 (4096 to 14336, two launches: 51 us against 41).
 int64_t lora_apply_groups(int64_t T, int64_t S, int64_t C, int64_t N, int64_t R, bool shared) {
     const int64_t groups = lora_max_groups(T, S), waves = SH_WAVES;
     if (groups > 256 || (shared && R * C * 2 > 384 << 10)) return 0;
