@@ -725,6 +725,8 @@ def _new_gradients(table, column, g, old, ns, stream):
     if at != table._g_at:
         stream = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():  # a replay would copy from host memory long reused
+                raise RuntimeError("set_gradients: other gradients cannot be named while a graph is captured")
             host = torch.tensor(at, dtype=torch.int64, pin_memory=True)
             table.segs[:, column].copy_(host, non_blocking=True)
         for t in old:  # the stream may still have to read them
@@ -834,7 +836,8 @@ class AdamWTable:
 
     def set_gradients(self, g, stream=None):
         """Other tensors of the same sizes and type as gradients from here on: steps enqueued
-        on this stream (None: the current one) from now on read them."""
+        on this stream (None: the current one) from now on read them, replays of a captured
+        step too.  Not within a capture."""
         _new_gradients(self, 1, g, self._keep[1], self._ns, stream)
         self._keep[1] = list(g)
 

@@ -65,3 +65,24 @@ def test_set_gradients_refuses_others():
             with pytest.raises(ValueError):
                 t.set_gradients(bad)
     assert torch.equal(table.segs, before[0]) and torch.equal(norms.segs, before[1])
+
+
+def test_set_gradients_refuses_a_capture():
+    """The same gradients are fine there, for nothing is written; others are refused, and the
+    table stays as it was."""
+    p, m, v, g = lists(torch.float32)
+    table, x = pulse.AdamWTable(p, g, m, v), torch.zeros(4, device="cuda")
+    before = table.segs.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.add_(1)
+        table.set_gradients(g)
+        with pytest.raises(RuntimeError):
+            table.set_gradients(v)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(table.segs, before) and bool((x == 1).all())
+    table.set_gradients(v)
+    torch.cuda.synchronize()
+    assert table.segs[:, 1].tolist() == [t.data_ptr() for t in v]
