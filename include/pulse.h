@@ -746,6 +746,108 @@ int pulse_lora_backward(const uint16_t *x, int64_t ldx, const uint16_t *dy, int6
                         int64_t h_bytes, uint16_t *dx, int64_t lddx, float *da, float *db, int32_t accumulate,
                         void *ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---- the sampler's layer over the FP8 view --------------------------------------
+ * What an FP8 sampler does with the codes and scales that the receiver keeps
+ * ([Perplexity] "Potok zadan": the weights are quantised for FP8 inference): the
+ * norm in front of a projection with its output in E4M3, the products with weights
+ * in 128 x 128 blocks, the activation between them, and an expert layer for a few
+ * tokens.  A trainer of adapters over that frozen view has the gradients of the norm
+ * and of the products' input too.
+ *
+ * Quantised rows: codes [T][cols] E4M3 and scales [T][ceil(cols/128)] float32, one for
+ * each group of 128 columns of a row.  With amax = max |x| of the group, s =
+ * fl32(amax / 448), or 1 where amax < 2^-96 (the codes are zeros then), and code =
+ * E4M3(fl32(x / s)), to nearest, ties to even.  A group that holds an Inf or a NaN has an
+ * Inf or NaN as its scale, and none of its codes times it is a number.
+ *
+ * x, y and the like are BF16 rows with any row stride that is a multiple of 8 elements;
+ * T is up to 2^24.  Outputs overlap no other buffer of their call. */
+
+/* y = s rstd weight with rstd = 1 / sqrt(mean(s^2) + eps) of each row, s = x, or with a
+ * residual s = bf16(x + residual), which is written back to it.  Sums are held in float32
+ * (squares past its range make a row of zeros or NaN, as the formula does there).
+ *   x         [T][ldx] (read); cols a multiple of 8 up to 16384.
+ *   weight    [cols] BF16.      eps  > 0, as float32 too.
+ *   residual  [T][ldr], updated, or NULL.
+ *   y         [T][ldy] (written), or NULL with codes given.
+ *   codes, scales  y as quantised rows, from its float32 values (written), or both NULL.
+ *   rstd      [T] float32 for the backward pass (written), or NULL. */
+int pulse_rms_norm(const uint16_t *x, int64_t ldx, const uint16_t *weight, double eps, uint16_t *residual,
+                   int64_t ldr, uint16_t *y, int64_t ldy, uint8_t *codes, float *scales, float *rstd,
+                   int64_t n_tokens, int64_t cols, hipStream_t stream);
+
+/* The gradients of pulse_rms_norm's y:
+ *   dx = rstd (dy weight - s rstd mean(dy weight s rstd)) + dres,  dweight = sum over rows of dy s rstd
+ *   s       [T][lds] the rows that were normalised: the updated residual, or x.
+ *   rstd    as the forward pass wrote it.
+ *   dres    [T][lddres] the gradient that reaches s by the residual's way, or NULL.
+ *   dx      [T][lddx] BF16 (written; the gradient of x and of the residual), or NULL.
+ *           It may be dy or dres.
+ *   dweight [cols] float32: written, or with accumulate = 1 added to.
+ *   ws      pulse_rms_norm_ws_bytes(T, cols); it may hold anything before a call. */
+int64_t pulse_rms_norm_ws_bytes(int64_t n_tokens, int64_t cols);
+int pulse_rms_norm_backward(const uint16_t *s, int64_t lds, const uint16_t *weight, const float *rstd,
+                            const uint16_t *dy, int64_t lddy, const uint16_t *dres, int64_t lddres, uint16_t *dx,
+                            int64_t lddx, float *dweight, int32_t accumulate, int64_t n_tokens, int64_t cols,
+                            void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Rows quantised as above: x [T][ldx], cols a multiple of 8 up to 2^24; with glu = 1 x is
+ * [gate, up] of 2 cols columns and the values are gate / (1 + e^-gate) * up, in float32. */
+int fp8_group_quant(const uint16_t *x, int64_t ldx, int64_t n_tokens, int64_t cols, int32_t glu, uint8_t *codes,
+                    float *scales, hipStream_t stream);
+
+/* Quantised rows times weights in 128 x 128 blocks (fp8_block_quant's w [n][k] and scales
+ * [ceil(n/128)][ceil(k/128)]), each block's sum multiplied by both scales in float32:
+ *   PULSE_GEMM_NT  y [m][n] = x [m][k] w^T + bias: a projection; k a multiple of 16.
+ *   PULSE_GEMM_NN  y [m][k] = x [m][n] w: the gradient of a projection's input, from that of
+ *                  its output; n and k multiples of 16.
+ * n and k up to 2^22.  y [m][ldy] is rounded to BF16 once; ldy >= its columns, any.  The matrix
+ * instructions add up eight neighbouring products at a time, each cut to a multiple of about
+ * 2^-13 of their largest, and everything else is added in float32.
+ *   x, x_scales  quantised rows (dense: row stride k, or n).
+ *   bias   [n] BF16 (PULSE_GEMM_NT, else ignored), or NULL.
+ *   ws     fp8_block_gemm_ws_bytes(m, n, k, form); it may hold anything before a call. */
+#define PULSE_GEMM_NT 0
+#define PULSE_GEMM_NN 1
+int64_t fp8_block_gemm_ws_bytes(int64_t m, int64_t n, int64_t k, int32_t form);
+int fp8_block_gemm(const uint8_t *x, const float *x_scales, const uint8_t *w, const float *w_scales,
+                   const uint16_t *bias, int32_t form, int64_t m, int64_t n, int64_t k, uint16_t *y, int64_t ldy,
+                   void *ws, size_t ws_bytes, hipStream_t stream);
+
+#define PULSE_MOE_MAX_EXPERTS 1024
+#define PULSE_MOE_MAX_TOP_K 32
+#define PULSE_MOE_MAX_TOKENS 1024 /* of pulse_moe_forward, with n_tokens * top_k: */
+#define PULSE_MOE_MAX_PAIRS 8192
+
+/* A token's experts from its logits [T][ld]: the top_k largest, in descending order (equal
+ * ones by the lowest index; a NaN counts as larger than all), and their softmax times
+ * scale, over the chosen ones or, with over_all = 1, over all experts.  An expert whose
+ * logit is -Inf is not chosen: its place has id -1 and weight 0.
+ *   ids, weights  [T][top_k] int32 and float32 (written). */
+int pulse_moe_route(const float *logits, int64_t ld, int64_t n_tokens, int64_t experts, int64_t top_k,
+                    int32_t over_all, double scale, int32_t *ids, float *weights, hipStream_t stream);
+
+/* y[t] = sum over a token's choices j, e = ids[t][j], of weights[t][j] down_e h,
+ * h = silu(gate_e x[t]) * (up_e x[t]), for a few tokens: the time is that of reading the
+ * chosen experts' weights.  x enters as BF16, h as the sum of two BF16 (2^-16 of itself is
+ * left out), weights as code times scale; sums are held in float32 and y is rounded once.
+ *   x       [T][ldx] BF16, ldx up to 2^20.   hidden and inter multiples of 16 up to 65536.
+ *   ids     [T][top_k] int32 (any expert any number of times; -1 for none): y of a token
+ *           without an expert is zero.  weights [T][top_k] float32.
+ *   up      [experts][2 inter][hidden] codes, gate's rows first, and scales
+ *           [experts][ceil(2 inter / 128)][ceil(hidden / 128)]; down [experts][hidden][inter]
+ *           and scales [experts][ceil(hidden / 128)][ceil(inter / 128)]: fp8_block_quant's
+ *           layout for a batch of experts.
+ *   y       [T][ldy] BF16 (written).
+ *   d_status  PULSE_DS_BADINDEX when an id is neither -1 nor in [0, experts) (that choice
+ *           is left out).
+ *   ws      pulse_moe_ws_bytes; it may hold anything before a call. */
+int64_t pulse_moe_ws_bytes(int64_t n_tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k);
+int pulse_moe_forward(const uint16_t *x, int64_t ldx, const int32_t *ids, const float *weights,
+                      const uint8_t *up, const float *up_scales, const uint8_t *down, const float *down_scales,
+                      int64_t n_tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, uint16_t *y,
+                      int64_t ldy, uint32_t *d_status, void *ws, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

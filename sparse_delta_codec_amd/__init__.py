@@ -28,6 +28,9 @@ __all__ = [
     "PULSE_OP_GRAD_NORM", "PULSE_OP_ADAMW", "PULSE_ADAMW_BLOCK", "GradTable", "AdamWTable", "pulse_grad_norm",
     "pulse_adamw_step", "PULSE_LORA_MAX_RANK", "PULSE_LORA_MAX_ADAPTERS", "LoraPlan", "lora_workspace", "lora_hidden",
     "pulse_lora_plan", "pulse_lora_forward", "pulse_lora_backward",
+    "pulse_rms_norm", "pulse_rms_norm_backward", "rms_norm_workspace", "fp8_group_quant", "fp8_block_gemm",
+    "fp8_gemm_workspace", "PULSE_GEMM_NT", "PULSE_GEMM_NN", "pulse_moe_route", "pulse_moe_forward", "moe_workspace",
+    "PULSE_MOE_MAX_EXPERTS", "PULSE_MOE_MAX_TOP_K", "PULSE_MOE_MAX_TOKENS", "PULSE_MOE_MAX_PAIRS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -108,7 +111,21 @@ _lib.pulse_lora_forward.argtypes = [_P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, 
                                     _P, _SZ, _P]
 _lib.pulse_lora_backward.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I32, _P, _I64,
                                      _P, _I64, _P, _P, _I32, _P, _SZ, _P]
-for _f in ("pulse_lora_plan", "pulse_lora_forward", "pulse_lora_backward", "pulse_grad_norm", "pulse_adamw_step", "pulse_cast_diff_segments", "pulse_apply_patch_segments", "patch_pack", "patch_unpack",
+_lib.pulse_rms_norm_ws_bytes.argtypes = [_I64, _I64]
+_lib.fp8_block_gemm_ws_bytes.argtypes = [_I64, _I64, _I64, _I32]
+_lib.pulse_moe_ws_bytes.argtypes = [_I64, _I64, _I64, _I64, _I64]
+for _f in ("pulse_rms_norm_ws_bytes", "fp8_block_gemm_ws_bytes", "pulse_moe_ws_bytes"):
+    getattr(_lib, _f).restype = _I64
+_lib.pulse_rms_norm.argtypes = [_P, _I64, _P, ctypes.c_double, _P, _I64, _P, _I64, _P, _P, _P, _I64, _I64, _P]
+_lib.pulse_rms_norm_backward.argtypes = [_P, _I64, _P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _I64, _I64, _P, _SZ,
+                                         _P]
+_lib.fp8_group_quant.argtypes = [_P, _I64, _I64, _I64, _I32, _P, _P, _P]
+_lib.fp8_block_gemm.argtypes = [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _P, _I64, _P, _SZ, _P]
+_lib.pulse_moe_route.argtypes = [_P, _I64, _I64, _I64, _I64, _I32, ctypes.c_double, _P, _P, _P]
+_lib.pulse_moe_forward.argtypes = [_P, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _SZ,
+                                   _P]
+for _f in ("pulse_rms_norm", "pulse_rms_norm_backward", "fp8_group_quant", "fp8_block_gemm", "pulse_moe_route",
+           "pulse_moe_forward", "pulse_lora_plan", "pulse_lora_forward", "pulse_lora_backward", "pulse_grad_norm", "pulse_adamw_step", "pulse_cast_diff_segments", "pulse_apply_patch_segments", "patch_pack", "patch_unpack",
            "pulse_workspace_init", "pulse_cast_diff", "pulse_compact", "pulse_apply_patch",
            "xor_mask_apply", "lz4_encode_blocks", "lz4_decode_blocks", "fp8_block_quant",
            "fp8_view_delta", "fp8_view_apply", "pulse_loco_gate", "pulse_loco_accumulate",
@@ -991,3 +1008,187 @@ def pulse_lora_backward(x, dy, a, b, scales, plan, h, dx, da, db, ws, accumulate
         px, ldx, pdy, lddy, pa, pb, ps, plan.pointer, plan.nbytes, tokens, k, n, r, plan.n_adapters,
         _dev(h, "h", torch.uint8), h.numel(), pdx, lddx, _dev(da, "da", torch.float32),
         _dev(db, "db", torch.float32), int(accumulate), wsp, wsb, _stream(stream)), "pulse_lora_backward")
+
+
+# ---- the sampler's layer over the FP8 view ----------------------------------------------
+PULSE_GEMM_NT = 0
+PULSE_GEMM_NN = 1
+PULSE_MOE_MAX_EXPERTS = 1024
+PULSE_MOE_MAX_TOP_K = 32
+PULSE_MOE_MAX_TOKENS = 1024
+PULSE_MOE_MAX_PAIRS = 8192
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _scratch(nbytes, what, device):
+    nbytes = _size(nbytes, what)
+    return torch.empty((max(nbytes, 16) + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def _dense(t, shape, dtypes, name):
+    """The data pointer of a contiguous GPU tensor of this shape and one of these types."""
+    try:
+        if t.shape == shape and t.is_cuda and t.dtype in dtypes and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtypes}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+_F32, _I32T = (torch.float32,), (torch.int32,)
+
+
+def _launch_stream(t, stream):
+    """The handle of the stream to launch on; the operands' device must be the stream's (the
+    current one's)."""
+    device = t.get_device()
+    if stream is None:
+        current = _get_device()
+        if current is not None and current != device:
+            raise ValueError(f"operands are on GPU {device}, the current one is {current}")
+        return _raw_stream(device)
+    if stream.device_index != device:
+        raise ValueError(f"operands are on GPU {device}, the stream is of {stream.device_index}")
+    return stream.cuda_stream
+
+
+def _same_device(first, *others):
+    device = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"operands are on GPUs {device} and {t.get_device()}")
+
+
+def rms_norm_workspace(n_tokens, cols, device="cuda"):
+    """A workspace for pulse_rms_norm_backward of up to n_tokens rows."""
+    return _scratch(_lib.pulse_rms_norm_ws_bytes(n_tokens, cols), "pulse_rms_norm_ws_bytes", device)
+
+
+def pulse_rms_norm(x, weight, eps=1e-6, residual=None, y=None, codes=None, scales=None, rstd=None, stream=None):
+    """Root-mean-square norm of x [tokens, cols] BF16, with a residual of its rounded sum with
+    x, which the residual then holds.  The output goes to y (BF16), to codes [tokens, cols]
+    and scales [tokens, ceil(cols / 128)] (E4M3), or to both; rstd [tokens] keeps what the backward
+    pass needs."""
+    t, n = x.shape
+    px, ldx = _rows(x, t, n, "x")
+    pw = _dense(weight, (n,), _U16, "weight")
+    pr, ldr = (None, 0) if residual is None else _rows(residual, t, n, "residual")
+    py, ldy = (None, 0) if y is None else _rows(y, t, n, "y")
+    pc = None if codes is None else _dense(codes, (t, n), _CODES, "codes")
+    ps = None if scales is None else _dense(scales, (t, -(-n // 128)), _F32, "scales")
+    pd = None if rstd is None else _dense(rstd, (t,), _F32, "rstd")
+    _same_device(x, weight, residual, y, codes, scales, rstd)
+    rc = _lib.pulse_rms_norm(px, ldx, pw, eps, pr, ldr, py, ldy, pc, ps, pd, t, n, _launch_stream(x, stream))
+    if rc:
+        _check(rc, "pulse_rms_norm")
+
+
+def pulse_rms_norm_backward(s, weight, rstd, dy, dx, dweight, ws, dres=None, accumulate=False, stream=None):
+    """The gradients of pulse_rms_norm's y: s [tokens, cols] are the rows that were normalised
+    (the updated residual, or x); dx (None: not wanted) is that of x and of the residual, dres
+    what reaches it by the residual's way; dweight [cols] float32 is written or, with accumulate,
+    added to."""
+    t, n = s.shape
+    p, lds = _rows(s, t, n, "s")
+    pdy, lddy = _rows(dy, t, n, "dy")
+    pdr, lddr = (None, 0) if dres is None else _rows(dres, t, n, "dres")
+    pdx, lddx = (None, 0) if dx is None else _rows(dx, t, n, "dx")
+    pw, pd = _dense(weight, (n,), _U16, "weight"), _dense(rstd, (t,), _F32, "rstd")
+    pdw = _dense(dweight, (n,), _F32, "dweight")
+    wsp, wsb = _ws(ws)
+    _same_device(s, weight, rstd, dy, dx, dweight, ws, dres)
+    rc = _lib.pulse_rms_norm_backward(p, lds, pw, pd, pdy, lddy, pdr, lddr, pdx, lddx, pdw, int(accumulate), t, n, wsp,
+                                      wsb, _launch_stream(s, stream))
+    if rc:
+        _check(rc, "pulse_rms_norm_backward")
+
+
+def fp8_group_quant(x, codes, scales, glu=False, stream=None):
+    """E4M3 codes [tokens, cols] of x [tokens, cols] BF16 and their scales for each 128 columns
+    of a row; with glu of silu(gate) * up, x = [gate, up]."""
+    t, n = codes.shape
+    px, ldx = _rows(x, t, 2 * n if glu else n, "x")
+    pc, ps = _dense(codes, (t, n), _CODES, "codes"), _dense(scales, (t, -(-n // 128)), _F32, "scales")
+    _same_device(x, codes, scales)
+    rc = _lib.fp8_group_quant(px, ldx, t, n, int(glu), pc, ps, _launch_stream(x, stream))
+    if rc:
+        _check(rc, "fp8_group_quant")
+
+
+_FORMS = {"nt": PULSE_GEMM_NT, "nn": PULSE_GEMM_NN}
+
+
+def fp8_gemm_workspace(m, n, k, form="nt", device="cuda"):
+    """A workspace for fp8_block_gemm of m rows with weights [n, k]."""
+    return _scratch(_lib.fp8_block_gemm_ws_bytes(m, n, k, _FORMS[form]), "fp8_block_gemm_ws_bytes", device)
+
+
+def fp8_block_gemm(x, x_scales, w, w_scales, y, ws=None, bias=None, form="nt", stream=None):
+    """y (BF16) = x w^T + bias ("nt": x [m, k], y [m, n]) or x w ("nn": x [m, n], y [m, k]): x E4M3 codes
+    with a scale for each 128 columns of a row, w [n, k] codes with one for each 128 x 128 block."""
+    nn = _FORMS[form]
+    n, k = w.shape
+    m, (inner, out) = x.shape[0], ((n, k) if nn else (k, n))
+    if nn and bias is not None:
+        raise ValueError("a bias goes with form 'nt'")
+    px, psx = _dense(x, (m, inner), _CODES, "x"), _dense(x_scales, (m, -(-inner // 128)), _F32, "x_scales")
+    pw = _dense(w, (n, k), _CODES, "w")
+    psw = _dense(w_scales, (-(-n // 128), -(-k // 128)), _F32, "w_scales")
+    py, ldy = _rows(y, m, out, "y")
+    pb = None if bias is None else _dense(bias, (n,), _U16, "bias")
+    wsp, wsb = _ws(ws)
+    _same_device(x, x_scales, w, w_scales, y, ws, bias)
+    rc = _lib.fp8_block_gemm(px, psx, pw, psw, pb, nn, m, n, k, py, ldy, wsp, wsb, _launch_stream(x, stream))
+    if rc:
+        _check(rc, "fp8_block_gemm")
+
+
+def pulse_moe_route(logits, ids, weights, over_all=False, scale=1.0, stream=None):
+    """Each token's experts from its logits [tokens, experts] float32: ids [tokens, top_k] int32 by
+    descending logit (-1 where only logits of -inf are left) and weights float32, the softmax over
+    the chosen ones (over_all: over all experts) times scale."""
+    t, e = logits.shape
+    k = ids.shape[1]
+    if not logits.is_cuda or logits.dtype is not torch.float32 or (logits.stride(1) != 1 and e > 1):
+        raise ValueError("logits must be a float32 GPU tensor with contiguous rows")
+    pi, pw = _dense(ids, (t, k), _I32T, "ids"), _dense(weights, (t, k), _F32, "weights")
+    _same_device(logits, ids, weights)
+    rc = _lib.pulse_moe_route(logits.data_ptr(), logits.stride(0) if t > 1 else e, t, e, k, int(over_all), scale, pi, pw,
+                              _launch_stream(logits, stream))
+    if rc:
+        _check(rc, "pulse_moe_route")
+
+
+def moe_workspace(n_tokens, hidden, inter, experts, top_k, device="cuda"):
+    """A workspace for pulse_moe_forward of up to n_tokens tokens."""
+    return _scratch(_lib.pulse_moe_ws_bytes(n_tokens, hidden, inter, experts, top_k), "pulse_moe_ws_bytes", device)
+
+
+def pulse_moe_forward(x, ids, weights, up, up_scales, down, down_scales, y, d_status, ws, stream=None):
+    """y [tokens, hidden] = the chosen experts' outputs for x, by weights [tokens, top_k]: up [experts,
+    2 inter, hidden] holds gate's rows, then up's; down [experts, hidden, inter]; both E4M3 codes with a
+    scale for each 128 x 128 block of an expert."""
+    t, h = x.shape
+    e, hh, i = down.shape
+    k = ids.shape[1]
+    px, ldx = _rows(x, t, h, "x")
+    py, ldy = _rows(y, t, h, "y")
+    pi, pp = _dense(ids, (t, k), _I32T, "ids"), _dense(weights, (t, k), _F32, "weights")
+    pu, pd = _dense(up, (e, 2 * i, h), _CODES, "up"), _dense(down, (e, h, i), _CODES, "down")
+    psu = _dense(up_scales, (e, -(-2 * i // 128), -(-h // 128)), _F32, "up_scales")
+    psd = _dense(down_scales, (e, -(-h // 128), -(-i // 128)), _F32, "down_scales")
+    wsp, wsb = _ws(ws)
+    _need(d_status, 4, "d_status")
+    st = _dev(d_status, "d_status", torch.int32)
+    _same_device(x, ids, weights, up, up_scales, down, down_scales, y, d_status, ws)
+    rc = _lib.pulse_moe_forward(px, ldx, pi, pp, pu, psu, pd, psd, t, h, i, e, k, py, ldy, st, wsp, wsb,
+                                _launch_stream(x, stream))
+    if rc:
+        _check(rc, "pulse_moe_forward")

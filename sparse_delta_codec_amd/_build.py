@@ -16,7 +16,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["capi.cpp", "util.hip", "cast_diff.hip", "apply.hip", "lz4_encode.hip", "lz4_decode.hip",
            "fp8_quant.hip", "delta_compact.hip",
-           "patch_pack.hip", "adamw.hip", "lora.hip"]
+           "patch_pack.hip", "adamw.hip", "lora.hip", "norm.hip", "fp8_gemm.hip", "moe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

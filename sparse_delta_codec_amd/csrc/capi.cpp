@@ -83,6 +83,22 @@ int pulse_launch_lora_backward(const uint16_t *, int64_t, const uint16_t *, int6
                                const uint16_t *, const float *, const void *, int64_t, int64_t, int64_t, int64_t,
                                int64_t, const void *, uint16_t *, int64_t, float *, float *, int32_t, void *,
                                hipStream_t);
+int64_t pulse_rms_norm_ws_size(int64_t rows, int64_t cols);
+int pulse_launch_rms_norm(const uint16_t *, int64_t, const uint16_t *, double, uint16_t *, int64_t, uint16_t *, int64_t,
+                          uint8_t *, float *, float *, int64_t, int64_t, hipStream_t);
+int pulse_launch_rms_norm_backward(const uint16_t *, int64_t, const uint16_t *, const float *, const uint16_t *, int64_t,
+                                   const uint16_t *, int64_t, uint16_t *, int64_t, float *, int32_t, int64_t, int64_t,
+                                   void *, hipStream_t);
+int pulse_launch_group_quant(const uint16_t *, int64_t, int64_t, int64_t, int32_t, uint8_t *, float *, hipStream_t);
+int64_t pulse_fp8_gemm_ws_size(int64_t M, int64_t J, int64_t C);
+int pulse_launch_fp8_gemm(const uint8_t *, const float *, const uint8_t *, const float *, const uint16_t *, int32_t,
+                          int64_t, int64_t, int64_t, uint16_t *, int64_t, void *, hipStream_t);
+int64_t pulse_moe_ws_size(int64_t T, int64_t H, int64_t I, int64_t top_k);
+int pulse_launch_moe_route(const float *, int64_t, int64_t, int64_t, int32_t, int32_t, float, int32_t *, float *,
+                           hipStream_t);
+int pulse_launch_moe_forward(const uint16_t *, int64_t, const int32_t *, const float *, const uint8_t *, const float *,
+                             const uint8_t *, const float *, int64_t, int64_t, int64_t, int64_t, int64_t, uint16_t *,
+                             int64_t, uint32_t *, void *, hipStream_t);
 }
 
 namespace {
@@ -668,6 +684,147 @@ int pulse_lora_backward(const uint16_t *x, int64_t ldx, const uint16_t *dy, int6
         return PULSE_EWORKSPACE;
     return pulse_launch_lora_backward(x, ldx, dy, lddy, a, b, scales, plan, n_tokens, k, n, rank, n_adapters, h, dx,
                                       lddx, da, db, accumulate, ws, stream);
+}
+
+}  // extern "C"
+
+// ---- the sampler's layer over the FP8 view ------------------------------------------
+namespace {
+
+constexpr int64_t kMaxNormCols = 16384;    // a row stays in one workgroup's registers
+constexpr int64_t kMaxQuantCols = 1 << 24;
+constexpr int64_t kMaxGemmSide = 1 << 22;  // 256 rows of codes count in 31 bits
+constexpr int64_t kMaxMoeSide = 1 << 16, kMaxMoeStride = 1 << 20;
+
+int check_norm_sizes(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 8 || cols % 8 != 0) return PULSE_EINVAL;
+    return rows > kMaxLora || cols > kMaxNormCols ? PULSE_ERANGE : PULSE_OK;
+}
+
+int check_gemm_sizes(int64_t m, int64_t n, int64_t k, int32_t form) {
+    if (m < 0 || n < 1 || k < 16 || k % 16 != 0 || (form != PULSE_GEMM_NT && form != PULSE_GEMM_NN) ||
+        (form == PULSE_GEMM_NN && n % 16 != 0))
+        return PULSE_EINVAL;
+    if (m > kMaxLora || n > kMaxGemmSide || k > kMaxGemmSide) return PULSE_ERANGE;
+    // workgroups of a launch
+    const int64_t j = form == PULSE_GEMM_NN ? k : n;
+    return ((m + 63) / 64) * ((j + 127) / 128) > 0x7FFFFF00 || m * j > (int64_t)0x7FFFFF00 * 256 ? PULSE_ERANGE : PULSE_OK;
+}
+
+int check_moe_sizes(int64_t T, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k) {
+    if (T < 0 || hidden < 16 || hidden % 16 != 0 || inter < 16 || inter % 16 != 0 || experts < 1 || top_k < 1 ||
+        top_k > experts)
+        return PULSE_EINVAL;
+    return T > PULSE_MOE_MAX_TOKENS || hidden > kMaxMoeSide || inter > kMaxMoeSide || experts > PULSE_MOE_MAX_EXPERTS ||
+                   top_k > PULSE_MOE_MAX_TOP_K || T * top_k > PULSE_MOE_MAX_PAIRS
+               ? PULSE_ERANGE
+               : PULSE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t pulse_rms_norm_ws_bytes(int64_t n_tokens, int64_t cols) {
+    const int rc = check_norm_sizes(n_tokens, cols);
+    return rc != PULSE_OK ? rc : pulse_rms_norm_ws_size(n_tokens, cols);
+}
+
+int pulse_rms_norm(const uint16_t *x, int64_t ldx, const uint16_t *weight, double eps, uint16_t *residual,
+                   int64_t ldr, uint16_t *y, int64_t ldy, uint8_t *codes, float *scales, float *rstd,
+                   int64_t n_tokens, int64_t cols, hipStream_t stream) {
+    const int rc = check_norm_sizes(n_tokens, cols);
+    if (rc != PULSE_OK) return rc;
+    if (!(eps > 0) || !((float)eps > 0) || !std::isfinite((float)eps)) return PULSE_EINVAL;
+    if (n_tokens == 0) return PULSE_OK;
+    if (!x || !weight || !codes != !scales || (!y && !codes) || bad_stride(ldx, cols) || (residual && bad_stride(ldr, cols)) || (y && bad_stride(ldy, cols)))
+        return PULSE_EINVAL;
+    if (!aligned16(x) || !aligned16(weight) || !aligned16(residual) || !aligned16(y) || !aligned16(codes)) return PULSE_EALIGN;
+    return pulse_launch_rms_norm(x, ldx, weight, eps, residual, ldr, y, ldy, codes, scales, rstd, n_tokens, cols, stream);
+}
+
+int pulse_rms_norm_backward(const uint16_t *s, int64_t lds, const uint16_t *weight, const float *rstd,
+                            const uint16_t *dy, int64_t lddy, const uint16_t *dres, int64_t lddres, uint16_t *dx,
+                            int64_t lddx, float *dweight, int32_t accumulate, int64_t n_tokens, int64_t cols,
+                            void *ws, size_t ws_bytes, hipStream_t stream) {
+    const int rc = check_norm_sizes(n_tokens, cols);
+    if (rc != PULSE_OK) return rc;
+    if (!dweight || (accumulate != 0 && accumulate != 1)) return PULSE_EINVAL;
+    if (n_tokens == 0)  // no token: the gradient is zero
+        return accumulate ? PULSE_OK : pulse_launch_fill_zero(dweight, (size_t)cols * 4, stream);
+    if (!s || !weight || !rstd || !dy || bad_stride(lds, cols) || bad_stride(lddy, cols) ||
+        (dres && bad_stride(lddres, cols)) || (dx && bad_stride(lddx, cols)))
+        return PULSE_EINVAL;
+    if (!aligned16(s) || !aligned16(weight) || !aligned16(dy) || !aligned16(dres) || !aligned16(dx) ||
+        !aligned16(dweight) || !aligned16(ws))
+        return PULSE_EALIGN;
+    if (!ws || ws_bytes < (size_t)pulse_rms_norm_ws_size(n_tokens, cols)) return PULSE_EWORKSPACE;
+    return pulse_launch_rms_norm_backward(s, lds, weight, rstd, dy, lddy, dres, lddres, dx, lddx, dweight, accumulate,
+                                          n_tokens, cols, ws, stream);
+}
+
+int fp8_group_quant(const uint16_t *x, int64_t ldx, int64_t n_tokens, int64_t cols, int32_t glu, uint8_t *codes,
+                    float *scales, hipStream_t stream) {
+    if (n_tokens < 0 || cols < 8 || cols % 8 != 0 || (glu != 0 && glu != 1)) return PULSE_EINVAL;
+    if (n_tokens > kMaxLora || cols > kMaxQuantCols || n_tokens * ((cols + 511) / 512) / 16 > 0x7FFFFF00) return PULSE_ERANGE;
+    if (n_tokens == 0) return PULSE_OK;
+    if (!x || !codes || !scales || bad_stride(ldx, glu ? 2 * cols : cols)) return PULSE_EINVAL;
+    if (!aligned16(x) || !aligned16(codes)) return PULSE_EALIGN;
+    return pulse_launch_group_quant(x, ldx, n_tokens, cols, glu, codes, scales, stream);
+}
+
+int64_t fp8_block_gemm_ws_bytes(int64_t m, int64_t n, int64_t k, int32_t form) {
+    const int rc = check_gemm_sizes(m, n, k, form);
+    if (rc != PULSE_OK) return rc;
+    return m == 0 ? 0 : pulse_fp8_gemm_ws_size(m, form == PULSE_GEMM_NN ? k : n, form == PULSE_GEMM_NN ? n : k);
+}
+
+int fp8_block_gemm(const uint8_t *x, const float *x_scales, const uint8_t *w, const float *w_scales,
+                   const uint16_t *bias, int32_t form, int64_t m, int64_t n, int64_t k, uint16_t *y, int64_t ldy,
+                   void *ws, size_t ws_bytes, hipStream_t stream) {
+    const int rc = check_gemm_sizes(m, n, k, form);
+    if (rc != PULSE_OK) return rc;
+    const int64_t j = form == PULSE_GEMM_NN ? k : n;
+    if (m == 0) return PULSE_OK;
+    if (!x || !x_scales || !w || !w_scales || !y || ldy < j) return PULSE_EINVAL;
+    if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(ws)) return PULSE_EALIGN;
+    const size_t need = (size_t)pulse_fp8_gemm_ws_size(m, j, form == PULSE_GEMM_NN ? n : k);
+    if (need && (!ws || ws_bytes < need)) return PULSE_EWORKSPACE;
+    return pulse_launch_fp8_gemm(x, x_scales, w, w_scales, bias, form, m, n, k, y, ldy, ws, stream);
+}
+
+int pulse_moe_route(const float *logits, int64_t ld, int64_t n_tokens, int64_t experts, int64_t top_k,
+                    int32_t over_all, double scale, int32_t *ids, float *weights, hipStream_t stream) {
+    if (n_tokens < 0 || experts < 1 || top_k < 1 || top_k > experts || (over_all != 0 && over_all != 1) ||
+        !std::isfinite((float)scale))
+        return PULSE_EINVAL;
+    if (n_tokens > kMaxLora || experts > PULSE_MOE_MAX_EXPERTS || top_k > PULSE_MOE_MAX_TOP_K) return PULSE_ERANGE;
+    if (n_tokens == 0) return PULSE_OK;
+    if (!logits || !ids || !weights || ld < experts) return PULSE_EINVAL;
+    return pulse_launch_moe_route(logits, ld, n_tokens, experts, (int32_t)top_k, over_all, (float)scale, ids, weights,
+                                  stream);
+}
+
+int64_t pulse_moe_ws_bytes(int64_t n_tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k) {
+    const int rc = check_moe_sizes(n_tokens, hidden, inter, experts, top_k);
+    return rc != PULSE_OK ? rc : pulse_moe_ws_size(n_tokens, hidden, inter, top_k);
+}
+
+int pulse_moe_forward(const uint16_t *x, int64_t ldx, const int32_t *ids, const float *weights,
+                      const uint8_t *up, const float *up_scales, const uint8_t *down, const float *down_scales,
+                      int64_t n_tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k, uint16_t *y,
+                      int64_t ldy, uint32_t *d_status, void *ws, size_t ws_bytes, hipStream_t stream) {
+    const int rc = check_moe_sizes(n_tokens, hidden, inter, experts, top_k);
+    if (rc != PULSE_OK) return rc;
+    if (n_tokens == 0) return PULSE_OK;
+    if (!x || !ids || !weights || !up || !up_scales || !down || !down_scales || !y || !d_status ||
+        bad_stride(ldx, hidden) || bad_stride(ldy, hidden))
+        return PULSE_EINVAL;
+    if (ldx > kMaxMoeStride) return PULSE_ERANGE;
+    if (!aligned16(x) || !aligned16(up) || !aligned16(down) || !aligned16(y) || !aligned16(ws)) return PULSE_EALIGN;
+    if (!ws || ws_bytes < (size_t)pulse_moe_ws_size(n_tokens, hidden, inter, top_k)) return PULSE_EWORKSPACE;
+    return pulse_launch_moe_forward(x, ldx, ids, weights, up, up_scales, down, down_scales, n_tokens, hidden, inter,
+                                    experts, top_k, y, ldy, d_status, ws, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,348 @@
+// norm.hip -- the root-mean-square norm in front of a projection, with the
+// residual's addition before it and E4M3 codes behind it; its backward pass; and
+// the group quantiser for the rows that no norm makes (attention's output, an
+// MLP's activation, gradients).
+//
+// For a row of n columns:
+//   s = bf16(x + residual), or x         (what later layers and the backward pass read)
+//   r = 1 / sqrt(mean(s^2) + eps),  y = s r w
+//   dx = r (dy w - s r mean(dy w s r)) + dres,  dw = sum over rows of dy s r
+// Every byte is read and written once, so the large calls are bound by HBM and the
+// small ones by the chain load - sum - barrier - store.  A row stays in the
+// registers of one workgroup between its sum and its output: 8 columns (16 bytes)
+// a lane, so that 16 lanes hold a quantisation group and 64 lanes read 1024
+// contiguous bytes.
+#include "e4m3.hpp"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace pulse {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int NP = 512;         // columns of a wave's piece
+constexpr int NORM_WAVES = 16;  // most waves of a workgroup
+constexpr int NORM_PIECES = 8;  // most pieces of a lane, with at most four waves then
+constexpr int NORM_BACK_WAVES = 8;  // of the backward pass, whose lanes hold dw too
+constexpr int norm_threads(int pieces, int waves) { return (pieces <= 4 ? waves : 4) * kWave; }
+
+struct NormArgs {
+    const uint16_t *x, *w;
+    uint16_t *residual, *y;
+    uint8_t *codes;
+    float *scales, *rstd;
+    int64_t ldx, ldr, ldy;
+    int32_t cols;
+    float eps;
+};
+
+// the row's sum in every thread; s: LDS of a float a wave
+__device__ __forceinline__ float row_sum(float v, float *s) {
+    v = wave_reduce_sum(v);
+    const int nw = blockDim.x / kWave;
+    if (nw == 1) return v;
+    if (lane_id() == 0) s[wave_id()] = v;
+    lds_barrier();
+    v = s[0];
+    for (int i = 1; i < nw; ++i) v += s[i];
+    return v;
+}
+
+// A workgroup takes one row, wave w its pieces w, w + waves, ...
+template <int P, bool RES>
+__global__ __launch_bounds__(norm_threads(P, NORM_WAVES)) void k_rms_norm(NormArgs g) {
+    __shared__ float s_sum[NORM_WAVES];
+    const int64_t row = blockIdx.x;
+    const int nt = blockDim.x;
+    const uint16_t *const x = g.x + row * g.ldx;
+    uint16_t *const res = RES ? g.residual + row * g.ldr : nullptr;
+    u32x4 v[P], r[RES ? P : 1], w[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int c = (p * nt + (int)threadIdx.x) * 8;
+        v[p] = u32x4{0, 0, 0, 0};
+        if (RES) r[p] = u32x4{0, 0, 0, 0};
+        if (c < g.cols) {
+            v[p] = *reinterpret_cast<const u32x4 *>(x + c);
+            if (RES) r[p] = *reinterpret_cast<const u32x4 *>(res + c);
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int c = (p * nt + (int)threadIdx.x) * 8;
+        w[p] = u32x4{0, 0, 0, 0};
+        if (c < g.cols) w[p] = *reinterpret_cast<const u32x4 *>(g.w + c);
+    }
+    float sum = 0;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        float a[8];
+        widen8(v[p], a);
+        if (RES) {
+            float b[8];
+            widen8(r[p], b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] += b[i];
+            v[p] = narrow8(a);
+            const int c = (p * nt + (int)threadIdx.x) * 8;
+            if (c < g.cols) *reinterpret_cast<u32x4 *>(res + c) = v[p];
+            widen8(v[p], a);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(a[i], a[i], sum);
+    }
+    const float rstd = 1.0f / sqrtf(row_sum(sum, s_sum) / (float)g.cols + g.eps);
+    if (g.rstd && threadIdx.x == 0) g.rstd[row] = rstd;
+    const int64_t groups = (g.cols + QG - 1) / QG;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int c = (p * nt + (int)threadIdx.x) * 8;
+        float a[8], b[8];
+        widen8(v[p], a);
+        widen8(w[p], b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = a[i] * rstd * b[i];
+        if (g.y && c < g.cols) *reinterpret_cast<u32x4 *>(g.y + row * g.ldy + c) = narrow8(a);
+        if (g.codes) {
+            float s;
+            const u32x2 q = group_codes(a, &s);  // (lanes past the last column hold zeros)
+            if (c < g.cols) {
+                *reinterpret_cast<u32x2 *>(g.codes + row * g.cols + c) = q;
+                if (c % QG == 0) g.scales[row * groups + c / QG] = s;
+            }
+        }
+    }
+}
+
+struct NormBackArgs {
+    const uint16_t *s, *w, *dy, *dres;
+    const float *rstd;
+    uint16_t *dx;
+    float *parts;  // [workgroups][cols]: sums of dy s r over a workgroup's rows
+    int64_t lds, lddy, lddres, lddx, rows;
+    int32_t cols;
+};
+
+// A workgroup takes the rows blockIdx.x, + gridDim.x, ... and keeps its share of dw in registers.
+template <int P>
+__global__ __launch_bounds__(norm_threads(P, NORM_BACK_WAVES)) void k_rms_norm_back(NormBackArgs g) {
+    __shared__ float s_sum[2][NORM_BACK_WAVES];
+    const int nt = blockDim.x;
+    float dw[P][8];
+    u32x4 w[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int c = (p * nt + (int)threadIdx.x) * 8;
+        w[p] = u32x4{0, 0, 0, 0};
+        if (c < g.cols) w[p] = *reinterpret_cast<const u32x4 *>(g.w + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[p][i] = 0;
+    }
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < g.rows; row += gridDim.x, turn ^= 1) {
+        u32x4 v[P], d[P];
+        const float rstd = g.rstd[row];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int c = (p * nt + (int)threadIdx.x) * 8;
+            v[p] = d[p] = u32x4{0, 0, 0, 0};
+            if (c < g.cols) {
+                v[p] = *reinterpret_cast<const u32x4 *>(g.s + row * g.lds + c);
+                d[p] = *reinterpret_cast<const u32x4 *>(g.dy + row * g.lddy + c);
+            }
+        }
+        float sum = 0;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            float a[8], b[8], f[8];
+            widen8(v[p], a);
+            widen8(d[p], b);
+            widen8(w[p], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float hat = a[i] * rstd;
+                dw[p][i] = __builtin_fmaf(b[i], hat, dw[p][i]);
+                sum = __builtin_fmaf(b[i] * f[i], hat, sum);
+            }
+        }
+        if (!g.dx) continue;
+        // (the other half of s_sum next time: a wave still reads this one)
+        const float mean = row_sum(sum, s_sum[turn]) / (float)g.cols;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int c = (p * nt + (int)threadIdx.x) * 8;
+            if (c >= g.cols) continue;
+            float a[8], b[8], f[8], o[8];
+            widen8(v[p], a);
+            widen8(d[p], b);
+            widen8(w[p], f);
+            if (g.dres) widen8(*reinterpret_cast<const u32x4 *>(g.dres + row * g.lddres + c), o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float t = __builtin_fmaf(a[i] * rstd, -mean, b[i] * f[i]);
+                o[i] = g.dres ? __builtin_fmaf(t, rstd, o[i]) : t * rstd;
+            }
+            *reinterpret_cast<u32x4 *>(g.dx + row * g.lddx + c) = narrow8(o);
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int c = (p * nt + (int)threadIdx.x) * 8;
+        if (c >= g.cols) continue;
+        float *const out = g.parts + (int64_t)blockIdx.x * g.cols + c;
+        *reinterpret_cast<f32x4 *>(out) = f32x4{dw[p][0], dw[p][1], dw[p][2], dw[p][3]};
+        *reinterpret_cast<f32x4 *>(out + 4) = f32x4{dw[p][4], dw[p][5], dw[p][6], dw[p][7]};
+    }
+}
+
+// dw = the sum of the workgroups' parts, in their order: 64 columns a workgroup, wave w the parts w, w + 16, ...
+__global__ __launch_bounds__(1024) void k_rms_norm_sum(const float *__restrict__ parts, int32_t n, int32_t cols,
+                                                       float *__restrict__ dw, int32_t accumulate) {
+    __shared__ float s[16][kWave];
+    const int c = blockIdx.x * kWave + lane_id(), w = wave_id();
+    float sum = 0;
+    if (c < cols)
+        for (int i = w; i < n; i += 16) sum += parts[(int64_t)i * cols + c];
+    s[w][lane_id()] = sum;
+    __syncthreads();
+    if (w != 0 || c >= cols) return;
+    for (int i = 1; i < 16; ++i) sum += s[i][lane_id()];
+    dw[c] = accumulate ? dw[c] + sum : sum;
+}
+
+struct GroupQuantArgs {
+    const uint16_t *x;
+    uint8_t *codes;
+    float *scales;
+    int64_t ldx, pieces;
+    int32_t cols, per_row;
+};
+
+constexpr int GQ = 4;  // pieces of a wave, all read before the first is worked on
+
+// A wave takes GQ pieces of 512 columns, one after the other through the rows; GLU: silu(x[c]) x[cols + c].
+template <bool GLU>
+__global__ __launch_bounds__(256) void k_group_quant(GroupQuantArgs g) {
+    const int64_t first = ((int64_t)blockIdx.x * 4 + wave_id()) * GQ;
+    const int lane = lane_id();
+    u32x4 v[GQ], u[GLU ? GQ : 1];
+    int64_t row[GQ];
+    int c[GQ];
+    int64_t r = first / g.per_row;
+    int p = (int)(first - r * g.per_row);
+#pragma unroll
+    for (int i = 0; i < GQ; ++i) {
+        row[i] = r;
+        c[i] = p * NP + lane * 8;
+        if (first + i >= g.pieces) c[i] = g.cols;
+        if (++p == g.per_row) p = 0, ++r;
+        v[i] = u32x4{0, 0, 0, 0};
+        if (GLU) u[i] = u32x4{0, 0, 0, 0};
+        if (c[i] < g.cols) {
+            const uint16_t *const at = g.x + row[i] * g.ldx + c[i];
+            v[i] = *reinterpret_cast<const u32x4 *>(at);
+            if (GLU) u[i] = *reinterpret_cast<const u32x4 *>(at + g.cols);
+        }
+    }
+    const int64_t groups = (g.cols + QG - 1) / QG;
+#pragma unroll
+    for (int i = 0; i < GQ; ++i) {
+        float a[8], s;
+        widen8(v[i], a);
+        if (GLU) {
+            float b[8];
+            widen8(u[i], b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] = silu(a[j]) * b[j];
+        }
+        const u32x2 q = group_codes(a, &s);
+        if (c[i] < g.cols) {
+            *reinterpret_cast<u32x2 *>(g.codes + row[i] * g.cols + c[i]) = q;
+            if (c[i] % QG == 0) g.scales[row[i] * groups + c[i] / QG] = s;
+        }
+    }
+}
+
+// Waves of a row's workgroup and pieces of a wave.
+struct NormShape {
+    int waves, pieces;
+};
+
+inline NormShape norm_shape(int64_t rows, int64_t cols, int waves) {
+    const int n = (int)((cols + NP - 1) / NP);
+    const int most = rows >= 1024 ? 4 : waves;
+    int pieces = (n + most - 1) / most;
+    for (int p : {1, 2, 3, 4, 6, NORM_PIECES})
+        if (p >= pieces) {
+            pieces = p;
+            break;
+        }
+    return {(n + pieces - 1) / pieces, pieces};
+}
+
+// f.template operator()<pieces>() for the pieces of norm_shape
+template <typename F>
+inline void with_pieces(int pieces, F &&f) {
+    switch (pieces) {
+    case 1: return f(std::integral_constant<int, 1>{});
+    case 2: return f(std::integral_constant<int, 2>{});
+    case 3: return f(std::integral_constant<int, 3>{});
+    case 4: return f(std::integral_constant<int, 4>{});
+    case 6: return f(std::integral_constant<int, 6>{});
+    default: return f(std::integral_constant<int, NORM_PIECES>{});
+    }
+}
+
+// workgroups of the backward pass: a part of dw each
+inline int64_t norm_parts(int64_t rows) { return std::min<int64_t>(rows, 512); }
+
+}  // namespace pulse
+
+using namespace pulse;
+
+extern "C" {
+
+int64_t pulse_rms_norm_ws_size(int64_t rows, int64_t cols) { return norm_parts(rows) * cols * (int64_t)sizeof(float); }
+
+int pulse_launch_rms_norm(const uint16_t *x, int64_t ldx, const uint16_t *w, double eps, uint16_t *residual,
+                          int64_t ldr, uint16_t *y, int64_t ldy, uint8_t *codes, float *scales, float *rstd,
+                          int64_t rows, int64_t cols, hipStream_t stream) {
+    const NormArgs g{x, w, residual, y, codes, scales, rstd, ldx, ldr, ldy, (int32_t)cols, (float)eps};
+    const NormShape n = norm_shape(rows, cols, NORM_WAVES);
+    with_pieces(n.pieces, [&](auto p) {
+        constexpr int P = decltype(p)::value;
+        const dim3 grid((unsigned)rows), block((unsigned)(n.waves * kWave));
+        if (residual) k_rms_norm<P, true><<<grid, block, 0, stream>>>(g);
+        else k_rms_norm<P, false><<<grid, block, 0, stream>>>(g);
+    });
+    return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+
+int pulse_launch_rms_norm_backward(const uint16_t *s, int64_t lds, const uint16_t *w, const float *rstd,
+                                   const uint16_t *dy, int64_t lddy, const uint16_t *dres, int64_t lddres,
+                                   uint16_t *dx, int64_t lddx, float *dw, int32_t accumulate, int64_t rows,
+                                   int64_t cols, void *ws, hipStream_t stream) {
+    float *const parts = static_cast<float *>(ws);
+    const NormBackArgs g{s, w, dy, dres, rstd, dx, parts, lds, lddy, lddres, lddx, rows, (int32_t)cols};
+    const NormShape n = norm_shape(rows, cols, NORM_BACK_WAVES);
+    const int64_t wgs = norm_parts(rows);
+    with_pieces(n.pieces, [&](auto p) {
+        k_rms_norm_back<decltype(p)::value>
+            <<<dim3((unsigned)wgs), dim3((unsigned)(n.waves * kWave)), 0, stream>>>(g);
+    });
+    k_rms_norm_sum<<<dim3((unsigned)((cols + kWave - 1) / kWave)), dim3(1024), 0, stream>>>(parts, (int32_t)wgs,
+                                                                                       (int32_t)cols, dw, accumulate);
+    return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+
+int pulse_launch_group_quant(const uint16_t *x, int64_t ldx, int64_t rows, int64_t cols, int32_t glu, uint8_t *codes,
+                             float *scales, hipStream_t stream) {
+    GroupQuantArgs g{x, codes, scales, ldx, 0, (int32_t)cols, (int32_t)((cols + NP - 1) / NP)};
+    g.pieces = rows * g.per_row;
+    const dim3 grid((unsigned)((g.pieces + 4 * GQ - 1) / (4 * GQ)));
+    if (glu) k_group_quant<true><<<grid, dim3(256), 0, stream>>>(g);
+    else k_group_quant<false><<<grid, dim3(256), 0, stream>>>(g);
+    return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+}
