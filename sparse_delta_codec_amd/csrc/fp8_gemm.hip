@@ -38,52 +38,85 @@ struct GemmArgs {
     int32_t shares, per;    // `shares`, of `per` steps
 };
 
-// ---- the tile kernel ----------------------------------------------------------------
-// A workgroup makes BJ columns of BM tokens; its waves are WJ x WM, each with BJ / WJ
-// columns and BM / WM tokens.  A step's 128 columns of W and x lie in one of STAGES
-// buffers of LDS, STAGES - 1 steps ahead of the step that is multiplied.
+// ---- tiles ----------------------------------------------------------------------------
+// A workgroup makes BJ columns of BM tokens; its waves are WM x 2, each with BM / WM tokens
+// and 64 columns of every 128 (which have one scale a step).  A step's 128 columns of x and
+// W lie in LDS, put there while earlier steps are multiplied.
 //
 // In LDS a row of 128 bytes is eight pieces of 16, and piece p of row r lies at
 // p ^ swap(r).  A wave's matrix operand for four tiles of 16 columns takes row
 // 16 a + 4 t + b of its 64 as row 4 a + b of tile t: a lane's results of the four tiles
 // are then 16 neighbouring columns.  Within a tile, a and b vary, and swap() goes by
-// their low three bits.
+// their low three bits, so that the eight lanes which read at once are in eight places.
 __device__ __forceinline__ int swap_piece(int r) { return (r & 3) | ((r >> 2) & 4); }
 
-// nn: rows are steps of the contraction, BJ bytes of columns each; piece p of row r lies
+// nn: rows are steps of the contraction, 128 bytes of columns each; piece p of row r lies
 // at p ^ (r & 7), so that the eight rows of a transposing read are in eight places.
+
+template <int BM_, int BJ_, int WM_>
+struct Tile {
+    static constexpr int BM = BM_, BJ = BJ_, WM = WM_, WJ = 2;
+    static constexpr int waves = WM * WJ, threads = waves * kWave;
+    static constexpr int tm = BM / WM, mt = tm / 16;  // tokens of a wave, in tiles of 16
+    static constexpr int parts = BJ / GB;             // of 128 columns
+    static constexpr int results = mt * parts * 4;    // of a lane, four values each
+    static constexpr int x_bytes = BM * GB, w_bytes = GB * GB;  // of a step (w: of a part)
+    static constexpr int s_bytes = BM * 16;           // scales of four steps
+    static constexpr int xi = x_bytes / 1024 / waves, wi = w_bytes / 1024 / waves;  // loads of a wave
+    static constexpr int si = (BM / kWave + waves - 1) / waves;  // (a wave beyond the last repeats the last one)
+    static_assert(x_bytes % (1024 * waves) == 0 && w_bytes % (1024 * waves) == 0, "whole loads");
+    static_assert(BM % kWave == 0 && BJ % GB == 0 && tm % 16 == 0, "tile");
+};
+
 // The i-th of n when the workgroups 8 k + x, of XCD x, are to have neighbouring numbers
 __device__ __forceinline__ int spread(int i, int n) {
     const int x = i & 7, k = i >> 3, whole = n >> 3, rest = n & 7;
     return x * whole + (x < rest ? x : rest) + k;
 }
 
-template <int BM, int BJ>
-__device__ __forceinline__ void tile_origin(int tile, int tiles_m, int tiles_j, int &m0, int &j0) {
-    const int band = 8 * tiles_j, b0 = tile / band * 8, rows = tiles_m - b0 < 8 ? tiles_m - b0 : 8;
+// Where a tile lies: tiles go through eight rows of tiles of tokens at a time.
+template <typename T>
+__device__ __forceinline__ void tile_origin(const GemmArgs &g, int tile, int &m0, int &j0) {
+    const int band = 8 * g.tiles_j, b0 = tile / band * 8, rows = g.tiles_m - b0 < 8 ? g.tiles_m - b0 : 8;
     const int in = tile % band;
-    m0 = (b0 + in % rows) * BM;
-    j0 = in / rows * BJ;
+    m0 = (b0 + in % rows) * T::BM;
+    j0 = in / rows * T::BJ;
 }
 
-// Result `j` (tile of 16 columns), `m` (tile of 16 tokens) of a thread: its token and the first of
-// its four columns within a workgroup's tile
+// A workgroup's tile and its share of the contraction.  Workgroups go round the XCDs: each XCD
+// takes a run of tiles.
+struct Work {
+    int tile, share, s0, s1;
+};
+
+__device__ __forceinline__ Work work_of(const GemmArgs &g) {
+    const int wg = blockIdx.x;
+    if (wg < g.whole) return {spread(wg, g.whole), 0, 0, g.steps};
+    const int at = spread(wg - g.whole, (g.tiles_m * g.tiles_j - g.whole) * g.shares);
+    const int share = at % g.shares, s0 = share * g.per;
+    return {g.whole + at / g.shares, share, s0, s0 + g.per < g.steps ? s0 + g.per : g.steps};
+}
+
+// Result j (part and tile of 16 columns) and m (tile of 16 tokens) of a thread: its token and the
+// first of its four columns within a workgroup's tile
 template <typename T, bool NN>
 __device__ __forceinline__ void result_place(int thread, int j, int m, int &row, int &col) {
     const int lane = thread & 63, wave = thread / kWave, c16 = lane & 15, q = lane >> 4;
-    row = wave % T::wm * T::tm + m * 16 + c16;
-    col = wave / T::wm * T::tj + (j >> 2) * 64 + (NN ? (j & 3) * 16 + q * 4 : q * 16 + (j & 3) * 4);
+    row = wave % T::WM * T::tm + m * 16 + c16;
+    col = (j >> 2) * GB + wave / T::WM * 64 + (NN ? (j & 3) * 16 + q * 4 : q * 16 + (j & 3) * 4);
 }
 
 // four columns of y from float32 sums
+template <bool BIAS>
 __device__ __forceinline__ void store_result(const GemmArgs &g, int row, int col, f32x4 v) {
     uint16_t *const out = g.y + (int64_t)row * g.ldy + col;
-    if (g.bias)
+    const bool whole = col + 3 < g.J && g.ldy % 4 == 0;
+    if (BIAS)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (col + i < g.J) v[i] += __uint_as_float((uint32_t)g.bias[col + i] << 16);
     const u32x2 o = {cast_pair(v[0], v[1]), cast_pair(v[2], v[3])};
-    if (col + 3 < g.J && g.ldy % 4 == 0) {
+    if (whole) {
         *reinterpret_cast<u32x2 *>(out) = o;
     } else {
 #pragma unroll
@@ -92,232 +125,312 @@ __device__ __forceinline__ void store_result(const GemmArgs &g, int row, int col
     }
 }
 
-template <bool NN, int BM, int BJ, int WM, int WJ, int STAGES>
-struct Tile {
-    static constexpr int wm = WM;
-    static constexpr int waves = WM * WJ, threads = waves * kWave;
-    static constexpr int tm = BM / WM, tj = BJ / WJ;      // of a wave
-    static constexpr int mt = tm / 16, jg = tj / 64;      // tiles of 16 tokens, groups of 64 columns
-    static constexpr int results = mt * jg * 4;           // of a lane, four values each
-    static constexpr int x_bytes = BM * GB, w_bytes = BJ * GB, s_bytes = BM * 4;
-    static constexpr int stage = x_bytes + w_bytes + ((s_bytes + 255) / 256) * 256;
-    static constexpr int xi = x_bytes / 1024 / waves, wi = w_bytes / 1024 / waves;  // loads of a wave
-    static constexpr int si = (BM / kWave + waves - 1) / waves;  // (a wave beyond the last repeats the last one)
-    static constexpr int loads = xi + wi + si;
-    static_assert(x_bytes % (1024 * waves) == 0 && w_bytes % (1024 * waves) == 0, "whole loads");
-    static_assert(BM % kWave == 0 && tj % 64 == 0 && GB % tj == 0 && (STAGES - 2) * loads <= 63, "tile");
-};
-
-template <bool NN, int BM, int BJ, int WM, int WJ, int STAGES>
-__global__ __launch_bounds__(WM *WJ *kWave) void k_fp8_tile(GemmArgs g) {
-    using T = Tile<NN, BM, BJ, WM, WJ, STAGES>;
-    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[STAGES * T::stage];
-    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
-    const int c16 = lane & 15, q = lane >> 4;
-
-    // A tile and its share of the contraction.  Workgroups go round the XCDs: each XCD takes a run of
-    // tiles, which go through eight rows of tiles of tokens at a time.
-    const int wg = blockIdx.x, tiles = g.tiles_m * g.tiles_j;
-    int tile, share = 0, s0 = 0, s1 = g.steps;
-    if (wg < g.whole) {
-        tile = spread(wg, g.whole);
-    } else {
-        const int at = spread(wg - g.whole, (tiles - g.whole) * g.shares);
-        tile = g.whole + at / g.shares;
-        share = at % g.shares;
-        s0 = share * g.per;
-        s1 = s0 + g.per < g.steps ? s0 + g.per : g.steps;
-    }
-    int m0, j0;
-    tile_origin<BM, BJ>(tile, g.tiles_m, g.tiles_j, m0, j0);
-    // bases of the first step, and each load's offset from them
-    const int64_t c0 = (int64_t)s0 * GB;
-    const uint8_t *xb = load_base(g.x + (int64_t)m0 * g.C + c0);
-    const uint8_t *wb = load_base(NN ? g.w + c0 * g.K + j0 : g.w + (int64_t)j0 * g.K + c0);
-    const float *sb = load_base(g.sx + (int64_t)m0 * g.gx + s0);
-    uint32_t xo[T::xi], wo[T::wi], so[T::si];
-    constexpr int per_row = BJ / 16, rows_w = 64 / per_row;  // nn: pieces of a row, rows of a load
-    const auto clamped = [](int r, int n) { return r < n ? r : n - 1; };
+template <typename T, bool NN>
+__device__ __forceinline__ void store_results(const GemmArgs &g, const Work &k, int m0, int j0,
+                                              const f32x4 (&acc)[T::parts * 4][T::mt]) {
+    int thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));  // as rare_lane
+    f32x4 *const part = g.parts + ((int64_t)(k.tile - g.whole) * g.shares + k.share) * T::results * T::threads + thread;
+    const auto each = [&](auto &&f) {
 #pragma unroll
-    for (int i = 0; i < T::xi; ++i) {
-        const int r = (wave * T::xi + i) * 8 + (lane >> 3);
-        xo[i] = (uint32_t)(clamped(m0 + r, g.M) - m0) * (uint32_t)g.C + ((lane & 7) ^ swap_piece(r)) * 16;
-    }
+        for (int m = 0; m < T::mt; ++m)
 #pragma unroll
-    for (int i = 0; i < T::wi; ++i) {
-        if constexpr (NN) {
-            const int r = (wave * T::wi + i) * rows_w + lane / per_row;
-            int p = (lane % per_row) ^ (r & 7);
-            if (j0 + p * 16 >= g.J) p = 0;  // columns past the last are not written
-            wo[i] = (uint32_t)r * (uint32_t)g.K + p * 16;
-        } else {
-            const int r = (wave * T::wi + i) * 8 + (lane >> 3);
-            wo[i] = (uint32_t)(clamped(j0 + r, g.J) - j0) * (uint32_t)g.K + ((lane & 7) ^ swap_piece(r)) * 16;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < T::si; ++i) {
-        int at = wave * T::si + i;
-        if (at >= BM / kWave) at = BM / kWave - 1;
-        so[i] = (uint32_t)(clamped(m0 + at * kWave + lane, g.M) - m0) * (uint32_t)g.gx * 4;
-    }
-    const uint32_t mem = __builtin_amdgcn_readfirstlane(lds_at(s_mem));
-    // a step's loads into its buffer; in the last step of a ragged contraction pieces past its end are
-    // taken from its first ones (x's are cleared there before they are multiplied)
-    const auto issue = [&](int s) {
-        const uint32_t at = mem + (uint32_t)((s - s0) % STAGES) * T::stage;
-        const int left = g.C - s * GB;  // columns from this step's first on
-        if (left < GB) {
-#pragma unroll
-            for (int i = 0; i < T::xi; ++i) {
-                const int p = (lane & 7) ^ swap_piece((wave * T::xi + i) * 8 + (lane >> 3));
-                if (p * 16 >= left) xo[i] -= p * 16;
+            for (int j = 0; j < T::parts * 4; ++j) {
+                int row, col;
+                result_place<T, NN>(thread, j, m, row, col);
+                if (m0 + row < g.M) f(m * T::parts * 4 + j, m0 + row, j0 + col, acc[j][m]);
             }
-#pragma unroll
-            for (int i = 0; i < T::wi; ++i) {
-                if constexpr (NN) {
-                    const int r = (wave * T::wi + i) * rows_w + lane / per_row;
-                    if (r >= left) wo[i] -= (uint32_t)r * (uint32_t)g.K;
-                } else {
-                    const int p = (lane & 7) ^ swap_piece((wave * T::wi + i) * 8 + (lane >> 3));
-                    if (p * 16 >= left) wo[i] -= p * 16;
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < T::xi; ++i) load_lds16(at + (wave * T::xi + i) * 1024, xb, xo[i]);
-#pragma unroll
-        for (int i = 0; i < T::wi; ++i) load_lds16(at + T::x_bytes + (wave * T::wi + i) * 1024, wb, wo[i]);
-#pragma unroll
-        for (int i = 0; i < T::si; ++i) {
-            int n = wave * T::si + i;
-            if (n >= BM / kWave) n = BM / kWave - 1;
-            load_lds4(at + T::x_bytes + T::w_bytes + n * 256, sb, so[i]);
-        }
-        xb += GB;
-        wb += NN ? (int64_t)GB * g.K : GB;
-        sb += 1;
     };
-
-    const int wm = wave % WM, wj = wave / WM;
-    f32x4 acc[T::jg * 4][T::mt];
-#pragma unroll
-    for (int j = 0; j < T::jg * 4; ++j)
-#pragma unroll
-        for (int m = 0; m < T::mt; ++m) acc[j][m] = f32x4{0, 0, 0, 0};
-    // a wave's columns lie in one block of 128
-    const scalar_floats sw = (scalar_floats)(uint64_t)g.sw + (int64_t)((j0 + wj * T::tj) / GB) * g.gwj;
-
-    for (int s = s0; s < s0 + STAGES - 1 && s < s1; ++s) issue(s);
-    for (int s = s0; s < s1; ++s) {
-        if (s + STAGES - 2 < s1) wait_loads<(STAGES - 2) * T::loads>();
-        else wait_loads<0>();
-        lds_barrier();  // this step is there, and the last one's buffer is free
-        uint8_t *const buf = s_mem + ((s - s0) % STAGES) * T::stage;
-        if (g.C - s * GB < GB) {  // the ragged end
-            const int left = (g.C - s * GB) / 16, gone = 8 - left;
-            for (int i = threadIdx.x; i < BM * gone; i += T::threads) {
-                const int r = i / gone, p = left + i % gone;
-                *reinterpret_cast<u32x4 *>(buf + r * GB + (p ^ swap_piece(r)) * 16) = u32x4{0, 0, 0, 0};
-            }
-            lds_barrier();
-        }
-        if (s + STAGES - 1 < s1) issue(s + STAGES - 1);
-        const uint8_t *const bx = buf, *const bw = buf + T::x_bytes;
-        const float *const bs = reinterpret_cast<const float *>(buf + T::x_bytes + T::w_bytes);
-        const float sws = sw[(int64_t)s * g.gwc];
-        i32x8 xf[T::mt];
-        float f[T::mt];
-#pragma unroll
-        for (int m = 0; m < T::mt; ++m) {
-            const int r = wm * T::tm + m * 16 + c16;
-            const u32x4 lo = *reinterpret_cast<const u32x4 *>(bx + r * GB + (q ^ swap_piece(r)) * 16);
-            const u32x4 hi = *reinterpret_cast<const u32x4 *>(bx + r * GB + ((q + 4) ^ swap_piece(r)) * 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) xf[m][i] = lo[i], xf[m][i + 4] = hi[i];
-            f[m] = bs[r] * sws;
-        }
-        // Tile j's products are on their way while those of tile j - 1 are added and the operand of
-        // tile j + 1 is read.
-        constexpr int JT = T::jg * 4;
-        i32x8 wf[2];
-        f32x4 p[2][T::mt];
-        const auto operand = [&](int j) {
-            i32x8 v;
-            if constexpr (NN) {
-                typedef __attribute__((address_space(3))) i32x2 *lds2;
-                const int col = wj * (T::tj / 16) + j;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int r = (h >> 1) * 64 + q * 16 + (h & 1) * 8 + (c16 >> 1);
-                    const i32x2 u = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                        (lds2)(uintptr_t)lds_at(bw + r * BJ + (col ^ (r & 7)) * 16 + (c16 & 1) * 8));
-                    v[2 * h] = u[0], v[2 * h + 1] = u[1];
-                }
-            } else {
-                const int r = wj * T::tj + (j >> 2) * 64 + (c16 >> 2) * 16 + (j & 3) * 4 + (c16 & 3);
-                const u32x4 lo = *reinterpret_cast<const u32x4 *>(bw + r * GB + (q ^ swap_piece(r)) * 16);
-                const u32x4 hi = *reinterpret_cast<const u32x4 *>(bw + r * GB + ((q + 4) ^ swap_piece(r)) * 16);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = lo[i], v[i + 4] = hi[i];
-            }
-            return v;
-        };
-        const auto add = [&](int j, int m) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][m][i] = __builtin_fmaf(f[m], p[j & 1][m][i], acc[j][m][i]);
-        };
-        wf[0] = operand(0);
-#pragma unroll
-        for (int j = 0; j < JT; ++j) {
-            if (j + 1 < JT) wf[(j + 1) & 1] = operand(j + 1);
-#pragma unroll
-            for (int m = 0; m < T::mt; ++m) {
-                p[j & 1][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[j & 1], xf[m], f32x4{0, 0, 0, 0}, 0, 0,
-                                                                               0, 0, 0, 0);
-                if (j > 0) add(j - 1, m);
-            }
-            // in this order: the operand's reads, then four FMAs behind each matrix instruction
-            __builtin_amdgcn_sched_group_barrier(0x100, NN ? 4 : 2, 0);
-#pragma unroll
-            for (int m = 0; m < T::mt; ++m) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-            }
-            sched_fence();
-        }
-#pragma unroll
-        for (int m = 0; m < T::mt; ++m) add(JT - 1, m);
-    }
-
-#pragma unroll
-    for (int m = 0; m < T::mt; ++m)
-#pragma unroll
-        for (int j = 0; j < T::jg * 4; ++j) {
-            int row, col;
-            result_place<T, NN>(threadIdx.x, j, m, row, col);
-            if (m0 + row >= g.M) continue;
-            if (wg < g.whole)
-                store_result(g, m0 + row, j0 + col, acc[j][m]);
-            else
-                g.parts[(((int64_t)(tile - g.whole) * g.shares + share) * T::results + m * T::jg * 4 + j) * T::threads +
-                        threadIdx.x] = acc[j][m];
-        }
+    if (k.tile >= g.whole) each([&](int n, int, int, const f32x4 &v) { part[n * T::threads] = v; });
+    else if (g.bias) each([&](int, int row, int col, const f32x4 &v) { store_result<true>(g, row, col, v); });
+    else each([&](int, int row, int col, const f32x4 &v) { store_result<false>(g, row, col, v); });
 }
 
 // y of the shared tiles: the sum of their shares, in order; a workgroup takes one result of every thread
-template <bool NN, int BM, int BJ, int WM, int WJ, int STAGES>
-__global__ __launch_bounds__(WM *WJ *kWave) void k_fp8_join(GemmArgs g) {
-    using T = Tile<NN, BM, BJ, WM, WJ, STAGES>;
-    const int tile = g.whole + blockIdx.y, result = blockIdx.x;
+template <typename T, bool NN>
+__global__ __launch_bounds__(T::threads) void k_fp8_join(GemmArgs g) {
+    const int result = blockIdx.x;
     int m0, j0, row, col;
-    tile_origin<BM, BJ>(tile, g.tiles_m, g.tiles_j, m0, j0);
-    result_place<T, NN>(threadIdx.x, result % (T::jg * 4), result / (T::jg * 4), row, col);
+    tile_origin<T>(g, g.whole + blockIdx.y, m0, j0);
+    result_place<T, NN>(threadIdx.x, result % (T::parts * 4), result / (T::parts * 4), row, col);
     if (m0 + row >= g.M || j0 + col >= g.J) return;
     const f32x4 *part = g.parts + ((int64_t)blockIdx.y * g.shares * T::results + result) * T::threads + threadIdx.x;
     f32x4 v = part[0];
     for (int s = 1; s < g.shares; ++s) v += part[(int64_t)s * T::results * T::threads];
-    store_result(g, m0 + row, j0 + col, v);
+    if (g.bias) store_result<true>(g, m0 + row, j0 + col, v);
+    else store_result<false>(g, m0 + row, j0 + col, v);
+}
+
+// A wave's loads of x and of the parts of W, as offsets from the bases of a step, and of the scales
+// of four steps (one by one, a request for each row's and step's, they took 7% of the time).
+// Rows past the last are the last one's, columns (nn) past the last the first ones': their
+// results are not written.
+template <typename T, bool NN>
+struct Loads {
+    uint32_t x[T::xi], w[T::parts][T::wi], s[T::si];
+
+    static __device__ __forceinline__ int row(int lane, int i, int n) { return (uniform_wave() * n + i) * 8 + (lane >> 3); }
+    static __device__ __forceinline__ int uniform_wave() { return __builtin_amdgcn_readfirstlane(wave_id()); }
+    static __device__ __forceinline__ int piece(int lane, int r, bool w) {
+        return (lane & 7) ^ (NN && w ? r & 7 : swap_piece(r));
+    }
+    // The lane's number for what only a last step needs: the compiler does not see that it could be
+    // worked out before the loop, and held in registers that the loop does not have.
+    static __device__ __forceinline__ int rare_lane() {
+        int lane = lane_id();
+        asm volatile("" : "+v"(lane));
+        return lane;
+    }
+    static __device__ __forceinline__ int scale_row(int i) {
+        int n = uniform_wave() * T::si + i;
+        return n < T::BM / kWave ? n : T::BM / kWave - 1;
+    }
+
+    __device__ __forceinline__ Loads(const GemmArgs &g, int m0, int j0) {
+        const int lane = lane_id();
+        const auto clamped = [](int r, int n) { return (uint32_t)(r < n ? r : n - 1); };
+#pragma unroll
+        for (int i = 0; i < T::xi; ++i) {
+            const int r = row(lane, i, T::xi);
+            x[i] = (clamped(m0 + r, g.M) - m0) * (uint32_t)g.C + piece(lane, r, false) * 16;
+        }
+#pragma unroll
+        for (int p = 0; p < T::parts; ++p)
+#pragma unroll
+            for (int i = 0; i < T::wi; ++i) {
+                const int r = row(lane, i, T::wi);
+                if constexpr (NN) {
+                    const int c = p * GB + piece(lane, r, true) * 16;
+                    w[p][i] = (uint32_t)r * (uint32_t)g.K + (j0 + c < g.J ? c : 0);
+                } else {
+                    w[p][i] = (clamped(j0 + p * GB + r, g.J) - j0) * (uint32_t)g.K + piece(lane, r, true) * 16;
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < T::si; ++i)
+            s[i] = (clamped(m0 + scale_row(i) * kWave + lane, g.M) - m0) * (uint32_t)g.gx * 4;
+    }
+
+    // whether a tile from row m0 on has a row with one of the array's last four scales
+    static __device__ __forceinline__ bool near_end(const GemmArgs &g, int m0) { return m0 + T::BM + 4 > g.M; }
+
+    // The scales of steps 4 n .. 4 n + 3 of row r are four neighbours in memory, from its (4 n)th one
+    // on (what is behind a row's last one is not used); at the array's end they are its last four,
+    // and row r's first one is late() places further on.  An array of less than four is written by hand.
+    static __device__ __forceinline__ int late(const GemmArgs &g, int row, int s) {
+        const int64_t all = (int64_t)g.M * g.gx, at = (int64_t)(row < g.M ? row : g.M - 1) * g.gx + (s & ~3);
+        return all >= 4 && at > all - 4 ? (int)(at - (all - 4)) : 0;
+    }
+
+    // for a last step of `left` columns: pieces past its end are taken from its beginning (x's are
+    // cleared in LDS before they are multiplied)
+    __device__ __forceinline__ void end_x(int left) {
+        const int lane = rare_lane();
+#pragma unroll
+        for (int i = 0; i < T::xi; ++i) {
+            const int p = piece(lane, row(lane, i, T::xi), false) * 16;
+            if (p >= left) x[i] -= p;
+        }
+    }
+    __device__ __forceinline__ void end_w(const GemmArgs &g, int part, int left) {
+        const int lane = rare_lane();
+#pragma unroll
+        for (int i = 0; i < T::wi; ++i) {
+            const int r = row(lane, i, T::wi), p = piece(lane, r, true) * 16;
+            if (NN && r >= left) w[part][i] -= (uint32_t)r * (uint32_t)g.K;
+            if (!NN && p >= left) w[part][i] -= p;
+        }
+    }
+
+    __device__ __forceinline__ void load_x(uint32_t lds, const uint8_t *base) const {
+#pragma unroll
+        for (int i = 0; i < T::xi; ++i) load_lds16(lds + (uniform_wave() * T::xi + i) * 1024, base, x[i]);
+    }
+    __device__ __forceinline__ void load_w(uint32_t lds, const uint8_t *base, int part) const {
+#pragma unroll
+        for (int i = 0; i < T::wi; ++i) load_lds16(lds + (uniform_wave() * T::wi + i) * 1024, base, w[part][i]);
+    }
+    __device__ __forceinline__ void load_s(const GemmArgs &g, int m0, int s4, uint8_t *to, uint32_t lds) const {
+        if ((int64_t)g.M * g.gx < 4) {
+            for (int r = threadIdx.x; r < T::BM; r += T::threads)
+                for (int i = 0; i < 4; ++i)
+                    reinterpret_cast<float *>(to)[r * 4 + i] = i < g.gx ? g.sx[(r < g.M ? r : g.M - 1) * g.gx + i] : 0.0f;
+            return;
+        }
+        // (offsets from a base are not negative: it lies four back where the array has begun by then)
+        const int64_t from = (int64_t)m0 * g.gx + s4;
+        const int back = from >= 4 ? 4 : 0;
+        const float *const base = g.sx + (from - back);
+        const bool end = near_end(g, m0);
+#pragma unroll
+        for (int i = 0; i < T::si; ++i) {
+            uint32_t o = s[i] + 4 * back;
+            if (end) o -= 4 * late(g, m0 + scale_row(i) * kWave + lane_id(), s4);
+            load_lds16(lds + scale_row(i) * 1024, base, o);
+        }
+    }
+};
+
+// the pieces of x from column `left` of a step on are zero (and a barrier behind that)
+template <typename T>
+__device__ __forceinline__ void clear_end(uint8_t *x, int left) {
+    const int from = left / 16, gone = 8 - from;
+    int thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));  // as rare_lane
+    for (int i = thread; i < T::BM * gone; i += T::threads) {
+        const int r = i / gone, p = from + i % gone;
+        *reinterpret_cast<u32x4 *>(x + r * GB + (p ^ swap_piece(r)) * 16) = u32x4{0, 0, 0, 0};
+    }
+    lds_barrier();
+}
+
+// Row r of a step as a matrix operand: lane group q has columns 16 q .. + 15 and 64 + 16 q .. + 15.
+__device__ __forceinline__ i32x8 row_operand(const uint8_t *at, int r) {
+    const int q = lane_id() >> 4;
+    const u32x4 lo = *reinterpret_cast<const u32x4 *>(at + r * GB + (q ^ swap_piece(r)) * 16);
+    const u32x4 hi = *reinterpret_cast<const u32x4 *>(at + r * GB + ((q + 4) ^ swap_piece(r)) * 16);
+    i32x8 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[i + 4] = hi[i];
+    return v;
+}
+
+// Tile t of a wave's 64 columns of W.  nn: a transposing read takes eight rows of 16 columns from
+// sixteen lanes and gives each lane a column; the rows are those that row_operand's lanes have.
+template <bool NN>
+__device__ __forceinline__ i32x8 w_operand(const uint8_t *at, int wj, int t) {
+    const int c16 = lane_id() & 15, q = lane_id() >> 4;
+    if constexpr (NN) {
+        typedef __attribute__((address_space(3))) i32x2 *lds2;
+        i32x8 v;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const int r = (h >> 1) * 64 + q * 16 + (h & 1) * 8 + (c16 >> 1);
+            const i32x2 u = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                (lds2)(uintptr_t)lds_at(at + r * GB + ((wj * 4 + t) ^ (r & 7)) * 16 + (c16 & 1) * 8));
+            v[2 * h] = u[0], v[2 * h + 1] = u[1];
+        }
+        return v;
+    } else {
+        return row_operand(at, wj * 64 + (c16 >> 2) * 16 + t * 4 + (c16 & 3));
+    }
+}
+
+// acc += f * (W x): products are added LAG matrix instructions after theirs was issued, while the
+// next tile's operand is read beside this tile's products.
+template <typename T, bool NN>
+__device__ __forceinline__ void multiply(const uint8_t *w, int wj, const i32x8 (&x)[T::mt], const float (&f)[T::parts][T::mt],
+                                         f32x4 (&acc)[T::parts * 4][T::mt]) {
+    constexpr int LAG = T::mt < 4 ? T::mt : 4, N = T::parts * 4 * T::mt;
+    i32x8 wf[2];
+    f32x4 p[LAG + 1];
+    const auto add = [&](int n) {
+        f32x4 &a = acc[n / T::mt][n % T::mt];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(f[n / T::mt / 4][n % T::mt], p[n % (LAG + 1)][i], a[i]);
+    };
+    const auto operand = [&](int t) { return w_operand<NN>(w + (t >> 2) * T::w_bytes, wj, t & 3); };
+    wf[0] = operand(0);
+#pragma unroll
+    for (int t = 0; t < T::parts * 4; ++t) {
+        if (t + 1 < T::parts * 4) wf[(t + 1) & 1] = operand(t + 1);
+#pragma unroll
+        for (int m = 0; m < T::mt; ++m) {
+            const int n = t * T::mt + m;
+            p[n % (LAG + 1)] =
+                __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[t & 1], x[m], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+            if (n >= LAG) add(n - LAG);
+        }
+        // in this order: the operand's reads, then four FMAs behind each matrix instruction
+        __builtin_amdgcn_sched_group_barrier(0x100, NN ? 4 : 2, 0);
+#pragma unroll
+        for (int m = 0; m < T::mt; ++m) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        }
+        sched_fence();
+    }
+#pragma unroll
+    for (int n = N - LAG; n < N; ++n) add(n);
+    // the sums are made here, not where the compiler would move them, behind the next wait
+#pragma unroll
+    for (int n = 0; n < N; ++n) asm volatile("" : "+v"(acc[n / T::mt][n % T::mt]));
+}
+
+// STAGES buffers of a step: it is loaded STAGES - 1 steps before it is multiplied.
+template <typename T, bool NN, int STAGES>
+__global__ __launch_bounds__(T::threads) void k_fp8_tile(GemmArgs g) {
+    constexpr int stage = T::x_bytes + T::parts * T::w_bytes, loads = T::xi + T::parts * T::wi, s_at = STAGES * stage;
+    static_assert((STAGES - 2) * loads <= 63 && STAGES <= 5, "buffers");
+    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[s_at + 2 * T::s_bytes];
+    const int wave = __builtin_amdgcn_readfirstlane(wave_id()), c16 = lane_id() & 15;
+    const int wm = wave % T::WM, wj = wave / T::WM;
+    const Work k = work_of(g);
+    int m0, j0;
+    tile_origin<T>(g, k.tile, m0, j0);
+    const int64_t c0 = (int64_t)k.s0 * GB, w_step = NN ? (int64_t)GB * g.K : GB;
+    const uint8_t *xb = load_base(g.x + (int64_t)m0 * g.C + c0);
+    const uint8_t *wb = load_base(NN ? g.w + c0 * g.K + j0 : g.w + (int64_t)j0 * g.K + c0);
+    const int blocks = (g.J + GB - 1) / GB;
+    Loads<T, NN> l(g, m0, j0);
+    const uint32_t mem = __builtin_amdgcn_readfirstlane(lds_at(s_mem));
+    const auto issue = [&](int s) {
+        const uint32_t at = mem + (uint32_t)((s - k.s0) % STAGES) * stage;
+        const int left = g.C - s * GB;
+        if (s == k.s0 || s % 4 == 0) {
+            const int to = s_at + (s / 4 & 1) * T::s_bytes;
+            l.load_s(g, m0, s & ~3, s_mem + to, mem + to);
+        }
+        if (left < GB) {
+            l.end_x(left);
+#pragma unroll
+            for (int p = 0; p < T::parts; ++p) l.end_w(g, p, left);
+        }
+        l.load_x(at, xb);
+#pragma unroll
+        for (int p = 0; p < T::parts; ++p) l.load_w(at + T::x_bytes + p * T::w_bytes, wb, p);
+        xb += GB, wb += w_step;
+    };
+    f32x4 acc[T::parts * 4][T::mt];
+#pragma unroll
+    for (int t = 0; t < T::parts * 4; ++t)
+#pragma unroll
+        for (int m = 0; m < T::mt; ++m) acc[t][m] = f32x4{0, 0, 0, 0};
+
+    for (int s = k.s0; s < k.s0 + STAGES - 1 && s < k.s1; ++s) issue(s);
+    for (int s = k.s0; s < k.s1; ++s) {
+        // (a step may have loaded scales too, as its first load: that is then waited for as well)
+        if (s + STAGES - 2 < k.s1) wait_loads<(STAGES - 2) * loads>();
+        else wait_loads<0>();
+        lds_barrier();  // this step is there, and the last one's buffer is free
+        uint8_t *const at = s_mem + ((s - k.s0) % STAGES) * stage;
+        if (g.C - s * GB < GB) clear_end<T>(at, g.C - s * GB);
+        if (s + STAGES - 1 < k.s1) issue(s + STAGES - 1);
+        const float *const scale = reinterpret_cast<const float *>(s_mem + s_at + (s / 4 & 1) * T::s_bytes) + (s & 3);
+        i32x8 x[T::mt];
+        float sx[T::mt];
+        int late[T::mt] = {};
+        if (Loads<T, NN>::near_end(g, m0))
+#pragma unroll
+            for (int m = 0; m < T::mt; ++m) late[m] = Loads<T, NN>::late(g, m0 + wm * T::tm + m * 16 + c16, s);
+#pragma unroll
+        for (int m = 0; m < T::mt; ++m) {
+            const int r = wm * T::tm + m * 16 + c16;
+            x[m] = row_operand(at, r);
+            sx[m] = scale[r * 4 + late[m]];
+        }
+        float f[T::parts][T::mt];
+#pragma unroll
+        for (int p = 0; p < T::parts; ++p) {
+            // (a tile's last part may lie past the last column)
+            const int block = j0 / GB + p < blocks ? j0 / GB + p : blocks - 1;
+            const float sw = ((scalar_floats)(uint64_t)g.sw)[(int64_t)block * g.gwj + (int64_t)s * g.gwc];
+#pragma unroll
+            for (int m = 0; m < T::mt; ++m) f[p][m] = sx[m] * sw;
+        }
+        multiply<T, NN>(at + T::x_bytes, wj, x, f, acc);
+    }
+    store_results<T, NN>(g, k, m0, j0, acc);
 }
 
 // The tile, and how the work is shared: one round of workgroups after the other as long as each
@@ -345,13 +458,19 @@ inline GemmPlan gemm_plan(int64_t M, int64_t J, int64_t C) {
     return p;
 }
 
-template <bool NN, int BM, int BJ, int WM, int WJ, int STAGES>
+template <typename T, bool NN, int STAGES>
 inline void launch_tiles(const GemmArgs &g, hipStream_t stream) {
-    using T = Tile<NN, BM, BJ, WM, WJ, STAGES>;
     const int64_t rest = (int64_t)g.tiles_m * g.tiles_j - g.whole;
-    k_fp8_tile<NN, BM, BJ, WM, WJ, STAGES><<<dim3((unsigned)(g.whole + rest * g.shares)), dim3(T::threads), 0, stream>>>(g);
-    if (rest)
-        k_fp8_join<NN, BM, BJ, WM, WJ, STAGES><<<dim3(T::results, (unsigned)rest), dim3(T::threads), 0, stream>>>(g);
+    const dim3 grid((unsigned)(g.whole + rest * g.shares)), block(T::threads);
+    k_fp8_tile<T, NN, STAGES><<<grid, block, 0, stream>>>(g);
+    if (rest) k_fp8_join<T, NN><<<dim3(T::results, (unsigned)rest), block, 0, stream>>>(g);
+}
+
+template <bool NN>
+inline void launch_gemm(const GemmPlan &p, const GemmArgs &g, hipStream_t stream) {
+    if (p.bm == 256) launch_tiles<Tile<256, 256, 4>, NN, 2>(g, stream);
+    else if (p.bm == 128) launch_tiles<Tile<128, 128, 2>, NN, 2>(g, stream);
+    else launch_tiles<Tile<64, 128, 2>, NN, 4>(g, stream);
 }
 
 }  // namespace pulse
@@ -373,16 +492,8 @@ int pulse_launch_fp8_gemm(const uint8_t *x, const float *sx, const uint8_t *w, c
     const GemmArgs g{x, w, sx, sw, bias, y, static_cast<f32x4 *>(ws), ldy, (int32_t)M, (int32_t)J, (int32_t)C, (int32_t)k,
                      (int32_t)((C + GB - 1) / GB), nn ? 1 : (int32_t)gk, nn ? (int32_t)gk : 1, (int32_t)p.tiles_m,
                      (int32_t)p.tiles_j, (int32_t)((C + GB - 1) / GB), p.whole, p.shares, p.per};
-    if (p.bm == 256) {
-        if (nn) launch_tiles<true, 256, 256, 4, 2, 2>(g, stream);
-        else launch_tiles<false, 256, 256, 4, 2, 2>(g, stream);
-    } else if (p.bm == 128) {
-        if (nn) launch_tiles<true, 128, 128, 2, 2, 2>(g, stream);
-        else launch_tiles<false, 128, 128, 2, 2, 2>(g, stream);
-    } else {
-        if (nn) launch_tiles<true, 64, 128, 2, 2, 4>(g, stream);
-        else launch_tiles<false, 64, 128, 2, 2, 4>(g, stream);
-    }
+    if (nn) launch_gemm<true>(p, g, stream);
+    else launch_gemm<false>(p, g, stream);
     return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 }
