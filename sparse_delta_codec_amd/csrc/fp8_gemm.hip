@@ -358,10 +358,12 @@ __device__ __forceinline__ void multiply(const uint8_t *w, int wj, const i32x8 (
 }
 
 // STAGES buffers of a step: it is loaded STAGES - 1 steps before it is multiplied.
+// (Eight waves: with four, and all registers for one wave a SIMD, the compiler puts products
+// into accumulation registers, which an FMA cannot read.)
 template <typename T, bool NN, int STAGES>
 __global__ __launch_bounds__(T::threads) void k_fp8_tile(GemmArgs g) {
     constexpr int stage = T::x_bytes + T::parts * T::w_bytes, loads = T::xi + T::parts * T::wi, s_at = STAGES * stage;
-    static_assert((STAGES - 2) * loads <= 63 && STAGES <= 5, "buffers");
+    static_assert((STAGES - 2) * loads <= 63 && STAGES <= 5, "buffers: two for the scales of four steps");
     __shared__ __attribute__((aligned(1024))) uint8_t s_mem[s_at + 2 * T::s_bytes];
     const int wave = __builtin_amdgcn_readfirstlane(wave_id()), c16 = lane_id() & 15;
     const int wm = wave % T::WM, wj = wave / T::WM;
@@ -438,24 +440,40 @@ __global__ __launch_bounds__(T::threads) void k_fp8_tile(GemmArgs g) {
 constexpr int kUnits = 256;  // compute units
 
 struct GemmPlan {
-    int bm, bj, whole, shares, per;
+    int kind, bm, bj, whole, shares, per;
     int64_t tiles_m, tiles_j;
 };
 
+// The tile is the one that takes the least time by this estimate.  Microseconds of a step while
+// the chip is full, measured with 256 tiles of 64 steps; a second launch and a float32 value
+// written and read again as measured for the shared tiles of 64 to 512 rows:
+// [512, 8192] x [8192, 4096] by kind 45.0, 40.2, 39.9 and 40.9 us (estimate 44, 39, 37, 38);
+// 1024 rows 62.8, 61.4, 55.9, 79.0; 2048 rows 101, 90, 107, 155; 4096 rows 139, 175, 212, 307.
+struct GemmKind {
+    int bm, bj;
+    float step;
+};
+
+constexpr GemmKind kKinds[] = {{256, 256, 2.1f}, {256, 128, 1.35f}, {128, 128, 0.81f}, {64, 128, 0.58f}};
+
 inline GemmPlan gemm_plan(int64_t M, int64_t J, int64_t C) {
-    GemmPlan p;
-    const int64_t big = ((M + 255) / 256) * ((J + 255) / 256);
-    p.bm = M > 128 && big >= 128 ? 256 : M > 64 ? 128 : 64;
-    p.bj = p.bm == 256 ? 256 : 128;
-    p.tiles_m = (M + p.bm - 1) / p.bm;
-    p.tiles_j = (J + p.bj - 1) / p.bj;
-    const int64_t tiles = p.tiles_m * p.tiles_j, steps = (C + GB - 1) / GB, slots = kUnits * (p.bm == 128 ? 2 : 1);
-    const int64_t rest = tiles % slots;
-    int64_t shares = rest ? std::min<int64_t>(slots / rest, steps) : 1;
-    p.per = (int)((steps + shares - 1) / shares);
-    p.shares = (int)((steps + p.per - 1) / p.per);
-    p.whole = (int)(p.shares > 1 ? tiles - rest : tiles);
-    return p;
+    const int64_t steps = (C + GB - 1) / GB;
+    GemmPlan best{};
+    float least = 0;
+    for (int kind = 0; kind < 4; ++kind) {
+        const GemmKind &k = kKinds[kind];
+        GemmPlan p{kind, k.bm, k.bj, 0, 1, (int)steps, (M + k.bm - 1) / k.bm, (J + k.bj - 1) / k.bj};
+        const int64_t tiles = p.tiles_m * p.tiles_j, rest = tiles % kUnits;
+        const int64_t shares = rest ? std::min<int64_t>(kUnits / rest, steps) : 1;
+        p.per = (int)((steps + shares - 1) / shares);
+        p.shares = (int)((steps + p.per - 1) / p.per);
+        p.whole = (int)(p.shares > 1 ? tiles - rest : tiles);
+        float t = (float)((p.whole + kUnits - 1) / kUnits * steps) * k.step;
+        if (p.shares > 1)  // the shared tiles, and the launch that joins them
+            t += (float)p.per * k.step + 4.0f + (float)(rest * p.shares) * (float)(k.bm * k.bj) * 8.0f / 5e6f;
+        if (best.per == 0 || t < least) best = p, least = t;
+    }
+    return best;
 }
 
 template <typename T, bool NN, int STAGES>
@@ -468,9 +486,12 @@ inline void launch_tiles(const GemmArgs &g, hipStream_t stream) {
 
 template <bool NN>
 inline void launch_gemm(const GemmPlan &p, const GemmArgs &g, hipStream_t stream) {
-    if (p.bm == 256) launch_tiles<Tile<256, 256, 4>, NN, 2>(g, stream);
-    else if (p.bm == 128) launch_tiles<Tile<128, 128, 2>, NN, 2>(g, stream);
-    else launch_tiles<Tile<64, 128, 2>, NN, 4>(g, stream);
+    switch (p.kind) {
+    case 0: return launch_tiles<Tile<256, 256, 4>, NN, 2>(g, stream);
+    case 1: return launch_tiles<Tile<256, 128, 4>, NN, 3>(g, stream);
+    case 2: return launch_tiles<Tile<128, 128, 4>, NN, 4>(g, stream);
+    default: return launch_tiles<Tile<64, 128, 4>, NN, 5>(g, stream);
+    }
 }
 
 }  // namespace pulse
