@@ -435,6 +435,85 @@ __global__ __launch_bounds__(T::threads) void k_fp8_tile(GemmArgs g) {
     store_results<T, NN>(g, k, m0, j0, acc);
 }
 
+// ---- up to 16 tokens -------------------------------------------------------------------
+// The time is that of reading W, a wave's share of it through LDS buffers of its own and
+// without a barrier: a workgroup has 16 rows of W, and its NW waves take their steps of 128
+// columns in turn, each D - 1 of its steps ahead (with x's and the scales).  The waves' sums are
+// added through LDS, in their order.
+template <int NX, int NW, int D>
+__global__ __launch_bounds__(NW *kWave) void k_fp8_rows(GemmArgs g) {
+    constexpr int w_bytes = 16 * GB, x_bytes = NX * GB, stage = w_bytes + x_bytes + 256;
+    constexpr int xi = x_bytes / 1024, loads = 2 + xi + 1;
+    static_assert(NX % 8 == 0 && NX <= 16 && (D - 1) * loads <= 63, "rows of x");
+    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[NW * D * stage];
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id()), c16 = lane & 15, q = lane >> 4;
+    const int n0 = (int)blockIdx.x * 16;
+    const auto clamped = [](int r, int n) { return (uint32_t)(r < n ? r : n - 1); };
+    const uint8_t *const wb = load_base(g.w + (int64_t)n0 * g.K), *const xb = load_base(g.x);
+    const float *const sb = load_base(g.sx);
+    const scalar_floats sw = (scalar_floats)(uint64_t)g.sw + (int64_t)(n0 / GB) * g.gwj;
+    const int r8 = lane >> 3, piece = (lane & 7) ^ (r8 & 7);  // of rows r8 and r8 + 8
+    const uint32_t wo[2] = {(clamped(n0 + r8, g.J) - n0) * (uint32_t)g.K, (clamped(n0 + r8 + 8, g.J) - n0) * (uint32_t)g.K};
+    const uint32_t xo[2] = {clamped(r8, g.M) * (uint32_t)g.K, clamped(r8 + 8, g.M) * (uint32_t)g.K};
+    const uint32_t so = clamped(c16, g.M) * (uint32_t)g.gx * 4;
+    uint8_t *const mine = s_mem + wave * D * stage;
+    const uint32_t mem = __builtin_amdgcn_readfirstlane(lds_at(mine));
+    const auto issue = [&](int s, int turn) {
+        const uint32_t at = mem + (uint32_t)(turn % D) * stage;
+        const uint32_t left = (uint32_t)(g.K - s * GB), p = (uint32_t)piece * 16 < left ? piece * 16 : 0;
+        const uint32_t c = (uint32_t)s * GB + p;
+        load_lds16_once(at, wb, wo[0] + c);
+        load_lds16_once(at + 1024, wb, wo[1] + c);
+#pragma unroll
+        for (int i = 0; i < xi; ++i) load_lds16(at + w_bytes + i * 1024, xb, xo[i] + c);
+        load_lds4(at + w_bytes + x_bytes, sb, so + (uint32_t)s * 4);
+    };
+    f32x4 acc = {0, 0, 0, 0};
+    int ahead = wave, turns = 0, turn = 0;
+    for (int i = 0; i < D - 1; ++i, ahead += NW)
+        if (ahead < g.steps) issue(ahead, turns++);
+    for (int s = wave; s < g.steps; s += NW, ++turn) {
+        if (ahead < g.steps) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last step's reads are done: its buffer is free
+            issue(ahead, turns++);
+            ahead += NW;
+            wait_loads<(D - 1) * loads>();
+        } else {
+            wait_loads<0>();
+        }
+        uint8_t *const at = mine + (turn % D) * stage;
+        if (g.K - s * GB < GB) {  // the pieces of x past the end are zero
+            const int from = (g.K - s * GB) / 16, gone = 8 - from;
+            for (int i = lane; i < NX * gone; i += kWave) {
+                const int r = i / gone, p = from + i % gone;
+                *reinterpret_cast<u32x4 *>(at + w_bytes + r * GB + (p ^ (r & 7)) * 16) = u32x4{0, 0, 0, 0};
+            }
+        }
+        const auto operand = [&](const uint8_t *m, int r) {
+            const u32x4 lo = *reinterpret_cast<const u32x4 *>(m + r * GB + (q ^ (r & 7)) * 16);
+            const u32x4 hi = *reinterpret_cast<const u32x4 *>(m + r * GB + ((q + 4) ^ (r & 7)) * 16);
+            i32x8 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = lo[i], v[i + 4] = hi[i];
+            return v;
+        };
+        const float f = reinterpret_cast<const float *>(at + w_bytes + x_bytes)[lane] * sw[(int64_t)s * g.gwc];
+        const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(at, c16), operand(at + w_bytes, c16 % NX),
+                                                                         f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(f, p[i], acc[i]);
+    }
+    __syncthreads();
+    f32x4 *const sums = reinterpret_cast<f32x4 *>(s_mem);
+    sums[wave * kWave + lane] = acc;
+    __syncthreads();
+    if (wave != 0 || c16 >= g.M) return;
+    for (int i = 1; i < NW; ++i) acc += sums[i * kWave + lane];
+    const int col = n0 + q * 4;
+    if (g.bias) store_result<true>(g, c16, col, acc);
+    else store_result<false>(g, c16, col, acc);
+}
+
 // The tile, and how the work is shared: one round of workgroups after the other as long as each
 // fills the chip; the tiles that are left over share the chip among them.
 constexpr int kUnits = 256;  // compute units
@@ -476,6 +555,10 @@ inline GemmPlan gemm_plan(int64_t M, int64_t J, int64_t C) {
     return best;
 }
 
+// k_fp8_rows: one token x [7168, 5120] 8.0 us, x [55296, 5120] 40.8 (6.9 TB/s), 16 tokens 10.7 and 52;
+// in tiles 14.5 and 55, and 15.2 and 59 (nn has no such form: its tiles' rows are what is contracted)
+inline bool by_rows(int64_t M, int32_t nn) { return !nn && M <= 16; }
+
 template <typename T, bool NN, int STAGES>
 inline void launch_tiles(const GemmArgs &g, hipStream_t stream) {
     const int64_t rest = (int64_t)g.tiles_m * g.tiles_j - g.whole;
@@ -500,7 +583,8 @@ using namespace pulse;
 
 extern "C" {
 
-int64_t pulse_fp8_gemm_ws_size(int64_t M, int64_t J, int64_t C) {
+int64_t pulse_fp8_gemm_ws_size(int64_t M, int64_t J, int64_t C, int32_t nn) {
+    if (by_rows(M, nn)) return 0;
     const GemmPlan p = gemm_plan(M, J, C);
     return (p.tiles_m * p.tiles_j - p.whole) * p.shares * p.bm * p.bj * 4;
 }
@@ -513,8 +597,15 @@ int pulse_launch_fp8_gemm(const uint8_t *x, const float *sx, const uint8_t *w, c
     const GemmArgs g{x, w, sx, sw, bias, y, static_cast<f32x4 *>(ws), ldy, (int32_t)M, (int32_t)J, (int32_t)C, (int32_t)k,
                      (int32_t)((C + GB - 1) / GB), nn ? 1 : (int32_t)gk, nn ? (int32_t)gk : 1, (int32_t)p.tiles_m,
                      (int32_t)p.tiles_j, (int32_t)((C + GB - 1) / GB), p.whole, p.shares, p.per};
-    if (nn) launch_gemm<true>(p, g, stream);
-    else launch_gemm<false>(p, g, stream);
+    if (by_rows(M, nn)) {
+        const dim3 grid((unsigned)((n + 15) / 16));
+        if (M <= 8) k_fp8_rows<8, 8, 3><<<grid, dim3(512), 0, stream>>>(g);
+        else k_fp8_rows<16, 4, 4><<<grid, dim3(256), 0, stream>>>(g);
+    } else if (nn) {
+        launch_gemm<true>(p, g, stream);
+    } else {
+        launch_gemm<false>(p, g, stream);
+    }
     return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 }
