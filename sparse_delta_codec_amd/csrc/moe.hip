@@ -46,19 +46,20 @@ __global__ __launch_bounds__(256) void k_moe_route(const float *__restrict__ log
         v[i] = e < E ? logits[(int64_t)t * ld + e] : 0.0f;
         key[i] = e < E ? ordered(v[i]) : 0u;
     }
-    float most = 0, sum = 0;
-    int mine = -1;      // lane j: the j-th choice and its logit
-    float chosen = 0;
+    float most = 0, sum = 0, chosen = 0;
+    int mine = -1;  // lane j: the j-th choice; chosen: its logit
     for (int j = 0; j < top_k; ++j) {
         uint32_t best = 0;
         int at = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (key[i] > best) best = key[i], at = i;
-        const uint32_t top = wave_reduce_max(best);
+        const uint32_t top = __builtin_amdgcn_readlane(wave_incl_max(best), 63);
         // of the lanes that hold it, the lowest index: the lowest place first, then the lowest lane
-        const uint32_t tie = best == top ? (uint32_t)(at * kWave + lane) : 0xFFFFFFFFu;
-        const uint32_t e = ~wave_reduce_max(~tie);
+        const uint32_t mine_at = (uint32_t)(at * kWave + lane), tie = best == top ? mine_at : 0xFFFFFFFFu;
+        const uint64_t ties = __ballot(best == top);
+        const uint32_t e = (ties & (ties - 1)) ? ~(uint32_t)__builtin_amdgcn_readlane(wave_incl_max(~tie), 63)
+                                               : (uint32_t)__builtin_amdgcn_readlane(mine_at, __builtin_ctzll(ties));
         const bool live = top > kMinusInf;  // an expert with -inf is not chosen
         if (lane == j) mine = live ? (int)e : -1;
         const uint32_t bits = top & 0x80000000u ? top ^ 0x80000000u : ~top;
@@ -138,16 +139,20 @@ struct MoeArgs {
     const float *sw;     // [E][blocks of R][blocks of K]
     uint16_t *h;         // up: written
     float *out;          // down: [pairs][R], written
+    const int32_t *ids;  // [pairs]
     MoePlan plan;
     int32_t P, E, R, K;  // R: rows of w (up: 2 I)
     int32_t top_k;
-    int32_t kw;          // waves that share the contraction: 1, 2 or 4
+    int32_t kw;          // few: waves that share the contraction: 1, 2 or 4
+    uint32_t *status;
 };
 
-constexpr int MW = 4;          // waves of a workgroup
-constexpr int MR = 32;         // rows of a wave: 16 of gate and of up, or 32 of down
-constexpr int MS = 256;        // columns of a step
+constexpr int MW = 4;   // waves of a workgroup
+constexpr int MR = 32;  // rows of a wave: 16 of gate and of up, or 32 of down
 
+typedef const __attribute__((address_space(4))) float *scalar_floats;
+
+// A lane's operand of 16 x 16 x 32: eight codes as BF16 (exactly: E4M3 has four bits)
 __device__ __forceinline__ bf16x8 widen_codes(uint32_t lo, uint32_t hi) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
@@ -157,38 +162,86 @@ __device__ __forceinline__ bf16x8 widen_codes(uint32_t lo, uint32_t hi) {
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// A step's buffer in LDS: the rows of codes of every wave, and NX rows of x (down: twice,
-// h's two parts) for all of them (SHARED) or for each.  Piece p (16 bytes) of row r lies at
-// p ^ (r & 15), where neither the loads, which fill whole rows, nor the reads, 16 rows at
-// one piece, have two lanes in a bank.
-template <bool UP, int NX, bool SHARED>
-struct MoeStage {
-    static constexpr int parts = UP ? 1 : 2;
-    static constexpr int w_bytes = MR * MS, x_bytes = parts * NX * MS * 2;
-    static constexpr int x_copies = SHARED ? 1 : MW;
-    static constexpr int bytes = MW * w_bytes + x_copies * x_bytes;
-    static constexpr int w_loads = w_bytes / 1024, x_loads = x_bytes / 1024 / (SHARED ? MW : 1);
-    static constexpr int loads = w_loads + x_loads;
-    static constexpr int stages = 3 * bytes <= 160 * 1024 && SHARED ? 3 : 2;
-    static_assert(x_loads * 1024 * (SHARED ? MW : 1) == x_bytes && stages * bytes <= 160 * 1024, "LDS of a compute unit");
-    static_assert((stages - 2) * loads <= 63, "loads in flight");
+// The n-th set bit (n < popcount)
+__device__ __forceinline__ int nth_bit(uint64_t m, int n) {
+    for (int i = 0; i < n; ++i) m &= m - 1;
+    return __builtin_ctzll(m);
+}
+
+// An item: an expert (or -1) and its pairs: bits of `few`, or order[first ...].
+struct MoeItem {
+    int expert, count, first;
+    uint64_t few;
 };
 
-template <bool UP, int NX, bool SHARED>
-__global__ __launch_bounds__(MW *kWave) void k_moe_rows(MoeArgs g) {
-    using S = MoeStage<UP, NX, SHARED>;
-    constexpr int CT = (NX + 15) / 16;  // tiles of tokens
-    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[S::stages * S::bytes];
-    const int item = blockIdx.y;
-    if (item >= g.plan.count[0]) return;
+__device__ __forceinline__ MoeItem planned_item(const MoeArgs &g, int item, int nx) {
+    MoeItem t{-1, 0, 0, 0};
+    if (item >= g.plan.count[0]) return t;
     const int e = g.plan.expert[item], p0 = g.plan.first[item];
     int np = g.plan.first[item + 1] - p0;
     // (whatever the plan's buffer holds, nothing outside the tensors is touched)
-    if ((uint32_t)e >= (uint32_t)g.E || (uint32_t)p0 >= (uint32_t)g.P || np <= 0) return;
-    np = np < NX ? np : NX;
-    np = np < g.P - p0 ? np : g.P - p0;
+    if ((uint32_t)e >= (uint32_t)g.E || (uint32_t)p0 >= (uint32_t)g.P || np <= 0) return t;
+    np = np < nx ? np : nx;
+    return {e, np < g.P - p0 ? np : g.P - p0, p0, 0};
+}
+
+// Without a plan: up to 64 pairs, a lane's each.  Items go by the first pair of their expert.
+__device__ __forceinline__ MoeItem few_item(const MoeArgs &g, int item, int nx) {
+    const int lane = lane_id(), id = lane < g.P ? g.ids[lane] : -1;
+    const bool live = (uint32_t)id < (uint32_t)g.E;
+    if (item == 0 && blockIdx.x == 0 && !live && id != -1) atomicOr(g.status, 2u);  // PULSE_DS_BADINDEX
+    uint64_t left = __ballot(live);
+    while (left) {
+        const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        uint64_t same = __ballot(live && id == e);
+        left &= ~same;
+        for (; same; --item) {  // up to nx of them make an item
+            uint64_t part = same;
+            for (int i = 0; i < nx && same; ++i) same &= same - 1;
+            part &= ~same;
+            if (item == 0) return {e, __builtin_popcountll(part), 0, part};
+        }
+    }
+    return {-1, 0, 0, 0};
+}
+
+// A step's buffer in LDS: the rows of codes of every wave, and NX rows of x (down: twice,
+// h's two parts), for all of them or, with one or two tokens (FEW), for each.  Two workgroups
+// a compute unit, so that one begins while the other is under way, where LDS holds them.
+// Piece p (16 bytes) of row r lies at p ^ r's low bits, where neither the loads, which fill
+// whole rows, nor the reads, 8 rows at one piece, have two lanes in a bank.
+template <bool UP, int NX, bool FEW>
+struct MoeStage {
+    static constexpr int parts = UP ? 1 : 2;
+    static constexpr int cols = NX <= 8 || (NX == 16 && UP) ? 256 : 128;  // of a step
+    static constexpr int w_bytes = MR * cols, x_bytes = parts * NX * cols * 2;
+    static constexpr int bytes = MW * w_bytes + (FEW ? MW : 1) * x_bytes;
+    static constexpr int wp = cols / 16, xp = cols / 8;        // pieces of a row
+    static constexpr int w_rows = 64 / wp, x_rows = 64 / xp;   // rows of a load
+    static constexpr int w_loads = w_bytes / 1024, x_loads = x_bytes / 1024 / (FEW ? 1 : MW);
+    static constexpr int loads = w_loads + x_loads;
+    static constexpr int half = 80 * 1024;                     // of a compute unit's LDS
+    static constexpr int stages = 4 * bytes <= half ? 4 : 3 * bytes <= half ? 3 : 2 * bytes <= half ? 2 : 3;
+    static constexpr int waves = stages * bytes <= half ? 2 : 1;  // of a SIMD
+    static_assert(x_loads * 1024 * (FEW ? 1 : MW) == x_bytes && stages * bytes <= 2 * half, "LDS of a compute unit");
+    static_assert((stages - 2) * loads <= 63, "loads in flight");
+};
+
+template <bool UP, int NX, bool FEW>
+__global__ __launch_bounds__(MW *kWave, (MoeStage<UP, NX, FEW>::waves)) void k_moe_rows(MoeArgs g) {
+    using S = MoeStage<UP, NX, FEW>;
+    constexpr int CT = (NX + 15) / 16;  // tiles of tokens
+    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[S::stages * S::bytes];
+    const MoeItem item = FEW ? few_item(g, blockIdx.y, NX) : planned_item(g, blockIdx.y, NX);
+    if (item.expert < 0) return;
+    const int e = __builtin_amdgcn_readfirstlane(item.expert), np = item.count;
+    const auto pair_of = [&](int n) {  // n < np
+        if (FEW) return nth_bit(item.few, n);
+        const int p = g.plan.order[item.first + n];
+        return (uint32_t)p < (uint32_t)g.P ? p : 0;
+    };
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id()), c16 = lane & 15, q = lane >> 4;
-    const int kw = SHARED ? 1 : g.kw;
+    const int kw = FEW ? g.kw : 1;
     const int half = g.R / 2;                               // up: gate's rows
     const int tile = (int)blockIdx.x * (MW / kw) + wave / kw, share = wave % kw;
     const int tiles = UP ? half / 16 : (g.R + MR - 1) / MR;
@@ -197,55 +250,43 @@ __global__ __launch_bounds__(MW *kWave) void k_moe_rows(MoeArgs g) {
     const int row0 = live ? (UP ? tile * 16 : tile * MR) : 0;
     const bool two = UP || row0 + 16 < g.R;
     const int row1 = UP ? half + row0 : two ? row0 + 16 : row0;
-    const int kb = (g.K + 127) / 128, steps = (g.K + MS - 1) / MS;
-    const uint8_t *w0 = load_base(g.w + ((int64_t)e * g.R + row0) * g.K + share * MS);
-    const uint8_t *w1 = load_base(g.w + ((int64_t)e * g.R + row1) * g.K + share * MS);
-    const uint16_t *xb = load_base(g.x + share * MS);
-    const float *const sw = g.sw + (int64_t)e * ((g.R + 127) / 128) * kb;
-    const float *const sw0 = sw + (int64_t)(row0 / 128) * kb, *const sw1 = sw + (int64_t)(row1 / 128) * kb;
+    const int kb = (g.K + 127) / 128, steps = (g.K + S::cols - 1) / S::cols;
+    const uint8_t *const w0 = load_base(g.w + ((int64_t)e * g.R + row0) * g.K);
+    const uint8_t *const w1 = load_base(g.w + ((int64_t)e * g.R + row1) * g.K);
+    const uint16_t *const xb = load_base(g.x);
+    const scalar_floats sw = (scalar_floats)(uint64_t)g.sw + (int64_t)e * ((g.R + 127) / 128) * kb;
+    const scalar_floats sw0 = sw + (int64_t)(row0 / 128) * kb, sw1 = sw + (int64_t)(row1 / 128) * kb;
 
     uint32_t wo[S::w_loads / 2], xo[S::x_loads];
+    const auto w_row = [&](int i) { return i * S::w_rows + lane / S::wp; };
+    const auto w_piece = [&](int i) { return (lane % S::wp) ^ (w_row(i) % S::wp); };
+    const auto x_row = [&](int i) { return ((FEW ? 0 : wave * S::x_loads) + i) * S::x_rows + lane / S::xp; };
+    const auto x_piece = [&](int i) { return (lane % S::xp) ^ (x_row(i) % NX % 16); };
 #pragma unroll
-    for (int i = 0; i < S::w_loads / 2; ++i) {
-        const int r = i * 4 + (lane >> 4);
-        wo[i] = (uint32_t)r * (uint32_t)g.K + (uint32_t)(c16 ^ r) * 16;
-    }
-    const auto x_row = [&](int i) { return ((SHARED ? wave * S::x_loads : 0) + i) * 2 + (lane >> 5); };
+    for (int i = 0; i < S::w_loads / 2; ++i) wo[i] = (uint32_t)w_row(i) * (uint32_t)g.K;
 #pragma unroll
     for (int i = 0; i < S::x_loads; ++i) {
-        const int r = x_row(i), c = r % NX;
-        int pair = g.plan.order[p0 + (c < np ? c : np - 1)];
-        if ((uint32_t)pair >= (uint32_t)g.P) pair = 0;
+        const int r = x_row(i), c = r % NX, pair = pair_of(c < np ? c : np - 1);
         const uint32_t row = UP ? (uint32_t)(pair / g.top_k) : (uint32_t)(r / NX * g.P + pair);
-        xo[i] = row * (uint32_t)g.ldx * 2 + (uint32_t)((lane & 31) ^ (c & 15)) * 16;
+        xo[i] = row * (uint32_t)g.ldx * 2;
     }
     const uint32_t mem = __builtin_amdgcn_readfirstlane(lds_at(s_mem));
-    const uint32_t w_at = wave * S::w_bytes, x_at = MW * S::w_bytes + (SHARED ? 0 : wave * S::x_bytes);
+    const uint32_t w_at = wave * S::w_bytes, x_at = MW * S::w_bytes + (FEW ? wave * S::x_bytes : 0);
     // a step's loads; pieces past the end of a row are taken from its beginning (x's are cleared below)
     const auto issue = [&](int s, int turn) {
-        const uint32_t at = mem + (uint32_t)(turn % S::stages) * S::bytes;
-        const int left = g.K - s * MS;
+        const uint32_t at = mem + (uint32_t)(turn % S::stages) * S::bytes, c = (uint32_t)s * S::cols;
+        const int left = g.K - s * S::cols;
 #pragma unroll
         for (int i = 0; i < S::w_loads; ++i) {
-            uint32_t o = wo[i % (S::w_loads / 2)];
-            if (left < MS) {
-                const int p = c16 ^ (i % (S::w_loads / 2) * 4 + (lane >> 4));
-                if (p * 16 >= left) o -= p * 16;
-            }
-            load_lds16_once(at + w_at + i * 1024, i < S::w_loads / 2 ? w0 : w1, o);
+            const int p = w_piece(i % (S::w_loads / 2)) * 16;
+            load_lds16_once(at + w_at + i * 1024, i < S::w_loads / 2 ? w0 : w1,
+                            wo[i % (S::w_loads / 2)] + c + (p < left ? p : 0));
         }
 #pragma unroll
         for (int i = 0; i < S::x_loads; ++i) {
-            uint32_t o = xo[i];
-            if (left < MS) {
-                const int p = (lane & 31) ^ (x_row(i) % NX & 15);
-                if (p * 8 >= left) o -= p * 16;
-            }
-            load_lds16(at + x_at + ((SHARED ? wave * S::x_loads : 0) + i) * 1024, xb, o);
+            const int p = x_piece(i) * 8;
+            load_lds16(at + x_at + ((FEW ? 0 : wave * S::x_loads) + i) * 1024, xb, xo[i] + (c + (p < left ? p : 0)) * 2);
         }
-        w0 += kw * MS;
-        w1 += kw * MS;
-        xb += kw * MS;
     };
 
     f32x4 acc[2][CT];
@@ -253,30 +294,31 @@ __global__ __launch_bounds__(MW *kWave) void k_moe_rows(MoeArgs g) {
     for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[t][c] = f32x4{0, 0, 0, 0};
-    int ahead = share, turns = 0;
+    int ahead = share, turns = 0, turn = 0;
     for (int i = 0; i < S::stages - 1; ++i, ahead += kw)
         if (ahead < steps) issue(ahead, turns++);
-    int turn = 0;
     for (int s = share; s < steps; s += kw, ++turn) {
         if (turns - turn >= S::stages - 1 && S::stages > 2) wait_loads<(S::stages - 2) * S::loads>();
         else wait_loads<0>();
-        if (SHARED) lds_barrier();
-        else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last step's reads are done
+        if (FEW) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last step's reads are done
+        else lds_barrier();
         uint8_t *const buf = s_mem + (turn % S::stages) * S::bytes;
         uint8_t *const bx = buf + x_at;
-        if (g.K - s * MS < MS) {  // the ragged end
-            const int from = (g.K - s * MS) / 8, gone = MS / 8 - from;
-            for (int i = SHARED ? (int)threadIdx.x : lane; i < S::parts * NX * gone; i += SHARED ? MW * kWave : kWave) {
+        if (g.K - s * S::cols < S::cols) {  // the ragged end
+            const int from = (g.K - s * S::cols) / 8, gone = S::xp - from;
+            for (int i = FEW ? lane : (int)threadIdx.x; i < S::parts * NX * gone; i += FEW ? kWave : MW * kWave) {
                 const int r = i / gone, p = from + i % gone;
-                *reinterpret_cast<u32x4 *>(bx + r * MS * 2 + (p ^ (r % NX & 15)) * 16) = u32x4{0, 0, 0, 0};
+                *reinterpret_cast<u32x4 *>(bx + r * S::cols * 2 + (p ^ (r % NX % 16)) * 16) = u32x4{0, 0, 0, 0};
             }
-            if (SHARED) lds_barrier();
+            if (!FEW) lds_barrier();
         }
         if (ahead < steps) issue(ahead, turns++);
         ahead += kw;
         const uint8_t *const bw = buf + w_at;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < S::cols / 128; ++b) {
+            const int at = s * (S::cols / 128) + b < kb ? s * (S::cols / 128) + b : kb - 1;
+            const float f0 = sw0[at], f1 = sw1[at];
             f32x4 p[2][CT];
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -288,7 +330,8 @@ __global__ __launch_bounds__(MW *kWave) void k_moe_rows(MoeArgs g) {
                 bf16x8 a[2][2];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(bw + (t * 16 + c16) * MS + (piece ^ c16) * 16);
+                    const u32x4 v =
+                        *reinterpret_cast<const u32x4 *>(bw + (t * 16 + c16) * S::cols + (piece ^ (c16 % S::wp)) * 16);
                     a[t][0] = widen_codes(v[0], v[1]);
                     a[t][1] = widen_codes(v[2], v[3]);
                 }
@@ -300,15 +343,13 @@ __global__ __launch_bounds__(MW *kWave) void k_moe_rows(MoeArgs g) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const bf16x8 xv = *reinterpret_cast<const bf16x8 *>(
-                                bx + (part * NX + r) * MS * 2 + ((2 * piece + k) ^ (r & 15)) * 16);
+                                bx + (part * NX + r) * S::cols * 2 + ((2 * piece + k) ^ (r % 16)) * 16);
 #pragma unroll
                             for (int t = 0; t < 2; ++t)
                                 p[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t][k], xv, p[t][c], 0, 0, 0);
                         }
                     }
             }
-            const int at = 2 * s + b < kb ? 2 * s + b : kb - 1;
-            const float f0 = sw0[at], f1 = sw1[at];
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
@@ -318,7 +359,7 @@ __global__ __launch_bounds__(MW *kWave) void k_moe_rows(MoeArgs g) {
                 }
         }
     }
-    if (!SHARED && kw > 1) {  // the waves' shares, in their order
+    if (FEW && kw > 1) {  // the waves' shares, in their order
         __syncthreads();
         f32x4 *const sums = reinterpret_cast<f32x4 *>(s_mem);
 #pragma unroll
@@ -338,8 +379,7 @@ __global__ __launch_bounds__(MW *kWave) void k_moe_rows(MoeArgs g) {
     for (int c = 0; c < CT; ++c) {
         const int place = c * 16 + c16;
         if (place >= np) continue;
-        const int pair = g.plan.order[p0 + place];
-        if ((uint32_t)pair >= (uint32_t)g.P) continue;
+        const int pair = pair_of(place);
         if constexpr (UP) {
             float h[4], rest[4];
 #pragma unroll
@@ -357,6 +397,116 @@ __global__ __launch_bounds__(MW *kWave) void k_moe_rows(MoeArgs g) {
             if (two) *reinterpret_cast<f32x4 *>(out + 16) = acc[1][c];
         }
     }
+}
+
+// One or two tokens: a workgroup makes 16 columns of y whole.  Its waves take the live pairs in
+// turn, 16 rows of the pair's down and the two parts of its h as two columns of the matrix
+// instruction, a pair's first steps on their way while the last one's end is multiplied.
+constexpr int FD_STAGES = 3;
+
+__global__ __launch_bounds__(MW *kWave) void k_moe_few_down(MoeArgs g, const float *__restrict__ weights, int32_t T,
+                                                           uint16_t *__restrict__ y, int64_t ldy) {
+    constexpr int cols = 256, w_bytes = 16 * cols, bytes = w_bytes + 1024, loads = 5;
+    __shared__ __attribute__((aligned(1024))) uint8_t s_mem[MW * FD_STAGES * bytes];
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id()), c16 = lane & 15, q = lane >> 4;
+    const int row0 = (int)blockIdx.x * 16, kb = (g.K + 127) / 128, steps = (g.K + cols - 1) / cols;
+    const int id = lane < g.P ? g.ids[lane] : -1;
+    const float weight = lane < g.P ? weights[lane] : 0.0f;
+    const uint64_t pairs = __ballot((uint32_t)id < (uint32_t)g.E);
+    const int n = __builtin_popcountll(pairs), mine = n > wave ? (n - wave + MW - 1) / MW : 0;
+    const uint8_t *const wb = load_base(g.w);
+    const uint16_t *const xb = load_base(g.x);
+    uint8_t *const buf = s_mem + wave * FD_STAGES * bytes;
+    const uint32_t mem = __builtin_amdgcn_readfirstlane(lds_at(buf));
+    uint32_t wo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wo[i] = (uint32_t)(i * 4 + (lane >> 4)) * (uint32_t)g.K;
+    const int xr = lane >> 5;  // part of h
+
+    // what is to be loaded next: step ls of pair lp (the wave's li-th)
+    int li = 0, ls = 0, lp = mine ? nth_bit(pairs, wave) : 0;
+    const auto issue = [&](int turn) {
+        const uint32_t at = mem + (uint32_t)(turn % FD_STAGES) * bytes;
+        const int e = __builtin_amdgcn_readlane(id, lp), left = g.K - ls * cols;
+        const uint8_t *const base = load_base(wb + ((int64_t)e * g.R + row0) * g.K + ls * cols);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = (c16 ^ (i * 4 + (lane >> 4))) * 16;
+            load_lds16_once(at + i * 1024, base, wo[i] + (p < left ? p : 0));
+        }
+        const int p = ((lane & 31) ^ xr) * 8;
+        load_lds16(at + w_bytes, xb, ((uint32_t)(xr * g.P + lp) * (uint32_t)g.K + ls * cols + (p < left ? p : 0)) * 2);
+        if (++ls == steps) {
+            ls = 0;
+            if (++li < mine) lp = nth_bit(pairs, wave + li * MW);
+        }
+    };
+    const int total = mine * steps;
+    int turns = 0;
+    while (turns < FD_STAGES - 1 && turns < total) issue(turns), ++turns;
+    f32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // of token 0 and 1
+    int turn = 0;
+    for (int i = 0; i < mine; ++i) {
+        const int pair = nth_bit(pairs, wave + i * MW), e = __builtin_amdgcn_readlane(id, pair);
+        const scalar_floats sw =
+            (scalar_floats)(uint64_t)g.sw + ((int64_t)e * ((g.R + 127) / 128) + row0 / 128) * kb;
+        f32x4 acc = {0, 0, 0, 0};
+        for (int s = 0; s < steps; ++s, ++turn) {
+            if (turns < total) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last step's reads are done: its buffer is free
+                issue(turns), ++turns;
+                wait_loads<(FD_STAGES - 1) * loads>();
+            } else {
+                wait_loads<0>();
+            }
+            uint8_t *const at = buf + (turn % FD_STAGES) * bytes, *const bx = at + w_bytes;
+            if (g.K - s * cols < cols) {
+                const int from = (g.K - s * cols) / 8, gone = 32 - from;
+                for (int k = lane; k < 2 * gone; k += kWave) {
+                    const int r = k / gone, p = from + k % gone;
+                    *reinterpret_cast<u32x4 *>(bx + r * 512 + (p ^ r) * 16) = u32x4{0, 0, 0, 0};
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                f32x4 p = {0, 0, 0, 0};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int piece = b * 8 + h * 4 + q, r = c16 & 1;
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(at + c16 * cols + (piece ^ c16) * 16);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const bf16x8 xv = *reinterpret_cast<const bf16x8 *>(bx + r * 512 + ((2 * piece + k) ^ r) * 16);
+                        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_codes(v[2 * k], v[2 * k + 1]), xv, p, 0, 0, 0);
+                    }
+                }
+                const float f = sw[2 * s + b < kb ? 2 * s + b : kb - 1];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(f, p[k], acc[k]);
+            }
+        }
+        const float share = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), pair));
+        const int t = pair / g.top_k;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            // (columns 0 and 1 are the products of h's parts)
+            const float both = acc[k] + __shfl_xor(acc[k], 1, kWave);
+            if (t == 0) sum[0][k] = __builtin_fmaf(share, both, sum[0][k]);
+            else sum[1][k] = __builtin_fmaf(share, both, sum[1][k]);
+        }
+    }
+    __syncthreads();
+    f32x4 *const sums = reinterpret_cast<f32x4 *>(s_mem);
+    if (c16 == 0)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) sums[(wave * 2 + t) * 4 + q] = sum[t];
+    __syncthreads();
+    if (threadIdx.x >= 8) return;
+    const int t = threadIdx.x >> 2, quarter = threadIdx.x & 3;
+    if (t >= T) return;
+    f32x4 v = sums[t * 4 + quarter];
+    for (int w = 1; w < MW; ++w) v += sums[(w * 2 + t) * 4 + quarter];
+    *reinterpret_cast<u32x2 *>(y + (int64_t)t * ldy + row0 + quarter * 4) = u32x2{cast_pair(v[0], v[1]), cast_pair(v[2], v[3])};
 }
 
 // y = the sum over a token's choices, in their order: a thread takes four columns
@@ -394,10 +544,23 @@ inline MoeWs moe_ws(int64_t P, int64_t H, int64_t I) {
     return w;
 }
 
-// Pairs of an item
-inline int moe_nx(int64_t T, int64_t P, int64_t E) {
-    if (T <= 2) return 2;
-    return P > 16 * E ? 32 : 16;
+// Pairs of an item, by the average of an expert.  (EDIT: figures)
+inline int moe_nx(int64_t P, int64_t E) { return P <= 5 * E ? 8 : P <= 12 * E ? 16 : P <= 24 * E ? 32 : 64; }
+
+// One or two tokens: the choices fit a wave.
+inline bool moe_few(int64_t T, int64_t P) { return T <= 2 && P <= kWave; }
+
+template <int NX, bool FEW>
+inline void launch_up(const MoeArgs &g, unsigned items, hipStream_t stream) {
+    const unsigned per = MW / g.kw, tiles = (unsigned)(g.R / 2 / 16);
+    k_moe_rows<true, NX, FEW><<<dim3((tiles + per - 1) / per, items), dim3(MW * kWave), 0, stream>>>(g);
+}
+
+template <int NX>
+inline void launch_both(const MoeArgs &u, const MoeArgs &d, unsigned items, hipStream_t stream) {
+    launch_up<NX, false>(u, items, stream);
+    const unsigned tiles = (unsigned)((d.R + MR - 1) / MR);
+    k_moe_rows<false, NX, false><<<dim3((tiles + MW - 1) / MW, items), dim3(MW * kWave), 0, stream>>>(d);
 }
 
 }  // namespace pulse
@@ -426,33 +589,26 @@ int pulse_launch_moe_forward(const uint16_t *x, int64_t ldx, const int32_t *ids,
     char *const mem = static_cast<char *>(ws);
     int32_t *const words = reinterpret_cast<int32_t *>(mem);
     const MoePlan plan{words, words + 1, words + 1 + P, reinterpret_cast<int32_t *>(mem + at.order)};
-    const int nx = moe_nx(T, P, E);
-    const int64_t items = std::min<int64_t>(P, E + P / nx);
-    k_moe_plan<<<dim3(1), dim3(1024), 0, stream>>>(ids, (int32_t)P, (int32_t)E, nx, plan, status);
     uint16_t *const h = reinterpret_cast<uint16_t *>(mem + at.h);
     float *const out = reinterpret_cast<float *>(mem + at.out);
-    MoeArgs u{x, ldx, up, up_scales, h, nullptr, plan, (int32_t)P, (int32_t)E, (int32_t)(2 * I), (int32_t)H,
-              (int32_t)top_k, 1};
-    MoeArgs d{h, I, down, down_scales, nullptr, out, plan, (int32_t)P, (int32_t)E, (int32_t)H, (int32_t)I,
-              (int32_t)top_k, 1};
-    if (nx == 2) {
-        u.kw = H >= 4096 ? 4 : 1;
-        d.kw = I >= 4096 ? 4 : 1;
+    MoeArgs u{x, ldx, up, up_scales, h, nullptr, ids, plan, (int32_t)P, (int32_t)E, (int32_t)(2 * I), (int32_t)H,
+              (int32_t)top_k, 1, status};
+    MoeArgs d{h, I, down, down_scales, nullptr, out, ids, plan, (int32_t)P, (int32_t)E, (int32_t)H, (int32_t)I,
+              (int32_t)top_k, 1, status};
+    if (moe_few(T, P)) {
+        u.kw = H >= 4096 ? 4 : H >= 2048 ? 2 : 1;
+        launch_up<2, true>(u, (unsigned)P, stream);
+        k_moe_few_down<<<dim3((unsigned)(H / 16)), dim3(MW * kWave), 0, stream>>>(d, weights, (int32_t)T, y, ldy);
+        return hipGetLastError() == hipSuccess ? 0 : -5;
     }
-    const auto grid = [&](int64_t tiles, int kw) {
-        const int64_t per = MW / kw;
-        return dim3((unsigned)((tiles + per - 1) / per), (unsigned)items);
-    };
-    const dim3 gu = grid(I / 16, u.kw), gd = grid((H + MR - 1) / MR, d.kw), block(MW * kWave);
-    if (nx == 2) {
-        k_moe_rows<true, 2, false><<<gu, block, 0, stream>>>(u);
-        k_moe_rows<false, 2, false><<<gd, block, 0, stream>>>(d);
-    } else if (nx == 16) {
-        k_moe_rows<true, 16, true><<<gu, block, 0, stream>>>(u);
-        k_moe_rows<false, 16, true><<<gd, block, 0, stream>>>(d);
-    } else {
-        k_moe_rows<true, 32, true><<<gu, block, 0, stream>>>(u);
-        k_moe_rows<false, 32, true><<<gd, block, 0, stream>>>(d);
+    const int nx = moe_nx(P, E);
+    const unsigned items = (unsigned)std::min<int64_t>(P, E + P / nx);
+    k_moe_plan<<<dim3(1), dim3(1024), 0, stream>>>(ids, (int32_t)P, (int32_t)E, nx, plan, status);
+    switch (nx) {
+    case 8: launch_both<8>(u, d, items, stream); break;
+    case 16: launch_both<16>(u, d, items, stream); break;
+    case 32: launch_both<32>(u, d, items, stream); break;
+    default: launch_both<64>(u, d, items, stream); break;
     }
     k_moe_join<<<dim3((unsigned)((T * H / 4 + 255) / 256)), dim3(256), 0, stream>>>(out, ids, weights, (int32_t)T,
                                                                                     (int32_t)top_k, (int32_t)E,
