@@ -147,7 +147,6 @@ struct MoeArgs {
     uint32_t *status;
 };
 
-constexpr int MW = 4;   // waves of a workgroup
 constexpr int MR = 32;  // rows of a wave: 16 of gate and of up, or 32 of down
 
 typedef const __attribute__((address_space(4))) float *scalar_floats;
@@ -212,6 +211,7 @@ __device__ __forceinline__ MoeItem few_item(const MoeArgs &g, int item, int nx) 
 // whole rows, nor the reads, 8 rows at one piece, have two lanes in a bank.
 template <bool UP, int NX, bool FEW>
 struct MoeStage {
+    static constexpr int MW = NX >= 64 ? 8 : 4;  // waves: eight share the largest x
     static constexpr int parts = UP ? 1 : 2;
     static constexpr int cols = NX <= 8 || (NX == 16 && UP) ? 256 : 128;  // of a step
     static constexpr int w_bytes = MR * cols, x_bytes = parts * NX * cols * 2;
@@ -220,16 +220,16 @@ struct MoeStage {
     static constexpr int w_rows = 64 / wp, x_rows = 64 / xp;   // rows of a load
     static constexpr int w_loads = w_bytes / 1024, x_loads = x_bytes / 1024 / (FEW ? 1 : MW);
     static constexpr int loads = w_loads + x_loads;
-    static constexpr int half = 80 * 1024;                     // of a compute unit's LDS
-    static constexpr int stages = 4 * bytes <= half ? 4 : 3 * bytes <= half ? 3 : 2 * bytes <= half ? 2 : 3;
-    static constexpr int waves = stages * bytes <= half ? 2 : 1;  // of a SIMD
-    static_assert(x_loads * 1024 * (FEW ? 1 : MW) == x_bytes && stages * bytes <= 2 * half, "LDS of a compute unit");
+    static constexpr int lds = MW == 8 ? 160 * 1024 : 80 * 1024;  // of a workgroup
+    static constexpr int stages = 4 * bytes <= lds ? 4 : 3 * bytes <= lds ? 3 : 2;
+    static_assert(x_loads * 1024 * (FEW ? 1 : MW) == x_bytes && stages * bytes <= lds, "LDS of a compute unit");
     static_assert((stages - 2) * loads <= 63, "loads in flight");
 };
 
 template <bool UP, int NX, bool FEW>
-__global__ __launch_bounds__(MW *kWave, (MoeStage<UP, NX, FEW>::waves)) void k_moe_rows(MoeArgs g) {
+__global__ __launch_bounds__((MoeStage<UP, NX, FEW>::MW * kWave), 2) void k_moe_rows(MoeArgs g) {
     using S = MoeStage<UP, NX, FEW>;
+    constexpr int MW = S::MW;
     constexpr int CT = (NX + 15) / 16;  // tiles of tokens
     __shared__ __attribute__((aligned(1024))) uint8_t s_mem[S::stages * S::bytes];
     const MoeItem item = FEW ? few_item(g, blockIdx.y, NX) : planned_item(g, blockIdx.y, NX);
@@ -402,11 +402,11 @@ __global__ __launch_bounds__(MW *kWave, (MoeStage<UP, NX, FEW>::waves)) void k_m
 // One or two tokens: a workgroup makes 16 columns of y whole.  Its waves take the live pairs in
 // turn, 16 rows of the pair's down and the two parts of its h as two columns of the matrix
 // instruction, a pair's first steps on their way while the last one's end is multiplied.
-constexpr int FD_STAGES = 3;
+constexpr int FD_STAGES = 3, FD_WAVES = 4;
 
-__global__ __launch_bounds__(MW *kWave) void k_moe_few_down(MoeArgs g, const float *__restrict__ weights, int32_t T,
+__global__ __launch_bounds__(FD_WAVES *kWave) void k_moe_few_down(MoeArgs g, const float *__restrict__ weights, int32_t T,
                                                            uint16_t *__restrict__ y, int64_t ldy) {
-    constexpr int cols = 256, w_bytes = 16 * cols, bytes = w_bytes + 1024, loads = 5;
+    constexpr int MW = FD_WAVES, cols = 256, w_bytes = 16 * cols, bytes = w_bytes + 1024, loads = 5;
     __shared__ __attribute__((aligned(1024))) uint8_t s_mem[MW * FD_STAGES * bytes];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id()), c16 = lane & 15, q = lane >> 4;
     const int row0 = (int)blockIdx.x * 16, kb = (g.K + 127) / 128, steps = (g.K + cols - 1) / cols;
@@ -544,23 +544,27 @@ inline MoeWs moe_ws(int64_t P, int64_t H, int64_t I) {
     return w;
 }
 
-// Pairs of an item, by the average of an expert.  (EDIT: figures)
-inline int moe_nx(int64_t P, int64_t E) { return P <= 5 * E ? 8 : P <= 12 * E ? 16 : P <= 24 * E ? 32 : 64; }
+// Pairs of an item, by an expert's average: more of them, and most experts are read once; fewer,
+// and less of LDS and of the columns is empty.  Microseconds with items of 8, 16, 32 and 64:
+// 1.9 a expert (30 tokens, top 4 of 64 x (4096, 2048)) 246, 250, 257, 331; 4 a expert (61, 4 of 60 x
+// (2048, 1408)) 98, 94, 99, 124; 8 a expert (64, 4 of 32 x (4096, 2048)) 181, 167, 179, 198; 16 a expert
+// (128 tokens) 247, 202, 171, 202; 32 a expert (128, 4 of 16) 202, 149, 128, 113.
+inline int moe_nx(int64_t P, int64_t E) { return P <= 2 * E ? 8 : P <= 10 * E ? 16 : P <= 20 * E ? 32 : 64; }
 
 // One or two tokens: the choices fit a wave.
 inline bool moe_few(int64_t T, int64_t P) { return T <= 2 && P <= kWave; }
 
-template <int NX, bool FEW>
-inline void launch_up(const MoeArgs &g, unsigned items, hipStream_t stream) {
-    const unsigned per = MW / g.kw, tiles = (unsigned)(g.R / 2 / 16);
-    k_moe_rows<true, NX, FEW><<<dim3((tiles + per - 1) / per, items), dim3(MW * kWave), 0, stream>>>(g);
+template <bool UP, int NX, bool FEW>
+inline void launch_rows(const MoeArgs &g, unsigned items, hipStream_t stream) {
+    constexpr int waves = MoeStage<UP, NX, FEW>::MW;
+    const unsigned tiles = (unsigned)(UP ? g.R / 2 / 16 : (g.R + MR - 1) / MR), per = (unsigned)(waves / g.kw);
+    k_moe_rows<UP, NX, FEW><<<dim3((tiles + per - 1) / per, items), dim3(waves * kWave), 0, stream>>>(g);
 }
 
 template <int NX>
 inline void launch_both(const MoeArgs &u, const MoeArgs &d, unsigned items, hipStream_t stream) {
-    launch_up<NX, false>(u, items, stream);
-    const unsigned tiles = (unsigned)((d.R + MR - 1) / MR);
-    k_moe_rows<false, NX, false><<<dim3((tiles + MW - 1) / MW, items), dim3(MW * kWave), 0, stream>>>(d);
+    launch_rows<true, NX, false>(u, items, stream);
+    launch_rows<false, NX, false>(d, items, stream);
 }
 
 }  // namespace pulse
@@ -597,8 +601,8 @@ int pulse_launch_moe_forward(const uint16_t *x, int64_t ldx, const int32_t *ids,
               (int32_t)top_k, 1, status};
     if (moe_few(T, P)) {
         u.kw = H >= 4096 ? 4 : H >= 2048 ? 2 : 1;
-        launch_up<2, true>(u, (unsigned)P, stream);
-        k_moe_few_down<<<dim3((unsigned)(H / 16)), dim3(MW * kWave), 0, stream>>>(d, weights, (int32_t)T, y, ldy);
+        launch_rows<true, 2, true>(u, (unsigned)P, stream);
+        k_moe_few_down<<<dim3((unsigned)(H / 16)), dim3(FD_WAVES * kWave), 0, stream>>>(d, weights, (int32_t)T, y, ldy);
         return hipGetLastError() == hipSuccess ? 0 : -5;
     }
     const int nx = moe_nx(P, E);
