@@ -1026,29 +1026,69 @@ def _scratch(nbytes, what, device):
     return torch.empty((max(nbytes, 16) + 15) // 16 * 16, dtype=torch.uint8, device=device)
 
 
-def _dense(t, shape, dtypes, name):
-    """The data pointer of a contiguous GPU tensor of this shape and one of these types."""
-    try:
-        if t.shape == shape and t.is_cuda and t.dtype in dtypes and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
+_F32, _I32T = (torch.float32,), (torch.int32,)
+
+
+# These calls too are made once per projection and batch: a tensor's checks stand in one
+# expression (get_device() is -1 for one that is not on a GPU), and only when it fails are they
+# gone through for the message.
+def _refuse(t, shape, dtypes, name, device, rows=False):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtypes}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on GPU {t.get_device()}, the first operand on {device}")
+    raise ValueError(f"{name} must have contiguous rows" if rows else f"{name} must be contiguous")
 
 
-_F32, _I32T = (torch.float32,), (torch.int32,)
+def _dense(t, shape, dtypes, name, device):
+    """The data pointer of a contiguous tensor of this shape and one of these types on the device."""
+    try:
+        if t.shape == shape and t.get_device() == device and t.dtype in dtypes and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, shape, dtypes, name, device)
 
 
-def _launch_stream(t, stream):
-    """The handle of the stream to launch on; the operands' device must be the stream's (the
-    current one's)."""
-    device = t.get_device()
+def _strided(t, rows, cols, name, device):
+    """The data pointer and row stride of a BF16 [rows, cols] with contiguous columns on the device."""
+    try:
+        if t.shape == (rows, cols) and t.get_device() == device and t.dtype in _U16:
+            row, col = t.stride()
+            if col == 1 or cols <= 1 or rows == 0:
+                return t.data_ptr(), row if rows > 1 else cols
+    except AttributeError:
+        pass
+    _refuse(t, (rows, cols), _U16, name, device, rows=True)
+
+
+def _scratch_of(ws, device):
+    if ws is None:
+        return None, 0
+    if ws.get_device() != device or not ws.is_contiguous():
+        _refuse(ws, ws.shape, (ws.dtype,), "ws", device)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _first(t, name, dims=2):
+    """The device and the sizes of a tensor that the other operands go by."""
+    try:
+        shape, device = t.shape, t.get_device()
+        if len(shape) == dims and device >= 0:
+            return device, shape
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {dims} dimensions")
+
+
+def _launch_stream(device, stream):
+    """The handle of the stream to launch on, which is one of the operands' device."""
     if stream is None:
         current = _get_device()
         if current is not None and current != device:
@@ -1057,13 +1097,6 @@ def _launch_stream(t, stream):
     if stream.device_index != device:
         raise ValueError(f"operands are on GPU {device}, the stream is of {stream.device_index}")
     return stream.cuda_stream
-
-
-def _same_device(first, *others):
-    device = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"operands are on GPUs {device} and {t.get_device()}")
 
 
 def rms_norm_workspace(n_tokens, cols, device="cuda"):
@@ -1076,16 +1109,15 @@ def pulse_rms_norm(x, weight, eps=1e-6, residual=None, y=None, codes=None, scale
     x, which the residual then holds.  The output goes to y (BF16), to codes [tokens, cols]
     and scales [tokens, ceil(cols / 128)] (E4M3), or to both; rstd [tokens] keeps what the backward
     pass needs."""
-    t, n = x.shape
-    px, ldx = _rows(x, t, n, "x")
-    pw = _dense(weight, (n,), _U16, "weight")
-    pr, ldr = (None, 0) if residual is None else _rows(residual, t, n, "residual")
-    py, ldy = (None, 0) if y is None else _rows(y, t, n, "y")
-    pc = None if codes is None else _dense(codes, (t, n), _CODES, "codes")
-    ps = None if scales is None else _dense(scales, (t, -(-n // 128)), _F32, "scales")
-    pd = None if rstd is None else _dense(rstd, (t,), _F32, "rstd")
-    _same_device(x, weight, residual, y, codes, scales, rstd)
-    rc = _lib.pulse_rms_norm(px, ldx, pw, eps, pr, ldr, py, ldy, pc, ps, pd, t, n, _launch_stream(x, stream))
+    d, (t, n) = _first(x, "x")
+    px, ldx = _strided(x, t, n, "x", d)
+    pw = _dense(weight, (n,), _U16, "weight", d)
+    pr, ldr = (None, 0) if residual is None else _strided(residual, t, n, "residual", d)
+    py, ldy = (None, 0) if y is None else _strided(y, t, n, "y", d)
+    pc = None if codes is None else _dense(codes, (t, n), _CODES, "codes", d)
+    ps = None if scales is None else _dense(scales, (t, (n + 127) // 128), _F32, "scales", d)
+    pd = None if rstd is None else _dense(rstd, (t,), _F32, "rstd", d)
+    rc = _lib.pulse_rms_norm(px, ldx, pw, eps, pr, ldr, py, ldy, pc, ps, pd, t, n, _launch_stream(d, stream))
     if rc:
         _check(rc, "pulse_rms_norm")
 
@@ -1095,17 +1127,16 @@ def pulse_rms_norm_backward(s, weight, rstd, dy, dx, dweight, ws, dres=None, acc
     (the updated residual, or x); dx (None: not wanted) is that of x and of the residual, dres
     what reaches it by the residual's way; dweight [cols] float32 is written or, with accumulate,
     added to."""
-    t, n = s.shape
-    p, lds = _rows(s, t, n, "s")
-    pdy, lddy = _rows(dy, t, n, "dy")
-    pdr, lddr = (None, 0) if dres is None else _rows(dres, t, n, "dres")
-    pdx, lddx = (None, 0) if dx is None else _rows(dx, t, n, "dx")
-    pw, pd = _dense(weight, (n,), _U16, "weight"), _dense(rstd, (t,), _F32, "rstd")
-    pdw = _dense(dweight, (n,), _F32, "dweight")
-    wsp, wsb = _ws(ws)
-    _same_device(s, weight, rstd, dy, dx, dweight, ws, dres)
-    rc = _lib.pulse_rms_norm_backward(p, lds, pw, pd, pdy, lddy, pdr, lddr, pdx, lddx, pdw, int(accumulate), t, n, wsp,
-                                      wsb, _launch_stream(s, stream))
+    d, (t, n) = _first(s, "s")
+    p, lds = _strided(s, t, n, "s", d)
+    pdy, lddy = _strided(dy, t, n, "dy", d)
+    pdr, lddr = (None, 0) if dres is None else _strided(dres, t, n, "dres", d)
+    pdx, lddx = (None, 0) if dx is None else _strided(dx, t, n, "dx", d)
+    pw, pr = _dense(weight, (n,), _U16, "weight", d), _dense(rstd, (t,), _F32, "rstd", d)
+    pdw = _dense(dweight, (n,), _F32, "dweight", d)
+    wsp, wsb = _scratch_of(ws, d)
+    rc = _lib.pulse_rms_norm_backward(p, lds, pw, pr, pdy, lddy, pdr, lddr, pdx, lddx, pdw, int(accumulate), t, n, wsp,
+                                      wsb, _launch_stream(d, stream))
     if rc:
         _check(rc, "pulse_rms_norm_backward")
 
@@ -1113,11 +1144,10 @@ def pulse_rms_norm_backward(s, weight, rstd, dy, dx, dweight, ws, dres=None, acc
 def fp8_group_quant(x, codes, scales, glu=False, stream=None):
     """E4M3 codes [tokens, cols] of x [tokens, cols] BF16 and their scales for each 128 columns
     of a row; with glu of silu(gate) * up, x = [gate, up]."""
-    t, n = codes.shape
-    px, ldx = _rows(x, t, 2 * n if glu else n, "x")
-    pc, ps = _dense(codes, (t, n), _CODES, "codes"), _dense(scales, (t, -(-n // 128)), _F32, "scales")
-    _same_device(x, codes, scales)
-    rc = _lib.fp8_group_quant(px, ldx, t, n, int(glu), pc, ps, _launch_stream(x, stream))
+    d, (t, n) = _first(codes, "codes")
+    px, ldx = _strided(x, t, 2 * n if glu else n, "x", d)
+    pc, ps = _dense(codes, (t, n), _CODES, "codes", d), _dense(scales, (t, (n + 127) // 128), _F32, "scales", d)
+    rc = _lib.fp8_group_quant(px, ldx, t, n, int(glu), pc, ps, _launch_stream(d, stream))
     if rc:
         _check(rc, "fp8_group_quant")
 
@@ -1134,18 +1164,18 @@ def fp8_block_gemm(x, x_scales, w, w_scales, y, ws=None, bias=None, form="nt", s
     """y (BF16) = x w^T + bias ("nt": x [m, k], y [m, n]) or x w ("nn": x [m, n], y [m, k]): x E4M3 codes
     with a scale for each 128 columns of a row, w [n, k] codes with one for each 128 x 128 block."""
     nn = _FORMS[form]
-    n, k = w.shape
-    m, (inner, out) = x.shape[0], ((n, k) if nn else (k, n))
+    d, (n, k) = _first(w, "w")
+    inner, out = (n, k) if nn else (k, n)
     if nn and bias is not None:
         raise ValueError("a bias goes with form 'nt'")
-    px, psx = _dense(x, (m, inner), _CODES, "x"), _dense(x_scales, (m, -(-inner // 128)), _F32, "x_scales")
-    pw = _dense(w, (n, k), _CODES, "w")
-    psw = _dense(w_scales, (-(-n // 128), -(-k // 128)), _F32, "w_scales")
-    py, ldy = _rows(y, m, out, "y")
-    pb = None if bias is None else _dense(bias, (n,), _U16, "bias")
-    wsp, wsb = _ws(ws)
-    _same_device(x, x_scales, w, w_scales, y, ws, bias)
-    rc = _lib.fp8_block_gemm(px, psx, pw, psw, pb, nn, m, n, k, py, ldy, wsp, wsb, _launch_stream(x, stream))
+    m = _first(x, "x")[1][0]
+    px, psx = _dense(x, (m, inner), _CODES, "x", d), _dense(x_scales, (m, (inner + 127) // 128), _F32, "x_scales", d)
+    pw = _dense(w, (n, k), _CODES, "w", d)
+    psw = _dense(w_scales, ((n + 127) // 128, (k + 127) // 128), _F32, "w_scales", d)
+    py, ldy = _strided(y, m, out, "y", d)
+    pb = None if bias is None else _dense(bias, (n,), _U16, "bias", d)
+    wsp, wsb = _scratch_of(ws, d)
+    rc = _lib.fp8_block_gemm(px, psx, pw, psw, pb, nn, m, n, k, py, ldy, wsp, wsb, _launch_stream(d, stream))
     if rc:
         _check(rc, "fp8_block_gemm")
 
@@ -1154,14 +1184,13 @@ def pulse_moe_route(logits, ids, weights, over_all=False, scale=1.0, stream=None
     """Each token's experts from its logits [tokens, experts] float32: ids [tokens, top_k] int32 by
     descending logit (-1 where only logits of -inf are left) and weights float32, the softmax over
     the chosen ones (over_all: over all experts) times scale."""
-    t, e = logits.shape
-    k = ids.shape[1]
-    if not logits.is_cuda or logits.dtype is not torch.float32 or (logits.stride(1) != 1 and e > 1):
+    d, (t, e) = _first(logits, "logits")
+    if logits.dtype is not torch.float32 or (logits.stride(1) != 1 and e > 1):
         raise ValueError("logits must be a float32 GPU tensor with contiguous rows")
-    pi, pw = _dense(ids, (t, k), _I32T, "ids"), _dense(weights, (t, k), _F32, "weights")
-    _same_device(logits, ids, weights)
+    k = _first(ids, "ids")[1][1]
+    pi, pw = _dense(ids, (t, k), _I32T, "ids", d), _dense(weights, (t, k), _F32, "weights", d)
     rc = _lib.pulse_moe_route(logits.data_ptr(), logits.stride(0) if t > 1 else e, t, e, k, int(over_all), scale, pi, pw,
-                              _launch_stream(logits, stream))
+                              _launch_stream(d, stream))
     if rc:
         _check(rc, "pulse_moe_route")
 
@@ -1175,20 +1204,18 @@ def pulse_moe_forward(x, ids, weights, up, up_scales, down, down_scales, y, d_st
     """y [tokens, hidden] = the chosen experts' outputs for x, by weights [tokens, top_k]: up [experts,
     2 inter, hidden] holds gate's rows, then up's; down [experts, hidden, inter]; both E4M3 codes with a
     scale for each 128 x 128 block of an expert."""
-    t, h = x.shape
-    e, hh, i = down.shape
-    k = ids.shape[1]
-    px, ldx = _rows(x, t, h, "x")
-    py, ldy = _rows(y, t, h, "y")
-    pi, pp = _dense(ids, (t, k), _I32T, "ids"), _dense(weights, (t, k), _F32, "weights")
-    pu, pd = _dense(up, (e, 2 * i, h), _CODES, "up"), _dense(down, (e, h, i), _CODES, "down")
-    psu = _dense(up_scales, (e, -(-2 * i // 128), -(-h // 128)), _F32, "up_scales")
-    psd = _dense(down_scales, (e, -(-h // 128), -(-i // 128)), _F32, "down_scales")
-    wsp, wsb = _ws(ws)
-    _need(d_status, 4, "d_status")
-    st = _dev(d_status, "d_status", torch.int32)
-    _same_device(x, ids, weights, up, up_scales, down, down_scales, y, d_status, ws)
+    d, (t, h) = _first(x, "x")
+    e, _, i = _first(down, "down", 3)[1]
+    k = _first(ids, "ids")[1][1]
+    px, ldx = _strided(x, t, h, "x", d)
+    py, ldy = _strided(y, t, h, "y", d)
+    pi, pp = _dense(ids, (t, k), _I32T, "ids", d), _dense(weights, (t, k), _F32, "weights", d)
+    pu, pd = _dense(up, (e, 2 * i, h), _CODES, "up", d), _dense(down, (e, h, i), _CODES, "down", d)
+    psu = _dense(up_scales, (e, (2 * i + 127) // 128, (h + 127) // 128), _F32, "up_scales", d)
+    psd = _dense(down_scales, (e, (h + 127) // 128, (i + 127) // 128), _F32, "down_scales", d)
+    wsp, wsb = _scratch_of(ws, d)
+    st = _dense(d_status, (1,), _I32T, "d_status", d)
     rc = _lib.pulse_moe_forward(px, ldx, pi, pp, pu, psu, pd, psd, t, h, i, e, k, py, ldy, st, wsp, wsb,
-                                _launch_stream(x, stream))
+                                _launch_stream(d, stream))
     if rc:
         _check(rc, "pulse_moe_forward")
