@@ -43,15 +43,18 @@ struct GemmArgs {
 // and 64 columns of every 128 (which have one scale a step).  A step's 128 columns of x and
 // W lie in LDS, put there while earlier steps are multiplied.
 //
-// In LDS a row of 128 bytes is eight pieces of 16, and piece p of row r lies at
-// p ^ swap(r).  A wave's matrix operand for four tiles of 16 columns takes row
-// 16 a + 4 t + b of its 64 as row 4 a + b of tile t: a lane's results of the four tiles
-// are then 16 neighbouring columns.  Within a tile, a and b vary, and swap() goes by
-// their low three bits, so that the eight lanes which read at once are in eight places.
-__device__ __forceinline__ int swap_piece(int r) { return (r & 3) | ((r >> 2) & 4); }
-
-// nn: rows are steps of the contraction, 128 bytes of columns each; piece p of row r lies
-// at p ^ (r & 7), so that the eight rows of a transposing read are in eight places.
+// In LDS a row of 128 bytes is eight pieces of 16, and piece p of row r lies at p ^ swap(r):
+// two rows fill the 64 banks, and the sixteen rows that a matrix operand takes at one piece are
+// to be in sixteen places.
+//  x: rows 16 m .. 16 m + 15, so swap goes by bits 1 to 3.
+//  W: a wave's operand for four tiles of 16 columns takes row 16 a + 4 t + b of its 64 as row
+//     4 a + b of tile t, which makes a lane's results of the four tiles 16 neighbouring columns; a
+//     and b vary within a tile, so swap goes by bits 1, 4 and 5.
+//  W (nn): rows are steps of the contraction, and a transposing read takes eight of them.
+// (By bits 0, 1 and 4 for both, reads of x met in banks four at a time: 8192 x [55296, 5120] 2280 us.)
+__device__ __forceinline__ int swap_x(int r) { return (r >> 1) & 7; }
+template <bool NN>
+__device__ __forceinline__ int swap_w(int r) { return NN ? r & 7 : ((r >> 1) & 1) | ((r >> 3) & 6); }
 
 template <int BM_, int BJ_, int WM_>
 struct Tile {
@@ -172,7 +175,7 @@ struct Loads {
     static __device__ __forceinline__ int row(int lane, int i, int n) { return (uniform_wave() * n + i) * 8 + (lane >> 3); }
     static __device__ __forceinline__ int uniform_wave() { return __builtin_amdgcn_readfirstlane(wave_id()); }
     static __device__ __forceinline__ int piece(int lane, int r, bool w) {
-        return (lane & 7) ^ (NN && w ? r & 7 : swap_piece(r));
+        return (lane & 7) ^ (w ? swap_w<NN>(r) : swap_x(r));
     }
     // The lane's number for what only a last step needs: the compiler does not see that it could be
     // worked out before the loop, and held in registers that the loop does not have.
@@ -279,16 +282,16 @@ __device__ __forceinline__ void clear_end(uint8_t *x, int left) {
     asm volatile("" : "+v"(thread));  // as rare_lane
     for (int i = thread; i < T::BM * gone; i += T::threads) {
         const int r = i / gone, p = from + i % gone;
-        *reinterpret_cast<u32x4 *>(x + r * GB + (p ^ swap_piece(r)) * 16) = u32x4{0, 0, 0, 0};
+        *reinterpret_cast<u32x4 *>(x + r * GB + (p ^ swap_x(r)) * 16) = u32x4{0, 0, 0, 0};
     }
     lds_barrier();
 }
 
 // Row r of a step as a matrix operand: lane group q has columns 16 q .. + 15 and 64 + 16 q .. + 15.
-__device__ __forceinline__ i32x8 row_operand(const uint8_t *at, int r) {
+__device__ __forceinline__ i32x8 row_operand(const uint8_t *at, int r, int swap) {
     const int q = lane_id() >> 4;
-    const u32x4 lo = *reinterpret_cast<const u32x4 *>(at + r * GB + (q ^ swap_piece(r)) * 16);
-    const u32x4 hi = *reinterpret_cast<const u32x4 *>(at + r * GB + ((q + 4) ^ swap_piece(r)) * 16);
+    const u32x4 lo = *reinterpret_cast<const u32x4 *>(at + r * GB + (q ^ swap) * 16);
+    const u32x4 hi = *reinterpret_cast<const u32x4 *>(at + r * GB + ((q + 4) ^ swap) * 16);
     i32x8 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = lo[i], v[i + 4] = hi[i];
@@ -307,12 +310,13 @@ __device__ __forceinline__ i32x8 w_operand(const uint8_t *at, int wj, int t) {
         for (int h = 0; h < 4; ++h) {
             const int r = (h >> 1) * 64 + q * 16 + (h & 1) * 8 + (c16 >> 1);
             const i32x2 u = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                (lds2)(uintptr_t)lds_at(at + r * GB + ((wj * 4 + t) ^ (r & 7)) * 16 + (c16 & 1) * 8));
+                (lds2)(uintptr_t)lds_at(at + r * GB + ((wj * 4 + t) ^ swap_w<NN>(r)) * 16 + (c16 & 1) * 8));
             v[2 * h] = u[0], v[2 * h + 1] = u[1];
         }
         return v;
     } else {
-        return row_operand(at, wj * 64 + (c16 >> 2) * 16 + t * 4 + (c16 & 3));
+        const int r = wj * 64 + (c16 >> 2) * 16 + t * 4 + (c16 & 3);
+        return row_operand(at, r, swap_w<NN>(r));
     }
 }
 
@@ -418,7 +422,7 @@ __global__ __launch_bounds__(T::threads) void k_fp8_tile(GemmArgs g) {
 #pragma unroll
         for (int m = 0; m < T::mt; ++m) {
             const int r = wm * T::tm + m * 16 + c16;
-            x[m] = row_operand(at, r);
+            x[m] = row_operand(at, r, swap_x(r));
             sx[m] = scale[r * 4 + late[m]];
         }
         float f[T::parts][T::mt];
@@ -452,7 +456,7 @@ __global__ __launch_bounds__(NW *kWave) void k_fp8_rows(GemmArgs g) {
     const uint8_t *const wb = load_base(g.w + (int64_t)n0 * g.K), *const xb = load_base(g.x);
     const float *const sb = load_base(g.sx);
     const scalar_floats sw = (scalar_floats)(uint64_t)g.sw + (int64_t)(n0 / GB) * g.gwj;
-    const int r8 = lane >> 3, piece = (lane & 7) ^ (r8 & 7);  // of rows r8 and r8 + 8
+    const int r8 = lane >> 3, pieces[2] = {(lane & 7) ^ swap_x(r8), (lane & 7) ^ swap_x(r8 + 8)};  // of rows r8 and r8 + 8
     const uint32_t wo[2] = {(clamped(n0 + r8, g.J) - n0) * (uint32_t)g.K, (clamped(n0 + r8 + 8, g.J) - n0) * (uint32_t)g.K};
     const uint32_t xo[2] = {clamped(r8, g.M) * (uint32_t)g.K, clamped(r8 + 8, g.M) * (uint32_t)g.K};
     const uint32_t so = clamped(c16, g.M) * (uint32_t)g.gx * 4;
@@ -460,12 +464,15 @@ __global__ __launch_bounds__(NW *kWave) void k_fp8_rows(GemmArgs g) {
     const uint32_t mem = __builtin_amdgcn_readfirstlane(lds_at(mine));
     const auto issue = [&](int s, int turn) {
         const uint32_t at = mem + (uint32_t)(turn % D) * stage;
-        const uint32_t left = (uint32_t)(g.K - s * GB), p = (uint32_t)piece * 16 < left ? piece * 16 : 0;
-        const uint32_t c = (uint32_t)s * GB + p;
-        load_lds16_once(at, wb, wo[0] + c);
-        load_lds16_once(at + 1024, wb, wo[1] + c);
+        const int left = g.K - s * GB;
+        uint32_t c[2];
 #pragma unroll
-        for (int i = 0; i < xi; ++i) load_lds16(at + w_bytes + i * 1024, xb, xo[i] + c);
+        for (int i = 0; i < 2; ++i) {
+            c[i] = (uint32_t)(s * GB + (pieces[i] * 16 < left ? pieces[i] * 16 : 0));
+            load_lds16_once(at + i * 1024, wb, wo[i] + c[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < xi; ++i) load_lds16(at + w_bytes + i * 1024, xb, xo[i] + c[i]);
         load_lds4(at + w_bytes + x_bytes, sb, so + (uint32_t)s * 4);
     };
     f32x4 acc = {0, 0, 0, 0};
@@ -486,17 +493,10 @@ __global__ __launch_bounds__(NW *kWave) void k_fp8_rows(GemmArgs g) {
             const int from = (g.K - s * GB) / 16, gone = 8 - from;
             for (int i = lane; i < NX * gone; i += kWave) {
                 const int r = i / gone, p = from + i % gone;
-                *reinterpret_cast<u32x4 *>(at + w_bytes + r * GB + (p ^ (r & 7)) * 16) = u32x4{0, 0, 0, 0};
+                *reinterpret_cast<u32x4 *>(at + w_bytes + r * GB + (p ^ swap_x(r)) * 16) = u32x4{0, 0, 0, 0};
             }
         }
-        const auto operand = [&](const uint8_t *m, int r) {
-            const u32x4 lo = *reinterpret_cast<const u32x4 *>(m + r * GB + (q ^ (r & 7)) * 16);
-            const u32x4 hi = *reinterpret_cast<const u32x4 *>(m + r * GB + ((q + 4) ^ (r & 7)) * 16);
-            i32x8 v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = lo[i], v[i + 4] = hi[i];
-            return v;
-        };
+        const auto operand = [&](const uint8_t *m, int r) { return row_operand(m, r, swap_x(r)); };
         const float f = reinterpret_cast<const float *>(at + w_bytes + x_bytes)[lane] * sw[(int64_t)s * g.gwc];
         const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(at, c16), operand(at + w_bytes, c16 % NX),
                                                                          f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
