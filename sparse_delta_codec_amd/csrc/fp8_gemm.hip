@@ -323,7 +323,7 @@ __device__ __forceinline__ i32x8 w_operand(const uint8_t *at, int wj, int t) {
 // acc += f * (W x): products are added LAG matrix instructions after theirs was issued, while the
 // next tile's operand is read beside this tile's products.
 template <typename T, bool NN>
-__device__ __forceinline__ void multiply(const uint8_t *w, int wj, const i32x8 (&x)[T::mt], const float (&f)[T::parts][T::mt],
+__device__ __forceinline__ void multiply(const uint8_t *w, int wj, const i32x8 &first, const i32x8 (&x)[T::mt], const float (&f)[T::parts][T::mt],
                                          f32x4 (&acc)[T::parts * 4][T::mt]) {
     constexpr int LAG = T::mt < 4 ? T::mt : 4, N = T::parts * 4 * T::mt;
     i32x8 wf[2];
@@ -334,7 +334,7 @@ __device__ __forceinline__ void multiply(const uint8_t *w, int wj, const i32x8 (
         for (int i = 0; i < 4; ++i) a[i] = __builtin_fmaf(f[n / T::mt / 4][n % T::mt], p[n % (LAG + 1)][i], a[i]);
     };
     const auto operand = [&](int t) { return w_operand<NN>(w + (t >> 2) * T::w_bytes, wj, t & 3); };
-    wf[0] = operand(0);
+    wf[0] = first;
 #pragma unroll
     for (int t = 0; t < T::parts * 4; ++t) {
         if (t + 1 < T::parts * 4) wf[(t + 1) & 1] = operand(t + 1);
@@ -404,7 +404,25 @@ __global__ __launch_bounds__(T::threads) void k_fp8_tile(GemmArgs g) {
         for (int m = 0; m < T::mt; ++m) acc[t][m] = f32x4{0, 0, 0, 0};
 
     for (int s = k.s0; s < k.s0 + STAGES - 1 && s < k.s1; ++s) issue(s);
+    // W's scales of 64 steps, a lane's each: a step takes its own without waiting for a load
+    float sw[T::parts];
+    const bool end = Loads<T, NN>::near_end(g, m0);
     for (int s = k.s0; s < k.s1; ++s) {
+        if (((s - k.s0) & 63) == 0) {
+            const int64_t at = s + lane_id() < g.steps ? s + lane_id() : g.steps - 1;
+#pragma unroll
+            for (int p = 0; p < T::parts; ++p)  // (a tile's last part may lie past the last column)
+                sw[p] = g.sw[(int64_t)(j0 / GB + p < blocks ? j0 / GB + p : blocks - 1) * g.gwj + at * g.gwc];
+#pragma unroll
+            for (int p = 0; p < T::parts; ++p) asm volatile("" : "+v"(sw[p]));  // waited for here, not in every step
+        }
+        int place[T::mt];
+#pragma unroll
+        for (int m = 0; m < T::mt; ++m) {
+            const int r = wm * T::tm + m * 16 + c16;
+            place[m] = r * 4 + (s & 3);
+            if (end) place[m] += Loads<T, NN>::late(g, m0 + r, s);
+        }
         // (a step may have loaded scales too, as its first load: that is then waited for as well)
         if (s + STAGES - 2 < k.s1) wait_loads<(STAGES - 2) * loads>();
         else wait_loads<0>();
@@ -412,29 +430,26 @@ __global__ __launch_bounds__(T::threads) void k_fp8_tile(GemmArgs g) {
         uint8_t *const at = s_mem + ((s - k.s0) % STAGES) * stage;
         if (g.C - s * GB < GB) clear_end<T>(at, g.C - s * GB);
         if (s + STAGES - 1 < k.s1) issue(s + STAGES - 1);
-        const float *const scale = reinterpret_cast<const float *>(s_mem + s_at + (s / 4 & 1) * T::s_bytes) + (s & 3);
+        sched_fence();
+        const float *const scale = reinterpret_cast<const float *>(s_mem + s_at + (s / 4 & 1) * T::s_bytes);
         i32x8 x[T::mt];
-        float sx[T::mt];
-        int late[T::mt] = {};
-        if (Loads<T, NN>::near_end(g, m0))
-#pragma unroll
-            for (int m = 0; m < T::mt; ++m) late[m] = Loads<T, NN>::late(g, m0 + wm * T::tm + m * 16 + c16, s);
+        float f[T::parts][T::mt];
+        const i32x8 w0 = w_operand<NN>(at + T::x_bytes, wj, 0);
 #pragma unroll
         for (int m = 0; m < T::mt; ++m) {
             const int r = wm * T::tm + m * 16 + c16;
             x[m] = row_operand(at, r, swap_x(r));
-            sx[m] = scale[r * 4 + late[m]];
         }
-        float f[T::parts][T::mt];
 #pragma unroll
-        for (int p = 0; p < T::parts; ++p) {
-            // (a tile's last part may lie past the last column)
-            const int block = j0 / GB + p < blocks ? j0 / GB + p : blocks - 1;
-            const float sw = ((scalar_floats)(uint64_t)g.sw)[(int64_t)block * g.gwj + (int64_t)s * g.gwc];
+        for (int m = 0; m < T::mt; ++m) f[0][m] = scale[place[m]];
+        sched_fence();
 #pragma unroll
-            for (int m = 0; m < T::mt; ++m) f[p][m] = sx[m] * sw;
+        for (int p = T::parts - 1; p >= 0; --p) {
+            const float b = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw[p]), (s - k.s0) & 63));
+#pragma unroll
+            for (int m = 0; m < T::mt; ++m) f[p][m] = f[0][m] * b;
         }
-        multiply<T, NN>(at + T::x_bytes, wj, x, f, acc);
+        multiply<T, NN>(at + T::x_bytes, wj, w0, x, f, acc);
     }
     store_results<T, NN>(g, k, m0, j0, acc);
 }
