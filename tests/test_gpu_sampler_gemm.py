@@ -145,3 +145,67 @@ def test_repeats_bit_for_bit(m):
 def test_no_tokens():
     x, sx, w, sw = problem(3, 128, 128, "nt")
     assert multiply(x[:0], sx[:0], w, sw, "nt").shape == (0, 128)
+
+
+# rows, columns of y and contraction that make each size of tile, alone, shared, both at once, and
+# one row of tiles: 256 x 256, 256 x 128, 128 x 128 and 64 x 128
+TILES = [(900, 8208, 144), (2000, 8208, 528), (900, 5136, 8208), (4100, 1000 + 8, 144), (1500, 1008, 8208), (2000, 8208, 144),
+         (250, 8208, 8208), (250, 8208, 144), (1500, 512, 4112), (70, 4112, 8208), (4100, 4112, 144), (70, 256, 144), (70, 8208, 144),
+         (250, 8208, 4112), (4099, 4112, 1040)]
+
+
+@pytest.mark.parametrize("form", ["nt", "nn"])
+@pytest.mark.parametrize("m,j,c", TILES)
+def test_each_tile_holds_whole_numbers(m, j, c, form):
+    """Whole numbers up to 8 by 8 that the sums hold exactly, over every row and column."""
+    n, k = (j, c) if form == "nt" else (c, j)
+    gen = torch.Generator(device="cuda").manual_seed(m + j + c)
+    whole = lambda *s: torch.randint(-8, 9, s, device="cuda", generator=gen).float()  # noqa: E731
+    power = lambda *s: torch.pow(2.0, torch.randint(-1, 2, s, device="cuda", generator=gen).float())  # noqa: E731
+    x, w = whole(m, c), whole(n, k)
+    sx, sw = power(m, ref.groups(c)), power(ref.groups(n), ref.groups(k))
+    y = torch.full((m + 1, j), -77.0, dtype=torch.bfloat16, device="cuda")
+    codes = lambda t: t.to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+    ws = pulse.fp8_gemm_workspace(m, n, k, form)
+    ws.fill_(255)
+    pulse.fp8_block_gemm(codes(x), sx, codes(w), sw, y[:m], ws, form=form)
+    wide = lambda s, d, size: s.repeat_interleave(128, d).narrow(d, 0, size)  # noqa: E731
+    xv = (x * wide(sx, 1, c)).double()
+    wv = (w * wide(wide(sw, 0, n), 1, k)).double()
+    want = xv @ (wv.t() if form == "nt" else wv)
+    assert torch.equal(y[:m], want.to(torch.bfloat16))
+    assert (y[m] == -77).all()
+
+
+@pytest.mark.parametrize("form", ["nt", "nn"])
+@pytest.mark.parametrize("m,j,c", [(900, 8208, 144), (2000, 2064, 1040), (1500, 1008, 8208), (70, 4112, 8208), (250, 1040, 4112)])
+def test_tiles_of_any_values(m, j, c, form):
+    """Some rows of larger products against float64."""
+    n, k = (j, c) if form == "nt" else (c, j)
+    x, sx, w, sw = problem(m, n, k, form, 12)
+    rows = np.unique(np.r_[0, 1, 15, 16, 63, 64, m - 2, m - 1, np.random.default_rng(m).integers(0, m, 24)])
+    y, e = ref.gemm(x[rows], sx[rows], w, sw, form)
+    check(multiply(x, sx, w, sw, form)[rows], y, e)
+
+
+def test_offsets_past_31_bits():
+    """Weights and output of more than 2^31 elements: the last rows and columns are right."""
+    n, k, m = 1 << 17, 16400, 16
+    w = torch.zeros((n, k), dtype=torch.uint8, device="cuda")  # 2.15e9 codes
+    sw = torch.ones((ref.groups(n), ref.groups(k)), device="cuda")
+    w[n - 1, k - 1], w[n - 1, 0], w[n - 130, k - 200], w[0, 5] = 0x38, 0x40, 0x38, 0x38  # 1, 2, 1, 1
+    x = torch.zeros((m, k), dtype=torch.uint8, device="cuda")
+    x[:, k - 1], x[:, 0], x[3, k - 200], x[:, 5] = 0x38, 0x40, 0x44, 0x38
+    sx = torch.ones((m, ref.groups(k)), device="cuda")
+    for rows in (m, 40):
+        xs, ss = (x, sx) if rows == m else (torch.cat([x, x, x])[:rows].contiguous(), torch.ones((rows, ref.groups(k)), device="cuda"))
+        y = torch.empty((rows, n), dtype=torch.bfloat16, device="cuda")
+        pulse.fp8_block_gemm(xs, ss, w, sw, y, pulse.fp8_gemm_workspace(rows, n, k))
+        assert (y[:, n - 1] == 5).all() and (y[:, 0] == 1).all() and y[3, n - 130] == 3 and y[2, n - 130] == 0
+        assert int((y != 0).sum()) == 2 * rows + sum(r % m == 3 for r in range(rows))
+    # nn: a contraction over those rows
+    dy = torch.zeros((8, n), dtype=torch.uint8, device="cuda")
+    dy[:, n - 1], dy[2, 0] = 0x38, 0x38
+    dx = torch.empty((8, k), dtype=torch.bfloat16, device="cuda")
+    pulse.fp8_block_gemm(dy, torch.ones((8, ref.groups(n)), device="cuda"), w, sw, dx, pulse.fp8_gemm_workspace(8, n, k, "nn"), form="nn")
+    assert (dx[:, k - 1] == 1).all() and (dx[:, 0] == 2).all() and dx[2, 5] == 1 and int((dx != 0).sum()) == 17

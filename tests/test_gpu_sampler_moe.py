@@ -158,3 +158,49 @@ def test_no_tokens():
     for a in range(3):
         args[a] = args[a][:0]
     assert forward(*args).shape == (0, 64)
+
+
+@pytest.mark.parametrize("t,e,k", [(1, 40, 32), (2, 40, 32), (2, 3, 3), (3, 33, 32), (100, 50, 1), (70, 300, 2), (300, 5, 2), (1000, 3, 2)])
+def test_crowded_experts(t, e, k):
+    """Nearly all tokens at one expert: many items of it, and most experts without any."""
+    args = list(layer(t, 144, 48, e, k, 11))
+    g = np.random.default_rng(t)
+    args[1][g.random(args[1].shape) < 0.9] = min(7, e - 1)
+    check(forward(*args), *ref.moe(*args))
+
+
+def test_routed_tokens_end_to_end():
+    """The router's choice fed on: an expert with -inf is left out, a token with nothing but -inf has zeros."""
+    t, e, k = 50, 12, 3
+    g = np.random.default_rng(3)
+    logits = g.normal(0, 1, (t, e)).astype(np.float32)
+    logits[:, 4], logits[10], logits[11, 2:] = -np.inf, -np.inf, -np.inf
+    ids, w = choose(logits, k)
+    args = list(layer(t, 272, 144, e, k, 12))
+    args[1], args[2] = ids, w
+    got = forward(*args)
+    check(got, *ref.moe(*args))
+    assert (ids != 4).all() and (ids[10] == -1).all() and (got[10] == 0).all() and (ids[11] == [*np.argsort(-logits[11, :2]), -1]).all()
+
+
+def test_codes_past_31_bits():
+    """Experts whose codes begin past 2^31: the last expert's results are those of it alone."""
+    h, i, e = 4096, 1024, 520  # up: 4.4e9 codes, down 2.2e9
+    args = list(layer(3, h, i, 1, 1, 13))
+    x, _, weights, up, su, down, sd = args
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    alone = forward(*args)
+    big_up, big_down = (torch.zeros((e, *a.shape[1:]), dtype=torch.uint8, device="cuda") for a in (up, down))
+    big_su, big_sd = (torch.ones((e, *a.shape[1:]), device="cuda") for a in (su, sd))
+    for b, a in ((big_up, up), (big_down, down), (big_su, su), (big_sd, sd)):
+        b[e - 1] = dev(a[0])
+    for t in (1, 3):
+        ids = torch.full((t, 1), e - 1, dtype=torch.int32, device="cuda")
+        y, st = torch.empty((t, h), dtype=torch.bfloat16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        pulse.pulse_moe_forward(dev(x[:t]).to(torch.bfloat16), ids, dev(weights[:t]), big_up, big_su, big_down, big_sd, y, st,
+                                pulse.moe_workspace(t, h, i, e, 1))
+        got = y.double().cpu().numpy()
+        # (one token's sums are made in another order than three's)
+        check(got, *ref.moe(x[:t], np.zeros((t, 1), dtype=int), weights[:t], up, su, down, sd))
+        if t == 3:
+            np.testing.assert_array_equal(got, alone)
