@@ -464,23 +464,28 @@ __global__ __launch_bounds__(T::threads) void k_fp8_tile(GemmArgs g) {
 
 // ---- up to 16 tokens -------------------------------------------------------------------
 // The time is that of reading W, a wave's share of it through LDS buffers of its own and
-// without a barrier: a workgroup has 16 rows of W, and its NW waves take their steps of 128
-// columns in turn, each D - 1 of its steps ahead (with x's and the scales).  The waves' sums are
-// added through LDS, in their order.
-template <int NX, int NW, int D>
+// without a barrier: a workgroup has RT times 16 rows of W, and its NW waves take their steps of
+// 128 columns in turn, each D - 1 of its steps ahead (with x's and the scales).  The waves' sums
+// are added through LDS, in their order.  Each workgroup reads x again, out of L2, so that 32 rows
+// halve what 16 rows' reads cost: x [55296, 5120], 8 tokens 45.3 -> 42.2 us, 16 tokens 57.6 -> 47.8;
+// one token 40.7 -> 41.0, x [28672, 5120] 22.8 -> 23.6.  Two workgroups fit a compute unit; with
+// eight waves, one: 16 tokens 55.0.
+template <int NX, int NW, int D, int RT>
 __global__ __launch_bounds__(NW *kWave) void k_fp8_rows(GemmArgs g) {
-    constexpr int w_bytes = 16 * GB, x_bytes = NX * GB, stage = w_bytes + x_bytes + 256;
-    constexpr int xi = x_bytes / 1024, loads = 2 + xi + 1;
+    constexpr int w_bytes = RT * 16 * GB, x_bytes = NX * GB, stage = w_bytes + x_bytes + 256;
+    constexpr int wi = RT * 2, xi = x_bytes / 1024, loads = wi + xi + 1;
     static_assert(NX % 8 == 0 && NX <= 16 && (D - 1) * loads <= 63, "rows of x");
     __shared__ __attribute__((aligned(1024))) uint8_t s_mem[NW * D * stage];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id()), c16 = lane & 15, q = lane >> 4;
-    const int n0 = (int)blockIdx.x * 16;
+    const int n0 = (int)blockIdx.x * RT * 16;
     const auto clamped = [](int r, int n) { return (uint32_t)(r < n ? r : n - 1); };
     const uint8_t *const wb = load_base(g.w + (int64_t)n0 * g.K), *const xb = load_base(g.x);
     const float *const sb = load_base(g.sx);
     const scalar_floats sw = (scalar_floats)(uint64_t)g.sw + (int64_t)(n0 / GB) * g.gwj;
     const int r8 = lane >> 3, pieces[2] = {(lane & 7) ^ swap_x(r8), (lane & 7) ^ swap_x(r8 + 8)};  // of rows r8 and r8 + 8
-    const uint32_t wo[2] = {(clamped(n0 + r8, g.J) - n0) * (uint32_t)g.K, (clamped(n0 + r8 + 8, g.J) - n0) * (uint32_t)g.K};
+    uint32_t wo[wi];
+#pragma unroll
+    for (int i = 0; i < wi; ++i) wo[i] = (clamped(n0 + i * 8 + r8, g.J) - n0) * (uint32_t)g.K;
     const uint32_t xo[2] = {clamped(r8, g.M) * (uint32_t)g.K, clamped(r8 + 8, g.M) * (uint32_t)g.K};
     const uint32_t so = clamped(c16, g.M) * (uint32_t)g.gx * 4;
     uint8_t *const mine = s_mem + wave * D * stage;
@@ -490,15 +495,16 @@ __global__ __launch_bounds__(NW *kWave) void k_fp8_rows(GemmArgs g) {
         const int left = g.K - s * GB;
         uint32_t c[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            c[i] = (uint32_t)(s * GB + (pieces[i] * 16 < left ? pieces[i] * 16 : 0));
-            load_lds16_once(at + i * 1024, wb, wo[i] + c[i]);
-        }
+        for (int i = 0; i < 2; ++i) c[i] = (uint32_t)(s * GB + (pieces[i] * 16 < left ? pieces[i] * 16 : 0));
+#pragma unroll
+        for (int i = 0; i < wi; ++i) load_lds16_once(at + i * 1024, wb, wo[i] + c[i & 1]);
 #pragma unroll
         for (int i = 0; i < xi; ++i) load_lds16(at + w_bytes + i * 1024, xb, xo[i] + c[i]);
         load_lds4(at + w_bytes + x_bytes, sb, so + (uint32_t)s * 4);
     };
-    f32x4 acc = {0, 0, 0, 0};
+    f32x4 acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = f32x4{0, 0, 0, 0};
     int ahead = wave, turns = 0, turn = 0;
     for (int i = 0; i < D - 1; ++i, ahead += NW)
         if (ahead < g.steps) issue(ahead, turns++);
@@ -521,20 +527,26 @@ __global__ __launch_bounds__(NW *kWave) void k_fp8_rows(GemmArgs g) {
         }
         const auto operand = [&](const uint8_t *m, int r) { return row_operand(m, r, swap_x(r)); };
         const float f = reinterpret_cast<const float *>(at + w_bytes + x_bytes)[lane] * sw[(int64_t)s * g.gwc];
-        const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(at, c16), operand(at + w_bytes, c16 % NX),
-                                                                         f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+        const i32x8 x = operand(at + w_bytes, c16 % NX);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(f, p[i], acc[i]);
+        for (int t = 0; t < RT; ++t) {
+            const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(at, t * 16 + c16), x,
+                                                                             f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(f, p[i], acc[t][i]);
+        }
     }
     __syncthreads();
     f32x4 *const sums = reinterpret_cast<f32x4 *>(s_mem);
-    sums[wave * kWave + lane] = acc;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) sums[(t * NW + wave) * kWave + lane] = acc[t];
     __syncthreads();
-    if (wave != 0 || c16 >= g.M) return;
-    for (int i = 1; i < NW; ++i) acc += sums[i * kWave + lane];
-    const int col = n0 + q * 4;
-    if (g.bias) store_result<true>(g, c16, col, acc);
-    else store_result<false>(g, c16, col, acc);
+    if (wave >= RT || c16 >= g.M) return;  // wave t joins tile t
+    f32x4 all = sums[wave * NW * kWave + lane];
+    for (int i = 1; i < NW; ++i) all += sums[(wave * NW + i) * kWave + lane];
+    const int col = n0 + wave * 16 + q * 4;
+    if (g.bias) store_result<true>(g, c16, col, all);
+    else store_result<false>(g, c16, col, all);
 }
 
 // The tile, and how the work is shared: one round of workgroups after the other as long as each
@@ -549,14 +561,15 @@ struct GemmPlan {
 // The tile is the one that takes the least time by this estimate.  Microseconds of a step while
 // the chip is full, measured with 256 tiles of 64 steps; a second launch and a float32 value
 // written and read again as measured for the shared tiles of 64 to 512 rows:
-// [512, 8192] x [8192, 4096] by kind 45.0, 40.2, 39.9 and 40.9 us (estimate 44, 39, 37, 38);
-// 1024 rows 62.8, 61.4, 55.9, 79.0; 2048 rows 101, 90, 107, 155; 4096 rows 139, 175, 212, 307.
+// [512, 8192] x [8192, 4096] by kind 44.6, 39.1, 38.9 and 38.6 us (estimate 47, 38, 37, 38);
+// 1024 rows 61.5, 58.5, 52.8, 74.5 (63, 59, 53, 77); 2048 rows 94.6, 82.2, 101, 147 (96, 83, 105,
+// 154); 4096 rows 130, 158, 197, 290 (130, 165, 210, 307).
 struct GemmKind {
     int bm, bj;
     float step;
 };
 
-constexpr GemmKind kKinds[] = {{256, 256, 2.1f}, {256, 128, 1.35f}, {128, 128, 0.81f}, {64, 128, 0.58f}};
+constexpr GemmKind kKinds[] = {{256, 256, 2.03f}, {256, 128, 1.29f}, {128, 128, 0.82f}, {64, 128, 0.6f}};
 
 inline GemmPlan gemm_plan(int64_t M, int64_t J, int64_t C) {
     const int64_t steps = (C + GB - 1) / GB;
@@ -578,8 +591,8 @@ inline GemmPlan gemm_plan(int64_t M, int64_t J, int64_t C) {
     return best;
 }
 
-// k_fp8_rows: one token x [7168, 5120] 8.0 us, x [55296, 5120] 40.8 (6.9 TB/s), 16 tokens 10.7 and 52;
-// in tiles 14.5 and 55, and 15.2 and 59 (nn has no such form: its tiles' rows are what is contracted)
+// k_fp8_rows: one token x [7168, 5120] 7.8 us, x [55296, 5120] 41.0 (6.9 TB/s), 16 tokens 9.2 and
+// 47.8; in tiles 13.1 and 50.9, and 13.3 and 52.1 (nn has no such form: W's rows are what it contracts)
 inline bool by_rows(int64_t M, int32_t nn) { return !nn && M <= 16; }
 
 template <typename T, bool NN, int STAGES>
@@ -622,9 +635,9 @@ int pulse_launch_fp8_gemm(const uint8_t *x, const float *sx, const uint8_t *w, c
                      (int32_t)((C + GB - 1) / GB), nn ? 1 : (int32_t)gk, nn ? (int32_t)gk : 1, (int32_t)p.tiles_m,
                      (int32_t)p.tiles_j, (int32_t)((C + GB - 1) / GB), p.whole, p.shares, p.per};
     if (by_rows(M, nn)) {
-        const dim3 grid((unsigned)((n + 15) / 16));
-        if (M <= 8) k_fp8_rows<8, 8, 3><<<grid, dim3(512), 0, stream>>>(g);
-        else k_fp8_rows<16, 4, 4><<<grid, dim3(256), 0, stream>>>(g);
+        const dim3 grid((unsigned)((n + 31) / 32)), block(256);
+        if (M <= 8) k_fp8_rows<8, 4, 3, 2><<<grid, block, 0, stream>>>(g);
+        else k_fp8_rows<16, 4, 3, 2><<<grid, block, 0, stream>>>(g);
     } else if (nn) {
         launch_gemm<true>(p, g, stream);
     } else {
