@@ -5,10 +5,16 @@
 // The layer, with [gate; up] and down of every expert in E4M3 codes and 128 x 128 blocks:
 //   h = silu(Wg_e x) * (Wu_e x),   y = sum over the token's experts of p_e Wd_e h
 // A few tokens reach many experts, so the work is to read each of these experts' codes
-// once, at HBM's rate: 2 bytes of matrix work for a byte read.  Codes go past the
-// registers into LDS, rows of 256 bytes at a time, from where a wave takes them as
-// rows of the matrix instruction, turned into BF16 (exactly: E4M3 has four bits), with
-// up to 16 tokens as its columns.
+// once, at HBM's rate.  Pairs (a token and a choice) are put in order by expert, up to NX of
+// an expert make an item, and an item's workgroups read the expert's rows past the registers
+// into LDS, 128 or 256 columns a step and two or three steps ahead; from there a wave takes
+// them as rows of the matrix instruction, turned into BF16 (exactly: E4M3 has four bits), with
+// the pairs as its columns.  Outputs of the pairs are added up per token in the order of its
+// choices, so that a result does not hang on which workgroup was first.
+//
+// Launches: plan, up (with silu and the product as its epilogue), down, join.  With one or two
+// tokens, whose pairs fit a wave, the plan is made by each wave itself and the sum belongs to
+// down: two launches.
 #include "e4m3.hpp"
 #include "lds_load.hpp"
 
@@ -143,7 +149,6 @@ struct MoeArgs {
     MoePlan plan;
     int32_t P, E, R, K;  // R: rows of w (up: 2 I)
     int32_t top_k;
-    int32_t kw;          // few: waves that share the contraction: 1, 2 or 4
     uint32_t *status;
 };
 
@@ -213,6 +218,9 @@ template <bool UP, int NX, bool FEW>
 struct MoeStage {
     static constexpr int MW = NX >= 64 ? 8 : 4;  // waves: eight share the largest x
     static constexpr int parts = UP ? 1 : 2;
+    // Waves that share a tile's contraction.  One token: 1, 2 and 4 of them, 8 of 384 experts x (7168, 2048)
+    // 63.7, 63.7 and 64.8 us, 4 of 60 x (2048, 1408) 20.1, 17.4, 17.2, 2 of 16 x (4096, 14336) 79, 80, 86.
+    static constexpr int kw = FEW ? 2 : 1;
     static constexpr int cols = NX <= 8 || (NX == 16 && UP) ? 256 : 128;  // of a step
     static constexpr int w_bytes = MR * cols, x_bytes = parts * NX * cols * 2;
     static constexpr int bytes = MW * w_bytes + (FEW ? MW : 1) * x_bytes;
@@ -229,7 +237,7 @@ struct MoeStage {
 template <bool UP, int NX, bool FEW>
 __global__ __launch_bounds__((MoeStage<UP, NX, FEW>::MW * kWave), 2) void k_moe_rows(MoeArgs g) {
     using S = MoeStage<UP, NX, FEW>;
-    constexpr int MW = S::MW;
+    constexpr int MW = S::MW, kw = S::kw;
     constexpr int CT = (NX + 15) / 16;  // tiles of tokens
     __shared__ __attribute__((aligned(1024))) uint8_t s_mem[S::stages * S::bytes];
     const MoeItem item = FEW ? few_item(g, blockIdx.y, NX) : planned_item(g, blockIdx.y, NX);
@@ -241,7 +249,6 @@ __global__ __launch_bounds__((MoeStage<UP, NX, FEW>::MW * kWave), 2) void k_moe_
         return (uint32_t)p < (uint32_t)g.P ? p : 0;
     };
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id()), c16 = lane & 15, q = lane >> 4;
-    const int kw = FEW ? g.kw : 1;
     const int half = g.R / 2;                               // up: gate's rows
     const int tile = (int)blockIdx.x * (MW / kw) + wave / kw, share = wave % kw;
     const int tiles = UP ? half / 16 : (g.R + MR - 1) / MR;
@@ -546,18 +553,21 @@ inline MoeWs moe_ws(int64_t P, int64_t H, int64_t I) {
 
 // Pairs of an item, by an expert's average: more of them, and most experts are read once; fewer,
 // and less of LDS and of the columns is empty.  Microseconds with items of 8, 16, 32 and 64:
-// 1.9 a expert (30 tokens, top 4 of 64 x (4096, 2048)) 246, 250, 257, 331; 4 a expert (61, 4 of 60 x
-// (2048, 1408)) 98, 94, 99, 124; 8 a expert (64, 4 of 32 x (4096, 2048)) 181, 167, 179, 198; 16 a expert
-// (128 tokens) 247, 202, 171, 202; 32 a expert (128, 4 of 16) 202, 149, 128, 113.
+// 1.9 an expert (30 tokens, top 4 of 64 x (4096, 2048)) 248, 249, 257, 336; 4 an expert (61, 4 of 60 x
+// (2048, 1408)) 97, 94, 97, 125; 8 an expert (64, 4 of 32 x (4096, 2048)) 183, 165, 165, 201; 16 an
+// expert (128 tokens) 249, 199, 171, 205; 32 an expert (128, 4 of 16) 202, 148, 126, 114; 64 an expert
+// (256 tokens) 338, 228, 177, 169.
 inline int moe_nx(int64_t P, int64_t E) { return P <= 2 * E ? 8 : P <= 10 * E ? 16 : P <= 20 * E ? 32 : 64; }
 
-// One or two tokens: the choices fit a wave.
+// One or two tokens, whose choices fit a wave, and two launches instead of four: one token, 8 of 384 experts
+// x (7168, 2048) 63.7 and 76.8 us, 4 of 60 x (2048, 1408) 17.4 and 30.1; two tokens 116 and 121, 24.1 and 31.9.
 inline bool moe_few(int64_t T, int64_t P) { return T <= 2 && P <= kWave; }
 
 template <bool UP, int NX, bool FEW>
 inline void launch_rows(const MoeArgs &g, unsigned items, hipStream_t stream) {
-    constexpr int waves = MoeStage<UP, NX, FEW>::MW;
-    const unsigned tiles = (unsigned)(UP ? g.R / 2 / 16 : (g.R + MR - 1) / MR), per = (unsigned)(waves / g.kw);
+    using S = MoeStage<UP, NX, FEW>;
+    constexpr int waves = S::MW, per = waves / S::kw;
+    const unsigned tiles = (unsigned)(UP ? g.R / 2 / 16 : (g.R + MR - 1) / MR);
     k_moe_rows<UP, NX, FEW><<<dim3((tiles + per - 1) / per, items), dim3(waves * kWave), 0, stream>>>(g);
 }
 
@@ -595,12 +605,11 @@ int pulse_launch_moe_forward(const uint16_t *x, int64_t ldx, const int32_t *ids,
     const MoePlan plan{words, words + 1, words + 1 + P, reinterpret_cast<int32_t *>(mem + at.order)};
     uint16_t *const h = reinterpret_cast<uint16_t *>(mem + at.h);
     float *const out = reinterpret_cast<float *>(mem + at.out);
-    MoeArgs u{x, ldx, up, up_scales, h, nullptr, ids, plan, (int32_t)P, (int32_t)E, (int32_t)(2 * I), (int32_t)H,
-              (int32_t)top_k, 1, status};
-    MoeArgs d{h, I, down, down_scales, nullptr, out, ids, plan, (int32_t)P, (int32_t)E, (int32_t)H, (int32_t)I,
-              (int32_t)top_k, 1, status};
+    const MoeArgs u{x, ldx, up, up_scales, h, nullptr, ids, plan, (int32_t)P, (int32_t)E, (int32_t)(2 * I), (int32_t)H,
+              (int32_t)top_k, status};
+    const MoeArgs d{h, I, down, down_scales, nullptr, out, ids, plan, (int32_t)P, (int32_t)E, (int32_t)H, (int32_t)I,
+              (int32_t)top_k, status};
     if (moe_few(T, P)) {
-        u.kw = H >= 4096 ? 4 : H >= 2048 ? 2 : 1;
         launch_rows<true, 2, true>(u, (unsigned)P, stream);
         k_moe_few_down<<<dim3((unsigned)(H / 16)), dim3(FD_WAVES * kWave), 0, stream>>>(d, weights, (int32_t)T, y, ldy);
         return hipGetLastError() == hipSuccess ? 0 : -5;
