@@ -7,11 +7,11 @@
 //   s = bf16(x + residual), or x         (what later layers and the backward pass read)
 //   r = 1 / sqrt(mean(s^2) + eps),  y = s r w
 //   dx = r (dy w - s r mean(dy w s r)) + dres,  dw = sum over rows of dy s r
-// Every byte is read and written once, so the large calls are bound by HBM and the
-// small ones by the chain load - sum - barrier - store.  A row stays in the
-// registers of one workgroup between its sum and its output: 8 columns (16 bytes)
-// a lane, so that 16 lanes hold a quantisation group and 64 lanes read 1024
-// contiguous bytes.
+// Every byte is read and written once, so the large calls are bound by HBM (5.5 TB/s where a
+// copy has 5.1: more is read than written) and the small ones by the launch and the chain
+// load - sum - barrier - store.  A row stays in the registers of one workgroup between its sum
+// and its output: 8 columns (16 bytes) a lane, so that 16 lanes hold a quantisation group and
+// 64 lanes read 1024 contiguous bytes.
 #include "e4m3.hpp"
 
 #include <algorithm>
@@ -238,7 +238,8 @@ struct GroupQuantArgs {
     int32_t cols, per_row;
 };
 
-constexpr int GQ = 4;  // pieces of a wave, all read before the first is worked on
+// pieces of a wave, all read before the first is worked on: 8191 x 28672 123 us (5.7 TB/s)
+constexpr int GQ = 4;
 
 // A wave takes GQ pieces of 512 columns, one after the other through the rows; GLU: silu(x[c]) x[cols + c].
 template <bool GLU>
@@ -283,7 +284,10 @@ __global__ __launch_bounds__(256) void k_group_quant(GroupQuantArgs g) {
     }
 }
 
-// Waves of a row's workgroup and pieces of a wave: with many rows few waves, with few rows many.
+// Waves of a row's workgroup and pieces of a wave: with many rows few waves, of which more rows
+// are under way at once, with few rows many.  With codes and a residual, up to 4 and 16 waves:
+// 512 x 5120 7.1 and 7.3 us (the launch's own time), 1024 x 5120 9.4 and 10.6, 8192 x 5120 53.0 and
+// 57.0 (5.5 TB/s), 8192 x 16384 170 and 165.
 struct NormShape {
     int waves, pieces;
 };
@@ -344,7 +348,7 @@ int pulse_launch_rms_norm_backward(const uint16_t *s, int64_t lds, const uint16_
                                    int64_t cols, void *ws, hipStream_t stream) {
     float *const parts = static_cast<float *>(ws);
     const NormBackArgs g{s, w, dy, dres, rstd, dx, parts, lds, lddy, lddres, lddx, rows, (int32_t)cols};
-    const NormShape n = norm_shape(cols, cols <= 8 * NP ? 4 : NORM_BACK_WAVES);
+    const NormShape n = norm_shape(cols, NORM_BACK_WAVES);  // (four: 4099 x 8192 76 instead of 56 us)
     const int64_t wgs = norm_parts(rows, cols);
     with_pieces(n.pieces, [&](auto p) {
         constexpr int P = decltype(p)::value < 4 ? decltype(p)::value : 4;  // (eight waves: no more)
