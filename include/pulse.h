@@ -761,7 +761,7 @@ int pulse_lora_backward(const uint16_t *x, int64_t ldx, const uint16_t *dy, int6
  * Inf or NaN as its scale, and none of its codes times it is a number.
  *
  * x, y and the like are BF16 rows with any row stride that is a multiple of 8 elements;
- * T is up to 2^24.  Outputs overlap no other buffer of their call. */
+ * T is below 2^24.  Outputs overlap no other buffer of their call. */
 
 /* y = s rstd weight with rstd = 1 / sqrt(mean(s^2) + eps) of each row, s = x, or with a
  * residual s = bf16(x + residual), which is written back to it.  Sums are held in float32
@@ -801,7 +801,7 @@ int fp8_group_quant(const uint16_t *x, int64_t ldx, int64_t n_tokens, int64_t co
  *   PULSE_GEMM_NT  y [m][n] = x [m][k] w^T + bias: a projection; k a multiple of 16.
  *   PULSE_GEMM_NN  y [m][k] = x [m][n] w: the gradient of a projection's input, from that of
  *                  its output; n and k multiples of 16.
- * n and k up to 2^22.  y [m][ldy] is rounded to BF16 once; ldy >= its columns, any.  The matrix
+ * n and k up to 2^22, y up to 2^23 tiles of 64 x 128.  y [m][ldy] is rounded to BF16 once; ldy >= its columns, any.  The matrix
  * instructions add up eight neighbouring products at a time, each cut to a multiple of about
  * 2^-13 of their largest, and everything else is added in float32.
  *   x, x_scales  quantised rows (dense: row stride k, or n).

@@ -1089,10 +1089,10 @@ def _first(t, name, dims=2):
 
 def _launch_stream(device, stream):
     """The handle of the stream to launch on, which is one of the operands' device."""
+    current = _get_device()
+    if current is not None and current != device:
+        raise ValueError(f"operands are on GPU {device}, the current one is {current}")
     if stream is None:
-        current = _get_device()
-        if current is not None and current != device:
-            raise ValueError(f"operands are on GPU {device}, the current one is {current}")
         return _raw_stream(device)
     if stream.device_index != device:
         raise ValueError(f"operands are on GPU {device}, the stream is of {stream.device_index}")
@@ -1155,15 +1155,21 @@ def fp8_group_quant(x, codes, scales, glu=False, stream=None):
 _FORMS = {"nt": PULSE_GEMM_NT, "nn": PULSE_GEMM_NN}
 
 
+def _form(form):
+    if form not in _FORMS:
+        raise ValueError(f"form is {form!r}, expected one of {tuple(_FORMS)}")
+    return _FORMS[form]
+
+
 def fp8_gemm_workspace(m, n, k, form="nt", device="cuda"):
     """A workspace for fp8_block_gemm of m rows with weights [n, k]."""
-    return _scratch(_lib.fp8_block_gemm_ws_bytes(m, n, k, _FORMS[form]), "fp8_block_gemm_ws_bytes", device)
+    return _scratch(_lib.fp8_block_gemm_ws_bytes(m, n, k, _form(form)), "fp8_block_gemm_ws_bytes", device)
 
 
 def fp8_block_gemm(x, x_scales, w, w_scales, y, ws=None, bias=None, form="nt", stream=None):
     """y (BF16) = x w^T + bias ("nt": x [m, k], y [m, n]) or x w ("nn": x [m, n], y [m, k]): x E4M3 codes
     with a scale for each 128 columns of a row, w [n, k] codes with one for each 128 x 128 block."""
-    nn = _FORMS[form]
+    nn = _form(form)
     d, (n, k) = _first(w, "w")
     inner, out = (n, k) if nn else (k, n)
     if nn and bias is not None:

@@ -691,6 +691,7 @@ int pulse_lora_backward(const uint16_t *x, int64_t ldx, const uint16_t *dy, int6
 // ---- the sampler's layer over the FP8 view ------------------------------------------
 namespace {
 
+constexpr int64_t kMaxRows = (1 << 24) - 1;  // with 256 threads each: a launch counts its threads in 32 bits
 constexpr int64_t kMaxNormCols = 16384;    // a row stays in one workgroup's registers
 constexpr int64_t kMaxQuantCols = 1 << 24;
 constexpr int64_t kMaxGemmSide = 1 << 22;  // 256 rows of codes count in 31 bits
@@ -698,17 +699,17 @@ constexpr int64_t kMaxMoeSide = 1 << 16, kMaxMoeStride = 1 << 20;
 
 int check_norm_sizes(int64_t rows, int64_t cols) {
     if (rows < 0 || cols < 8 || cols % 8 != 0) return PULSE_EINVAL;
-    return rows > kMaxLora || cols > kMaxNormCols ? PULSE_ERANGE : PULSE_OK;
+    return rows > kMaxRows || cols > kMaxNormCols ? PULSE_ERANGE : PULSE_OK;
 }
 
 int check_gemm_sizes(int64_t m, int64_t n, int64_t k, int32_t form) {
     if (m < 0 || n < 1 || k < 16 || k % 16 != 0 || (form != PULSE_GEMM_NT && form != PULSE_GEMM_NN) ||
         (form == PULSE_GEMM_NN && n % 16 != 0))
         return PULSE_EINVAL;
-    if (m > kMaxLora || n > kMaxGemmSide || k > kMaxGemmSide) return PULSE_ERANGE;
-    // workgroups of a launch
+    if (m > kMaxRows || n > kMaxGemmSide || k > kMaxGemmSide) return PULSE_ERANGE;
+    // workgroups of 512 threads, in the smallest tiles
     const int64_t j = form == PULSE_GEMM_NN ? k : n;
-    return ((m + 63) / 64) * ((j + 127) / 128) > 0x7FFFFF00 || m * j > (int64_t)0x7FFFFF00 * 256 ? PULSE_ERANGE : PULSE_OK;
+    return ((m + 63) / 64) * ((j + 127) / 128) > 0x7FFFFF ? PULSE_ERANGE : PULSE_OK;
 }
 
 int check_moe_sizes(int64_t T, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k) {
@@ -766,7 +767,7 @@ int pulse_rms_norm_backward(const uint16_t *s, int64_t lds, const uint16_t *weig
 int fp8_group_quant(const uint16_t *x, int64_t ldx, int64_t n_tokens, int64_t cols, int32_t glu, uint8_t *codes,
                     float *scales, hipStream_t stream) {
     if (n_tokens < 0 || cols < 8 || cols % 8 != 0 || (glu != 0 && glu != 1)) return PULSE_EINVAL;
-    if (n_tokens > kMaxLora || cols > kMaxQuantCols || n_tokens * ((cols + 511) / 512) / 16 > 0x7FFFFF00) return PULSE_ERANGE;
+    if (n_tokens > kMaxRows || cols > kMaxQuantCols || n_tokens * ((cols + 511) / 512) / 16 >= kMaxRows) return PULSE_ERANGE;
     if (n_tokens == 0) return PULSE_OK;
     if (!x || !codes || !scales || bad_stride(ldx, glu ? 2 * cols : cols)) return PULSE_EINVAL;
     if (!aligned16(x) || !aligned16(codes)) return PULSE_EALIGN;
@@ -798,7 +799,7 @@ int pulse_moe_route(const float *logits, int64_t ld, int64_t n_tokens, int64_t e
     if (n_tokens < 0 || experts < 1 || top_k < 1 || top_k > experts || (over_all != 0 && over_all != 1) ||
         !std::isfinite((float)scale))
         return PULSE_EINVAL;
-    if (n_tokens > kMaxLora || experts > PULSE_MOE_MAX_EXPERTS || top_k > PULSE_MOE_MAX_TOP_K) return PULSE_ERANGE;
+    if (n_tokens > kMaxRows || experts > PULSE_MOE_MAX_EXPERTS || top_k > PULSE_MOE_MAX_TOP_K) return PULSE_ERANGE;
     if (n_tokens == 0) return PULSE_OK;
     if (!logits || !ids || !weights || ld < experts) return PULSE_EINVAL;
     return pulse_launch_moe_route(logits, ld, n_tokens, experts, (int32_t)top_k, over_all, (float)scale, ids, weights,

@@ -3,6 +3,7 @@ import ctypes
 
 import pytest
 
+import sparse_delta_codec_amd as pulse
 from tests.test_abi import EALIGN, EINVAL, ERANGE, EWORKSPACE, lib  # noqa: F401  (the library fixture)
 
 V, I64, I32, F64, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_double, ctypes.c_size_t
@@ -113,6 +114,22 @@ GOOD_MOE = dict(x=A, ldx=256, ids=A, w=A, up=A, su=A, down=A, sd=A, t=4, h=256, 
     (dict(ws=None), EWORKSPACE), (dict(wsb=100), EWORKSPACE)])
 def test_moe(lib, bad, code):  # noqa: F811
     assert call(lib, "pulse_moe_forward", MOE, GOOD_MOE, bad) == code
+
+
+@pytest.mark.parametrize("name,types,good,bad", [
+    ("pulse_rms_norm", NORM, GOOD_NORM, dict(t=2 ** 24)), ("pulse_rms_norm_backward", BACK, GOOD_BACK, dict(t=2 ** 24, wsb=1 << 40)),
+    ("fp8_group_quant", QUANT, GOOD_QUANT, dict(t=2 ** 24)),
+    ("fp8_group_quant", QUANT, GOOD_QUANT, dict(t=2 ** 23, n=32 * 512, ldx=2 ** 15)),
+    ("fp8_block_gemm", GEMM, GOOD_GEMM, dict(m=2 ** 24)), ("pulse_moe_route", ROUTE, GOOD_ROUTE, dict(t=2 ** 24)),
+    ("fp8_block_gemm", GEMM, GOOD_GEMM, dict(m=2 ** 20, n=2 ** 16, k=16, ldy=2 ** 16))])
+def test_launches_that_count_past_32_bits(lib, name, types, good, bad):  # noqa: F811
+    """2^24 workgroups of 256 threads, 2^23 of 512."""
+    assert call(lib, name, types, good, bad) == ERANGE
+
+
+def test_unknown_form():
+    with pytest.raises(ValueError, match="expected one of"):
+        pulse.fp8_gemm_workspace(4, 256, 256, "tn", device="cpu")
 
 
 def test_nothing_to_do(lib):  # noqa: F811
