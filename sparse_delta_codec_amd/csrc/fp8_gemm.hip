@@ -559,17 +559,19 @@ struct GemmPlan {
 };
 
 // The tile is the one that takes the least time by this estimate.  Microseconds of a step while
-// the chip is full, measured with 256 tiles of 64 steps; a second launch and a float32 value
-// written and read again as measured for the shared tiles of 64 to 512 rows:
-// [512, 8192] x [8192, 4096] by kind 44.6, 39.1, 38.9 and 38.6 us (estimate 47, 38, 37, 38);
-// 1024 rows 61.5, 58.5, 52.8, 74.5 (63, 59, 53, 77); 2048 rows 94.6, 82.2, 101, 147 (96, 83, 105,
-// 154); 4096 rows 130, 158, 197, 290 (130, 165, 210, 307).
+// the chip is full, measured with 256 tiles of 64 steps, or, where one row of tiles reads W once,
+// with 55296 x 5120 and 5120 x 27648; a second launch and a float32 value written and read again
+// as measured for the shared tiles of 64 to 512 rows.  By kind:
+// [2048, 8192] x [8192, 4096] 94.6, 80.2, 101 and 147 us, 4096 rows 129, 163, 204, 292;
+// [96, 5120] x [5120, 55296] -, 60.0, 75.9, 99.0; [96, 27648] x [27648, 5120] -, 36.7, 40.4, 50.7;
+// 24 rows of that -, 33.7, 35.7, 29.3.  (256 x 128 in place of 128 x 256: 85.9 and 165 us of
+// 2048 and 4096 rows, 104 of 96 rows x [5120, 55296], whose tiles are half empty then.)
 struct GemmKind {
     int bm, bj;
-    float step;
+    float step, once;
 };
 
-constexpr GemmKind kKinds[] = {{256, 256, 2.03f}, {256, 128, 1.29f}, {128, 128, 0.82f}, {64, 128, 0.6f}};
+constexpr GemmKind kKinds[] = {{256, 256, 2.03f, 2.03f}, {128, 256, 1.28f, 1.45f}, {128, 128, 0.81f, 0.95f}, {64, 128, 0.6f, 0.74f}};
 
 inline GemmPlan gemm_plan(int64_t M, int64_t J, int64_t C) {
     const int64_t steps = (C + GB - 1) / GB;
@@ -583,9 +585,10 @@ inline GemmPlan gemm_plan(int64_t M, int64_t J, int64_t C) {
         p.per = (int)((steps + shares - 1) / shares);
         p.shares = (int)((steps + p.per - 1) / p.per);
         p.whole = (int)(p.shares > 1 ? tiles - rest : tiles);
-        float t = (float)((p.whole + kUnits - 1) / kUnits * steps) * k.step;
+        const float step = M <= k.bm ? k.once : k.step;
+        float t = (float)((p.whole + kUnits - 1) / kUnits * steps) * step;
         if (p.shares > 1)  // the shared tiles, and the launch that joins them
-            t += (float)p.per * k.step + 4.0f + (float)(rest * p.shares) * (float)(k.bm * k.bj) * 8.0f / 5e6f;
+            t += (float)p.per * step + 4.0f + (float)(rest * p.shares * std::min<int64_t>(M, k.bm) * k.bj) * 8.0f / 5e6f;
         if (best.per == 0 || t < least) best = p, least = t;
     }
     return best;
@@ -608,7 +611,7 @@ template <bool NN>
 inline void launch_gemm(const GemmPlan &p, const GemmArgs &g, hipStream_t stream) {
     switch (p.kind) {
     case 0: return launch_tiles<Tile<256, 256, 4>, NN, 2>(g, stream);
-    case 1: return launch_tiles<Tile<256, 128, 4>, NN, 3>(g, stream);
+    case 1: return launch_tiles<Tile<128, 256, 4>, NN, 3>(g, stream);
     case 2: return launch_tiles<Tile<128, 128, 4>, NN, 4>(g, stream);
     default: return launch_tiles<Tile<64, 128, 4>, NN, 5>(g, stream);
     }

@@ -148,10 +148,11 @@ def test_no_tokens():
 
 
 # rows, columns of y and contraction that make each size of tile, alone, shared, both at once, and
-# one row of tiles: 256 x 256, 256 x 128, 128 x 128 and 64 x 128
+# one row of tiles: 256 x 256, 128 x 256, 128 x 128 and 64 x 128
 TILES = [(900, 8208, 144), (2000, 8208, 528), (900, 5136, 8208), (4100, 1000 + 8, 144), (1500, 1008, 8208), (2000, 8208, 144),
          (250, 8208, 8208), (250, 8208, 144), (1500, 512, 4112), (70, 4112, 8208), (4100, 4112, 144), (70, 256, 144), (70, 8208, 144),
-         (250, 8208, 4112), (4099, 4112, 1040)]
+         (250, 8208, 4112), (4099, 4112, 1040), (4099, 8208, 528), (40, 16400, 4112), (40, 33040, 144), (70, 33040, 4112),
+         (70, 16400, 144), (70, 16400, 4112), (40, 33040, 1040), (40, 144, 144), (40, 16400, 144)]
 
 
 @pytest.mark.parametrize("form", ["nt", "nn"])
