@@ -159,6 +159,7 @@ __global__ __launch_bounds__(T::threads) void k_fp8_join(GemmArgs g) {
     if (m0 + row >= g.M || j0 + col >= g.J) return;
     const f32x4 *part = g.parts + ((int64_t)blockIdx.y * g.shares * T::results + result) * T::threads + threadIdx.x;
     f32x4 v = part[0];
+#pragma unroll 4
     for (int s = 1; s < g.shares; ++s) v += part[(int64_t)s * T::results * T::threads];
     if (g.bias) store_result<true>(g, m0 + row, j0 + col, v);
     else store_result<false>(g, m0 + row, j0 + col, v);
@@ -468,8 +469,8 @@ __global__ __launch_bounds__(T::threads) void k_fp8_tile(GemmArgs g) {
 // 128 columns in turn, each D - 1 of its steps ahead (with x's and the scales).  The waves' sums
 // are added through LDS, in their order.  Each workgroup reads x again, out of L2, so that 32 rows
 // halve what 16 rows' reads cost: x [55296, 5120], 8 tokens 45.3 -> 42.2 us, 16 tokens 57.6 -> 47.8;
-// one token 40.7 -> 41.0, x [28672, 5120] 22.8 -> 23.6.  Two workgroups fit a compute unit; with
-// eight waves, one: 16 tokens 55.0.
+// one token 40.7 -> 41.0, x [28672, 5120] 22.8 -> 23.6.  Where they are too few for the chip,
+// workgroups have 16 rows and more waves (kRows).
 template <int NX, int NW, int D, int RT>
 __global__ __launch_bounds__(NW *kWave) void k_fp8_rows(GemmArgs g) {
     constexpr int w_bytes = RT * 16 * GB, x_bytes = NX * GB, stage = w_bytes + x_bytes + 256;
@@ -549,8 +550,8 @@ __global__ __launch_bounds__(NW *kWave) void k_fp8_rows(GemmArgs g) {
     else store_result<false>(g, c16, col, all);
 }
 
-// The tile, and how the work is shared: one round of workgroups after the other as long as each
-// fills the chip; the tiles that are left over share the chip among them.
+// The form, and how the work is shared: one round of workgroups after the other as long as each
+// fills the chip; the tiles that are left over share the chip among them, in as many shares as pay.
 constexpr int kUnits = 256;  // compute units
 
 struct GemmPlan {
@@ -558,45 +559,69 @@ struct GemmPlan {
     int64_t tiles_m, tiles_j;
 };
 
-// The tile is the one that takes the least time by this estimate.  Microseconds of a step while
+// The form is the one that takes the least time by this estimate.  Microseconds of a step while
 // the chip is full, measured with 256 tiles of 64 steps, or, where one row of tiles reads W once,
-// with 55296 x 5120 and 5120 x 27648; a second launch and a float32 value written and read again
-// as measured for the shared tiles of 64 to 512 rows.  By kind:
+// with 55296 x 5120 and 5120 x 27648; a second launch, a share in it and a float32 value written and
+// read again as measured for the shared tiles of 1 to 512 rows.  By kind:
 // [2048, 8192] x [8192, 4096] 94.6, 80.2, 101 and 147 us, 4096 rows 129, 163, 204, 292;
 // [96, 5120] x [5120, 55296] -, 60.0, 75.9, 99.0; [96, 27648] x [27648, 5120] -, 36.7, 40.4, 50.7;
-// 24 rows of that -, 33.7, 35.7, 29.3.  (256 x 128 in place of 128 x 256: 85.9 and 165 us of
-// 2048 and 4096 rows, 104 of 96 rows x [5120, 55296], whose tiles are half empty then.)
+// 24 rows of that -, 33.7, 35.7, 29.3; [128, 14336] x [14336, 4096] -, 29.8, 24.5, 27.2.  (256 x 128 in place of 128 x 256: 85.9 and 165 us of
+// 2048 and 4096 rows, 104 of 96 rows x [5120, 55296], whose tiles are half empty then.)  Shares:
+// one row x [27200, 128] in 213 of them 58.3 us, in 43 12.1; 100 rows 35.2 and 13.5.
 struct GemmKind {
     int bm, bj;
     float step, once;
 };
 
-constexpr GemmKind kKinds[] = {{256, 256, 2.03f, 2.03f}, {128, 256, 1.28f, 1.45f}, {128, 128, 0.81f, 0.95f}, {64, 128, 0.6f, 0.74f}};
+constexpr GemmKind kKinds[] = {{256, 256, 2.03f, 2.03f}, {128, 256, 1.28f, 1.45f}, {128, 128, 0.81f, 0.95f}, {64, 128, 0.62f, 0.74f}};
 
-inline GemmPlan gemm_plan(int64_t M, int64_t J, int64_t C) {
+// k_fp8_rows: rows of W and waves of a workgroup; microseconds of a turn (a step of each wave) with
+// up to 8 tokens and up to 16.  W comes in at 6.9 and 6.0 TB/s at most.  Microseconds
+// in 32 rows, in 16 rows and in tiles: one token x [7168, 5120] 7.8, 7.8, 12.8; [4096, 14336] 13.3,
+// 10.9, 16.6; [5120, 27648] 24.4, 28.6, 28.1; [55296, 5120] 41.0, 40.7, 50.9; [128, 27200] 25.2,
+// 14.7, 12.1; 16 tokens 9.2, 11.8, 13.3; 17.8, 13.9, 17.1; 33.0, 44.2, 28.8; 47.8, 57.6, 52.1; 36.0, 24.6, 11.4.
+// (nn has no such form: W's rows are what it contracts.)
+struct RowsKind {
+    int rows, waves;
+    float turn[2];
+};
+
+constexpr RowsKind kRows[] = {{32, 4, {0.46f, 0.62f}}, {16, 8, {0.5f, 0.85f}}};
+constexpr int kRowsFrom = 4;  // kind of the first of them
+
+inline GemmPlan gemm_plan(int64_t M, int64_t J, int64_t C, bool nn) {
     const int64_t steps = (C + GB - 1) / GB;
     GemmPlan best{};
     float least = 0;
+    const auto consider = [&](const GemmPlan &p, float t) {
+        if (best.per == 0 || t < least) best = p, least = t;
+    };
+    if (!nn && M <= 16)
+        for (int i = 0; i < 2; ++i) {
+            const RowsKind &k = kRows[i];
+            const int64_t wgs = (J + k.rows - 1) / k.rows, turns = (steps + k.waves - 1) / k.waves;
+            const float t = (float)((wgs + kUnits - 1) / kUnits * turns) * k.turn[M > 8];
+            const float bytes = (float)(J * C) / (M > 8 ? 6.0e6f : 6.9e6f);
+            consider({kRowsFrom + i, 16, k.rows, (int)wgs, 1, (int)steps, 1, wgs}, std::max(t, bytes) + 2.5f);
+        }
     for (int kind = 0; kind < 4; ++kind) {
         const GemmKind &k = kKinds[kind];
-        GemmPlan p{kind, k.bm, k.bj, 0, 1, (int)steps, (M + k.bm - 1) / k.bm, (J + k.bj - 1) / k.bj};
-        const int64_t tiles = p.tiles_m * p.tiles_j, rest = tiles % kUnits;
-        const int64_t shares = rest ? std::min<int64_t>(kUnits / rest, steps) : 1;
-        p.per = (int)((steps + shares - 1) / shares);
-        p.shares = (int)((steps + p.per - 1) / p.per);
-        p.whole = (int)(p.shares > 1 ? tiles - rest : tiles);
+        const int64_t tiles_m = (M + k.bm - 1) / k.bm, tiles_j = (J + k.bj - 1) / k.bj, tiles = tiles_m * tiles_j;
+        const int64_t rest = tiles % kUnits;
         const float step = M <= k.bm ? k.once : k.step;
-        float t = (float)((p.whole + kUnits - 1) / kUnits * steps) * step;
-        if (p.shares > 1)  // the shared tiles, and the launch that joins them
-            t += (float)p.per * step + 4.0f + (float)(rest * p.shares * std::min<int64_t>(M, k.bm) * k.bj) * 8.0f / 5e6f;
-        if (best.per == 0 || t < least) best = p, least = t;
+        for (int64_t most = rest ? std::min<int64_t>(kUnits / rest, steps) : 1; most >= 1; most /= 2) {
+            GemmPlan p{kind, k.bm, k.bj, 0, 1, (int)((steps + most - 1) / most), tiles_m, tiles_j};
+            p.shares = (int)((steps + p.per - 1) / p.per);
+            p.whole = (int)(p.shares > 1 ? tiles - rest : tiles);
+            float t = (float)((p.whole + kUnits - 1) / kUnits * steps) * step + 2.0f;
+            if (p.shares > 1)  // the shared tiles, and the launch that joins them
+                t += (float)p.per * step + 4.0f + 0.07f * (float)p.shares +
+                     (float)(rest * p.shares * std::min<int64_t>(M, k.bm) * k.bj) * 8.0f / 5e6f;
+            consider(p, t);
+        }
     }
     return best;
 }
-
-// k_fp8_rows: one token x [7168, 5120] 7.8 us, x [55296, 5120] 41.0 (6.9 TB/s), 16 tokens 9.2 and
-// 47.8; in tiles 13.1 and 50.9, and 13.3 and 52.1 (nn has no such form: W's rows are what it contracts)
-inline bool by_rows(int64_t M, int32_t nn) { return !nn && M <= 16; }
 
 template <typename T, bool NN, int STAGES>
 inline void launch_tiles(const GemmArgs &g, hipStream_t stream) {
@@ -607,13 +632,22 @@ inline void launch_tiles(const GemmArgs &g, hipStream_t stream) {
     if (rest) k_fp8_join<T, NN><<<dim3(T::results, (unsigned)rest), block, 0, stream>>>(g);
 }
 
+template <int NW, int RT>
+inline void launch_rows(const GemmArgs &g, hipStream_t stream) {
+    const dim3 grid((unsigned)g.tiles_j), block(NW * kWave);
+    if (g.M <= 8) k_fp8_rows<8, NW, 3, RT><<<grid, block, 0, stream>>>(g);
+    else k_fp8_rows<16, NW, 3, RT><<<grid, block, 0, stream>>>(g);
+}
+
 template <bool NN>
 inline void launch_gemm(const GemmPlan &p, const GemmArgs &g, hipStream_t stream) {
     switch (p.kind) {
     case 0: return launch_tiles<Tile<256, 256, 4>, NN, 2>(g, stream);
     case 1: return launch_tiles<Tile<128, 256, 4>, NN, 3>(g, stream);
     case 2: return launch_tiles<Tile<128, 128, 4>, NN, 4>(g, stream);
-    default: return launch_tiles<Tile<64, 128, 4>, NN, 5>(g, stream);
+    case 3: return launch_tiles<Tile<64, 128, 4>, NN, 5>(g, stream);
+    case kRowsFrom: return launch_rows<4, 2>(g, stream);
+    default: return launch_rows<8, 1>(g, stream);
     }
 }
 
@@ -624,8 +658,7 @@ using namespace pulse;
 extern "C" {
 
 int64_t pulse_fp8_gemm_ws_size(int64_t M, int64_t J, int64_t C, int32_t nn) {
-    if (by_rows(M, nn)) return 0;
-    const GemmPlan p = gemm_plan(M, J, C);
+    const GemmPlan p = gemm_plan(M, J, C, nn);
     return (p.tiles_m * p.tiles_j - p.whole) * p.shares * p.bm * p.bj * 4;
 }
 
@@ -633,19 +666,12 @@ int pulse_launch_fp8_gemm(const uint8_t *x, const float *sx, const uint8_t *w, c
                           int32_t nn, int64_t M, int64_t n, int64_t k, uint16_t *y, int64_t ldy, void *ws,
                           hipStream_t stream) {
     const int64_t J = nn ? k : n, C = nn ? n : k, gk = (k + GB - 1) / GB;
-    const GemmPlan p = gemm_plan(M, J, C);
+    const GemmPlan p = gemm_plan(M, J, C, nn);
     const GemmArgs g{x, w, sx, sw, bias, y, static_cast<f32x4 *>(ws), ldy, (int32_t)M, (int32_t)J, (int32_t)C, (int32_t)k,
                      (int32_t)((C + GB - 1) / GB), nn ? 1 : (int32_t)gk, nn ? (int32_t)gk : 1, (int32_t)p.tiles_m,
                      (int32_t)p.tiles_j, (int32_t)((C + GB - 1) / GB), p.whole, p.shares, p.per};
-    if (by_rows(M, nn)) {
-        const dim3 grid((unsigned)((n + 31) / 32)), block(256);
-        if (M <= 8) k_fp8_rows<8, 4, 3, 2><<<grid, block, 0, stream>>>(g);
-        else k_fp8_rows<16, 4, 3, 2><<<grid, block, 0, stream>>>(g);
-    } else if (nn) {
-        launch_gemm<true>(p, g, stream);
-    } else {
-        launch_gemm<false>(p, g, stream);
-    }
+    if (nn) launch_gemm<true>(p, g, stream);
+    else launch_gemm<false>(p, g, stream);
     return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 }

@@ -44,9 +44,11 @@ def check(got, y, e):
 # one token to many, odd rows and columns, contractions that end inside a step, each variant's edges
 NT = [(1, 1, 16), (1, 16, 128), (1, 130, 144), (1, 512, 4096), (2, 257, 1040), (3, 100, 272), (5, 640, 2000), (7, 1000, 5120),
       (16, 128, 256), (17, 300, 640), (31, 77, 1936), (33, 136, 4096), (48, 256, 1264), (64, 384, 1024), (65, 129, 400), (96, 513, 2560),
-      (128, 128, 128), (129, 255, 272), (200, 700, 1552), (257, 300, 528), (640, 1001, 336), (1030, 2050, 400), (300, 3500, 656), (4100, 2050, 272), (2049, 4100, 128)]
+      (128, 128, 128), (129, 255, 272), (200, 700, 1552), (257, 300, 528), (640, 1001, 336), (1030, 2050, 400), (300, 3500, 656), (4100, 2050, 272), (2049, 4100, 128),
+      (1, 7168, 1040), (8, 5136, 2064), (9, 5136, 2064), (16, 4112, 1040), (12, 300, 5136), (1, 128, 27200), (16, 130, 9232), (100, 128, 9232)]
 NN = [(1, 16, 16), (1, 128, 128), (1, 144, 272), (2, 1040, 256), (5, 640, 2000), (16, 272, 144), (33, 4096, 136 + 8), (64, 1024, 384),
-      (65, 400, 144), (100, 2560, 528), (129, 272, 256), (257, 528, 304), (640, 336, 1008), (1030, 400, 2064), (300, 656, 3504), (4100, 272, 2064), (2049, 128, 4112)]
+      (65, 400, 144), (100, 2560, 528), (129, 272, 256), (257, 528, 304), (640, 336, 1008), (1030, 400, 2064), (300, 656, 3504), (4100, 272, 2064), (2049, 128, 4112),
+      (1, 27200, 128), (20, 9232, 144)]
 
 
 @pytest.mark.parametrize("m,n,k", NT)
@@ -152,7 +154,8 @@ def test_no_tokens():
 TILES = [(900, 8208, 144), (2000, 8208, 528), (900, 5136, 8208), (4100, 1000 + 8, 144), (1500, 1008, 8208), (2000, 8208, 144),
          (250, 8208, 8208), (250, 8208, 144), (1500, 512, 4112), (70, 4112, 8208), (4100, 4112, 144), (70, 256, 144), (70, 8208, 144),
          (250, 8208, 4112), (4099, 4112, 1040), (4099, 8208, 528), (40, 16400, 4112), (40, 33040, 144), (70, 33040, 4112),
-         (70, 16400, 144), (70, 16400, 4112), (40, 33040, 1040), (40, 144, 144), (40, 16400, 144)]
+         (70, 16400, 144), (70, 16400, 4112), (40, 33040, 1040), (40, 144, 144), (40, 16400, 144), (900, 16400, 528), (130, 33040, 4112),
+         (130, 16400, 4112), (120, 16400, 4112), (70, 144, 4112), (20, 144, 1040), (70, 2064, 4112)]
 
 
 @pytest.mark.parametrize("form", ["nt", "nn"])
