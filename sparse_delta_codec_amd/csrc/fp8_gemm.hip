@@ -368,6 +368,9 @@ __device__ __forceinline__ void multiply(const uint8_t *w, int wj, const i32x8 &
 }
 
 // STAGES buffers of a step: it is loaded STAGES - 1 steps before it is multiplied.
+// 8192 x [5120, 55296] takes 2200 us (2110 TFLOP/s); 2093 with all of it in L2, 1747 with nothing
+// loaded: matrix unit and loads take turns for a fifth of the time.  With few tokens the loads are all:
+// 96 x [5120, 55296] 60 us, W at 4.8 TB/s with x beside it, through the same path into LDS.
 // (Eight waves: with four, and all registers for one wave a SIMD, the compiler puts products
 // into accumulation registers, which an FMA cannot read.)
 // ONCE: one row of tiles, so W is read once and goes past the caches (96 x [5120, 27648] 44.0 and
@@ -562,12 +565,16 @@ struct GemmPlan {
 // The form is the one that takes the least time by this estimate.  Microseconds of a step while
 // the chip is full, measured with 256 tiles of 64 steps, or, where one row of tiles reads W once,
 // with 55296 x 5120 and 5120 x 27648; a second launch, a share in it and a float32 value written and
-// read again as measured for the shared tiles of 1 to 512 rows.  By kind:
-// [2048, 8192] x [8192, 4096] 94.6, 80.2, 101 and 147 us, 4096 rows 129, 163, 204, 292;
-// [96, 5120] x [5120, 55296] -, 60.0, 75.9, 99.0; [96, 27648] x [27648, 5120] -, 36.7, 40.4, 50.7;
-// 24 rows of that -, 33.7, 35.7, 29.3; [128, 14336] x [14336, 4096] -, 29.8, 24.5, 27.2.  (256 x 128 in place of 128 x 256: 85.9 and 165 us of
-// 2048 and 4096 rows, 104 of 96 rows x [5120, 55296], whose tiles are half empty then.)  Shares:
-// one row x [27200, 128] in 213 of them 58.3 us, in 43 12.1; 100 rows 35.2 and 13.5.
+// read again as measured for the shared tiles of 1 to 512 rows.  By kind, in microseconds:
+//   [2048, 8192] x [8192, 4096]   94.6   80.2  101   147
+//   [4096, 8192] x [8192, 4096]  129    163    204   292
+//   [96, 5120] x [5120, 55296]     -     60.0   75.9  99.0
+//   [96, 27648] x [27648, 5120]    -     36.7   40.4  50.7
+//   [24, 27648] x [27648, 5120]    -     33.7   35.7  29.3
+//   [128, 14336] x [14336, 4096]   -     29.8   24.5  27.2
+// (256 x 128 in place of 128 x 256: 85.9 and 165 of 2048 and 4096 rows, 104 of 96 rows x
+// [5120, 55296], whose tiles are half empty then.)  Shares: one row x [27200, 128] in 213 of them
+// 58.3 us, in 43 12.1; 100 rows 35.2 and 13.5.
 struct GemmKind {
     int bm, bj;
     float step, once;
@@ -576,11 +583,14 @@ struct GemmKind {
 constexpr GemmKind kKinds[] = {{256, 256, 2.03f, 2.03f}, {128, 256, 1.28f, 1.45f}, {128, 128, 0.81f, 0.95f}, {64, 128, 0.62f, 0.74f}};
 
 // k_fp8_rows: rows of W and waves of a workgroup; microseconds of a turn (a step of each wave) with
-// up to 8 tokens and up to 16.  W comes in at 6.9 and 6.0 TB/s at most.  Microseconds
-// in 32 rows, in 16 rows and in tiles: one token x [7168, 5120] 7.8, 7.8, 12.8; [4096, 14336] 13.3,
-// 10.9, 16.6; [5120, 27648] 24.4, 28.6, 28.1; [55296, 5120] 41.0, 40.7, 50.9; [128, 27200] 25.2,
-// 14.7, 12.1; 16 tokens 9.2, 11.8, 13.3; 17.8, 13.9, 17.1; 33.0, 44.2, 28.8; 47.8, 57.6, 52.1; 36.0, 24.6, 11.4.
-// (nn has no such form: W's rows are what it contracts.)
+// up to 8 tokens and up to 16.  W comes in at 6.9 and 6.0 TB/s at most.  Microseconds in 32 rows, in 16
+// rows and in tiles (nn has no such form: W's rows are what it contracts):
+//                    one token            16 tokens
+//   [7168, 5120]      7.8   7.8  12.8      9.2  11.8  13.3
+//   [4096, 14336]    13.3  10.9  16.6     17.8  13.9  17.1
+//   [5120, 27648]    24.4  28.6  28.1     33.0  44.2  28.8
+//   [55296, 5120]    41.0  40.7  50.9     47.8  57.6  52.1
+//   [128, 27200]     25.2  14.7  12.1     36.0  24.6  12.7
 struct RowsKind {
     int rows, waves;
     float turn[2];
