@@ -767,7 +767,7 @@ int pulse_rms_norm_backward(const uint16_t *s, int64_t lds, const uint16_t *weig
 int fp8_group_quant(const uint16_t *x, int64_t ldx, int64_t n_tokens, int64_t cols, int32_t glu, uint8_t *codes,
                     float *scales, hipStream_t stream) {
     if (n_tokens < 0 || cols < 8 || cols % 8 != 0 || (glu != 0 && glu != 1)) return PULSE_EINVAL;
-    if (n_tokens > kMaxRows || cols > kMaxQuantCols || n_tokens * ((cols + 511) / 512) / 16 >= kMaxRows) return PULSE_ERANGE;
+    if (n_tokens > kMaxRows || cols > kMaxQuantCols || n_tokens * ((cols + 511) / 512) / 8 >= kMaxRows) return PULSE_ERANGE;
     if (n_tokens == 0) return PULSE_OK;
     if (!x || !codes || !scales || bad_stride(ldx, glu ? 2 * cols : cols)) return PULSE_EINVAL;
     if (!aligned16(x) || !aligned16(codes)) return PULSE_EALIGN;

@@ -238,8 +238,9 @@ struct GroupQuantArgs {
     int32_t cols, per_row;
 };
 
-// pieces of a wave, all read before the first is worked on: 8191 x 28672 123 us (5.7 TB/s)
-constexpr int GQ = 4;
+// pieces of a wave, all read before the first is worked on.  With 1, 2 and 4: 8191 x 28672 129, 119
+// (5.9 TB/s) and 123 us, 1024 x 5120 5.3, 5.7 and 6.2, 96 x 27648 with silu 5.2, 5.3 and 6.2.
+constexpr int GQ = 2;
 
 // A wave takes GQ pieces of 512 columns, one after the other through the rows; GLU: silu(x[c]) x[cols + c].
 template <bool GLU>
