@@ -655,9 +655,7 @@ inline void launch_gemm(const GemmPlan &p, const GemmArgs &g, hipStream_t stream
     case 0: return launch_tiles<Tile<256, 256, 4>, NN, 2>(g, stream);
     case 1: return launch_tiles<Tile<128, 256, 4>, NN, 3>(g, stream);
     case 2: return launch_tiles<Tile<128, 128, 4>, NN, 4>(g, stream);
-    case 3: return launch_tiles<Tile<64, 128, 4>, NN, 5>(g, stream);
-    case kRowsFrom: return launch_rows<4, 2>(g, stream);
-    default: return launch_rows<8, 1>(g, stream);
+    default: return launch_tiles<Tile<64, 128, 4>, NN, 5>(g, stream);
     }
 }
 
@@ -680,7 +678,9 @@ int pulse_launch_fp8_gemm(const uint8_t *x, const float *sx, const uint8_t *w, c
     const GemmArgs g{x, w, sx, sw, bias, y, static_cast<f32x4 *>(ws), ldy, (int32_t)M, (int32_t)J, (int32_t)C, (int32_t)k,
                      (int32_t)((C + GB - 1) / GB), nn ? 1 : (int32_t)gk, nn ? (int32_t)gk : 1, (int32_t)p.tiles_m,
                      (int32_t)p.tiles_j, (int32_t)((C + GB - 1) / GB), p.whole, p.shares, p.per};
-    if (nn) launch_gemm<true>(p, g, stream);
+    if (p.kind == kRowsFrom) launch_rows<4, 2>(g, stream);
+    else if (p.kind > kRowsFrom) launch_rows<8, 1>(g, stream);
+    else if (nn) launch_gemm<true>(p, g, stream);
     else launch_gemm<false>(p, g, stream);
     return hipGetLastError() == hipSuccess ? 0 : -5;
 }
