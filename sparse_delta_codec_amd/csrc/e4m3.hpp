@@ -61,15 +61,24 @@ __device__ __forceinline__ u32x2 group_codes(const float (&x)[8], float *scale) 
 }
 
 // g / (1 + e^-g) in float32, off by a few units of 2^-24: the exponential as 2^t 2^d with t the
-// rounded product and d what its rounding left out (up to 2^-18 at |g| = 80).
+// rounded product and d what its rounding left out (up to 2^-18 at |g| = 80).  Gates below -44.4 have
+// 2^-64 of the exponential, beside which 1 is nothing, and give that factor back to the quotient:
+// the exponential itself passes float32's range at -88.7, and its reciprocal is below the normal
+// numbers, where the instruction gives zero, from -87.3 on, while the quotient is one down to -91.8.
+// (FAR = false: for gates from kFarGate on, without that part.)
+constexpr float kFarGate = -44.0f;
+
+template <bool FAR = true>
 __device__ __forceinline__ float silu(float g) {
     constexpr float kLog2e = 1.44269502162933349609375f, kRest = 1.925963033500011079e-8f, kLn2 = 0.693147182464599609375f;
     const float t = g * -kLog2e;
     const float d = __builtin_fmaf(g, -kRest, __builtin_fmaf(g, -kLog2e, -t));
-    const float p = __builtin_amdgcn_exp2f(t);
-    // beyond, e^-g is nothing beside 1 or past float32, and d may be inf - inf
-    const float e = fabsf(t) < 128.0f ? __builtin_fmaf(p, d * kLn2, p) : p;
-    return g * __builtin_amdgcn_rcpf(1.0f + e);
+    const bool far = FAR && t > 64.0f;
+    const float p = __builtin_amdgcn_exp2f(far ? t - 64.0f : t);  // (the difference is exact below 192)
+    // beyond, e^-g is nothing beside 1 or the quotient is zero, and d may be inf - inf
+    const float e = fabsf(t) < 192.0f ? __builtin_fmaf(p, d * kLn2, p) : p;
+    const float q = g * __builtin_amdgcn_rcpf(far ? e : 1.0f + e);
+    return far ? q * 5.42101086242752217e-20f : q;  // 2^-64
 }
 
 // eight BF16 of 16 bytes as float32
