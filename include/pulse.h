@@ -806,7 +806,9 @@ int fp8_group_quant(const uint16_t *x, int64_t ldx, int64_t n_tokens, int64_t co
  * 2^-13 of their largest, and everything else is added in float32.
  *   x, x_scales  quantised rows (dense: row stride k, or n).
  *   bias   [n] BF16 (PULSE_GEMM_NT, else ignored), or NULL.
- *   ws     fp8_block_gemm_ws_bytes(m, n, k, form); it may hold anything before a call. */
+ *   ws     fp8_block_gemm_ws_bytes of this m or any larger one (it does not fall as m grows), and
+ *          this n, k and form; it may hold anything before a call.  A call that does not share its
+ *          contraction takes none. */
 #define PULSE_GEMM_NT 0
 #define PULSE_GEMM_NN 1
 int64_t fp8_block_gemm_ws_bytes(int64_t m, int64_t n, int64_t k, int32_t form);

@@ -1162,7 +1162,7 @@ def _form(form):
 
 
 def fp8_gemm_workspace(m, n, k, form="nt", device="cuda"):
-    """A workspace for fp8_block_gemm of m rows with weights [n, k]."""
+    """A workspace for fp8_block_gemm of up to m rows with weights [n, k]."""
     return _scratch(_lib.fp8_block_gemm_ws_bytes(m, n, k, _form(form)), "fp8_block_gemm_ws_bytes", device)
 
 

@@ -90,7 +90,8 @@ int pulse_launch_rms_norm_backward(const uint16_t *, int64_t, const uint16_t *, 
                                    const uint16_t *, int64_t, uint16_t *, int64_t, float *, int32_t, int64_t, int64_t,
                                    void *, hipStream_t);
 int pulse_launch_group_quant(const uint16_t *, int64_t, int64_t, int64_t, int32_t, uint8_t *, float *, hipStream_t);
-int64_t pulse_fp8_gemm_ws_size(int64_t M, int64_t J, int64_t C, int32_t nn);
+int64_t pulse_fp8_gemm_ws_size(int64_t M, int64_t J, int64_t C);
+int32_t pulse_fp8_gemm_shares(int64_t M, int64_t J, int64_t C, int32_t nn);
 int pulse_launch_fp8_gemm(const uint8_t *, const float *, const uint8_t *, const float *, const uint16_t *, int32_t,
                           int64_t, int64_t, int64_t, uint16_t *, int64_t, void *, hipStream_t);
 int64_t pulse_moe_ws_size(int64_t T, int64_t H, int64_t I, int64_t top_k);
@@ -777,7 +778,7 @@ int fp8_group_quant(const uint16_t *x, int64_t ldx, int64_t n_tokens, int64_t co
 int64_t fp8_block_gemm_ws_bytes(int64_t m, int64_t n, int64_t k, int32_t form) {
     const int rc = check_gemm_sizes(m, n, k, form);
     if (rc != PULSE_OK) return rc;
-    return m == 0 ? 0 : pulse_fp8_gemm_ws_size(m, form == PULSE_GEMM_NN ? k : n, form == PULSE_GEMM_NN ? n : k, form);
+    return m == 0 ? 0 : pulse_fp8_gemm_ws_size(m, form == PULSE_GEMM_NN ? k : n, form == PULSE_GEMM_NN ? n : k);
 }
 
 int fp8_block_gemm(const uint8_t *x, const float *x_scales, const uint8_t *w, const float *w_scales,
@@ -789,8 +790,9 @@ int fp8_block_gemm(const uint8_t *x, const float *x_scales, const uint8_t *w, co
     if (m == 0) return PULSE_OK;
     if (!x || !x_scales || !w || !w_scales || !y || ldy < j) return PULSE_EINVAL;
     if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(ws)) return PULSE_EALIGN;
-    const size_t need = (size_t)pulse_fp8_gemm_ws_size(m, j, form == PULSE_GEMM_NN ? n : k, form);
-    if (need && (!ws || ws_bytes < need)) return PULSE_EWORKSPACE;
+    const int64_t c = form == PULSE_GEMM_NN ? n : k;
+    if (pulse_fp8_gemm_shares(m, j, c, form) > 1 && (!ws || ws_bytes < (size_t)pulse_fp8_gemm_ws_size(m, j, c)))
+        return PULSE_EWORKSPACE;
     return pulse_launch_fp8_gemm(x, x_scales, w, w_scales, bias, form, m, n, k, y, ldy, ws, stream);
 }
 

@@ -633,6 +633,20 @@ inline GemmPlan gemm_plan(int64_t M, int64_t J, int64_t C, bool nn) {
     return best;
 }
 
+// Bytes that hold the shared tiles of every plan for up to M rows: at most 128 tiles, whose shares
+// are at most 256 and no more than their steps, of the largest kind (256 rows only beyond 128: below, its plan
+// is that of 128 rows at a longer step).  The plans themselves rise and fall with M.
+inline int64_t gemm_ws_bound(int64_t M, int64_t J, int64_t C) {
+    const int64_t steps = (C + GB - 1) / GB;
+    int64_t most = 0;
+    for (const GemmKind &k : kKinds) {
+        if (steps < 2 || (k.bm > 128 && M <= 128)) continue;
+        const int64_t tiles = std::min<int64_t>((M + k.bm - 1) / k.bm * ((J + k.bj - 1) / k.bj), kUnits / 2);
+        most = std::max(most, std::min<int64_t>(kUnits, tiles * steps) * k.bm * k.bj * 4);
+    }
+    return most;
+}
+
 template <typename T, bool NN, int STAGES>
 inline void launch_tiles(const GemmArgs &g, hipStream_t stream) {
     const int64_t rest = (int64_t)g.tiles_m * g.tiles_j - g.whole;
@@ -665,10 +679,9 @@ using namespace pulse;
 
 extern "C" {
 
-int64_t pulse_fp8_gemm_ws_size(int64_t M, int64_t J, int64_t C, int32_t nn) {
-    const GemmPlan p = gemm_plan(M, J, C, nn);
-    return (p.tiles_m * p.tiles_j - p.whole) * p.shares * p.bm * p.bj * 4;
-}
+int64_t pulse_fp8_gemm_ws_size(int64_t M, int64_t J, int64_t C) { return gemm_ws_bound(M, J, C); }
+
+int32_t pulse_fp8_gemm_shares(int64_t M, int64_t J, int64_t C, int32_t nn) { return gemm_plan(M, J, C, nn).shares; }
 
 int pulse_launch_fp8_gemm(const uint8_t *x, const float *sx, const uint8_t *w, const float *sw, const uint16_t *bias,
                           int32_t nn, int64_t M, int64_t n, int64_t k, uint16_t *y, int64_t ldy, void *ws,
