@@ -13,15 +13,15 @@ __device__ __forceinline__ uint32_t lds_at(const void *p) {
 }
 __device__ __forceinline__ void load_lds16(uint32_t lds, const void *base, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory");
+                 : "m0", "memory");
 }
 __device__ __forceinline__ void load_lds16_once(uint32_t lds, const void *base, uint32_t off) {  // not read again
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory");
+                 : "m0", "memory");
 }
 __device__ __forceinline__ void load_lds4(uint32_t lds, const void *base, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory");
+                 : "m0", "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
