@@ -11,6 +11,11 @@ namespace pulse {
 __device__ __forceinline__ uint32_t lds_at(const void *p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)p;
 }
+
+// M0 is named as overwritten, so that the compiler expects no value of its own there behind such a
+// load; it warns of that, for M0 is not one of the registers in which it keeps a program's values.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds16(uint32_t lds, const void *base, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
                  : "m0", "memory");
@@ -23,6 +28,8 @@ __device__ __forceinline__ void load_lds4(uint32_t lds, const void *base, uint32
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base)
                  : "m0", "memory");
 }
+#pragma clang diagnostic pop
+
 template <int N>
 __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
