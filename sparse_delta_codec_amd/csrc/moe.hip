@@ -19,6 +19,7 @@
 #include "lds_load.hpp"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace pulse {
 
@@ -88,6 +89,23 @@ __global__ __launch_bounds__(256) void k_moe_route(const float *__restrict__ log
     if (lane < top_k) {
         ids[(int64_t)t * top_k + lane] = mine;
         weights[(int64_t)t * top_k + lane] = mine >= 0 ? expf(chosen - most) / sum * scale : 0.0f;
+    }
+}
+
+// f with the logits of a lane as a constant: the least of these that hold E, for each choice goes over
+// them all.  Microseconds of 1 and of 65536 tokens, top 8, in this one and in the next: 2 (E = 128) 3.1 and 3.4,
+// 31 and 38; 4 (256) 3.6 and 4.1, 42 and 49; 6 (384) 4.4 and 4.5, 53 and 59; 8 (512) 4.8 and, in 16, 6.5, 63 and 98.
+template <typename F>
+inline void with_logits(int64_t E, F &&f) {
+    static_assert(ME_EXPERTS <= 16 * kWave, "the largest holds them all");
+    switch ((E + 2 * kWave - 1) / (2 * kWave)) {
+    case 1: return f(std::integral_constant<int, 2>{});
+    case 2: return f(std::integral_constant<int, 4>{});
+    case 3: return f(std::integral_constant<int, 6>{});
+    case 4: return f(std::integral_constant<int, 8>{});
+    case 5:
+    case 6: return f(std::integral_constant<int, 12>{});
+    default: return f(std::integral_constant<int, 16>{});
     }
 }
 
@@ -588,9 +606,10 @@ int64_t pulse_moe_ws_size(int64_t T, int64_t H, int64_t I, int64_t top_k) { retu
 int pulse_launch_moe_route(const float *logits, int64_t ld, int64_t T, int64_t E, int32_t top_k, int32_t over_all,
                            float scale, int32_t *ids, float *weights, hipStream_t stream) {
     const dim3 grid((unsigned)((T + 3) / 4)), block(256);
-    if (E <= 128) k_moe_route<2><<<grid, block, 0, stream>>>(logits, ld, (int32_t)T, (int32_t)E, top_k, over_all, scale, ids, weights);
-    else if (E <= 384) k_moe_route<6><<<grid, block, 0, stream>>>(logits, ld, (int32_t)T, (int32_t)E, top_k, over_all, scale, ids, weights);
-    else k_moe_route<16><<<grid, block, 0, stream>>>(logits, ld, (int32_t)T, (int32_t)E, top_k, over_all, scale, ids, weights);
+    with_logits(E, [&](auto per) {
+        k_moe_route<decltype(per)::value>
+            <<<grid, block, 0, stream>>>(logits, ld, (int32_t)T, (int32_t)E, top_k, over_all, scale, ids, weights);
+    });
     return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 
