@@ -764,8 +764,8 @@ int pulse_lora_backward(const uint16_t *x, int64_t ldx, const uint16_t *dy, int6
  * T is below 2^24.  Outputs overlap no other buffer of their call. */
 
 /* y = s rstd weight with rstd = 1 / sqrt(mean(s^2) + eps) of each row, s = x, or with a
- * residual s = bf16(x + residual), which is written back to it.  Sums are held in float32
- * (squares past its range make a row of zeros or NaN, as the formula does there).
+ * residual s = bf16(x + residual), which is written back to it.  Sums are held in float32: a
+ * row whose squares add up past its range has rstd 0 and is zeros, NaN in the places of infinities.
  *   x         [T][ldx] (read); cols a multiple of 8 up to 16384.
  *   weight    [cols] BF16.      eps  > 0, as float32 too.
  *   residual  [T][ldr], updated, or NULL.
@@ -791,19 +791,22 @@ int pulse_rms_norm_backward(const uint16_t *s, int64_t lds, const uint16_t *weig
                             int64_t lddx, float *dweight, int32_t accumulate, int64_t n_tokens, int64_t cols,
                             void *ws, size_t ws_bytes, hipStream_t stream);
 
-/* Rows quantised as above: x [T][ldx], cols a multiple of 8 up to 2^24; with glu = 1 x is
- * [gate, up] of 2 cols columns and the values are gate / (1 + e^-gate) * up, in float32. */
+/* Rows quantised as above: x [T][ldx], cols a multiple of 8 up to 2^24, T ceil(cols/512) below
+ * 2^27 - 8; with glu = 1 x is [gate, up] of 2 cols columns and the values are
+ * gate / (1 + e^-gate) * up, the quotient and the product each in float32. */
 int fp8_group_quant(const uint16_t *x, int64_t ldx, int64_t n_tokens, int64_t cols, int32_t glu, uint8_t *codes,
                     float *scales, hipStream_t stream);
 
 /* Quantised rows times weights in 128 x 128 blocks (fp8_block_quant's w [n][k] and scales
- * [ceil(n/128)][ceil(k/128)]), each block's sum multiplied by both scales in float32:
+ * [ceil(n/128)][ceil(k/128)]), each block's sum multiplied by the float32 product of both
+ * scales (which is to lie within float32's normal range: below 2^-126 it has fewer bits or is
+ * zero, past 2^128 it is Inf, and NaN where the block's sum is zero):
  *   PULSE_GEMM_NT  y [m][n] = x [m][k] w^T + bias: a projection; k a multiple of 16.
  *   PULSE_GEMM_NN  y [m][k] = x [m][n] w: the gradient of a projection's input, from that of
  *                  its output; n and k multiples of 16.
- * n and k up to 2^22, y up to 2^23 tiles of 64 x 128.  y [m][ldy] is rounded to BF16 once; ldy >= its columns, any.  The matrix
- * instructions add up eight neighbouring products at a time, each cut to a multiple of about
- * 2^-13 of their largest, and everything else is added in float32.
+ * n and k up to 2^22, y fewer than 2^23 tiles of 64 x 128.  y [m][ldy] is rounded to BF16 once;
+ * ldy >= its columns, any.  The matrix instructions add up eight neighbouring products at a time,
+ * each cut to a multiple of about 2^-13 of their largest, and everything else is added in float32.
  *   x, x_scales  quantised rows (dense: row stride k, or n).
  *   bias   [n] BF16 (PULSE_GEMM_NT, else ignored), or NULL.
  *   ws     fp8_block_gemm_ws_bytes of this m or any larger one (it does not fall as m grows), and
@@ -834,8 +837,8 @@ int pulse_moe_route(const float *logits, int64_t ld, int64_t n_tokens, int64_t e
  * chosen experts' weights.  x enters as BF16, h as the sum of two BF16 (2^-16 of itself is
  * left out), weights as code times scale; sums are held in float32 and y is rounded once.
  *   x       [T][ldx] BF16, ldx up to 2^20.   hidden and inter multiples of 16 up to 65536.
- *   ids     [T][top_k] int32 (any expert any number of times; -1 for none): y of a token
- *           without an expert is zero.  weights [T][top_k] float32.
+ *   ids     [T][top_k] int32, top_k <= experts (any expert any number of times; -1 for none): y of
+ *           a token without an expert is zero.  weights [T][top_k] float32.
  *   up      [experts][2 inter][hidden] codes, gate's rows first, and scales
  *           [experts][ceil(2 inter / 128)][ceil(hidden / 128)]; down [experts][hidden][inter]
  *           and scales [experts][ceil(hidden / 128)][ceil(inter / 128)]: fp8_block_quant's
