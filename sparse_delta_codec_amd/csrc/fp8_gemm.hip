@@ -368,9 +368,11 @@ __device__ __forceinline__ void multiply(const uint8_t *w, int wj, const i32x8 &
 }
 
 // STAGES buffers of a step: it is loaded STAGES - 1 steps before it is multiplied.
-// 8192 x [5120, 55296] takes 2200 us (2110 TFLOP/s); 2093 with all of it in L2, 1747 with nothing
-// loaded: matrix unit and loads take turns for a fifth of the time.  With few tokens the loads are all:
-// 96 x [5120, 55296] 60 us, W at 4.8 TB/s with x beside it, through the same path into LDS.
+// 8192 x [5120, 55296] takes 2200 to 2280 us (2030 to 2110 TFLOP/s): 27 rounds of 40 steps of 2.0 to 2.1 us, of which
+// the instructions take 1.4 at the rate that products of this card reach.  A unit's registers and LDS hold one such
+// workgroup, so that nothing runs beside its waits, its barrier and a step's first reads.
+// With few tokens the loads are all: 96 x [5120, 55296] 60 us, W at 4.8 TB/s with x beside it, through the
+// same path into LDS.
 // (Eight waves: with four, and all registers for one wave a SIMD, the compiler puts products
 // into accumulation registers, which an FMA cannot read.)
 // ONCE: one row of tiles, so W is read once and goes past the caches (96 x [5120, 27648] 44.0 and

@@ -7,7 +7,7 @@
 // A few tokens reach many experts, so the work is to read each of these experts' codes
 // once, at HBM's rate.  Pairs (a token and a choice) are put in order by expert, up to NX of
 // an expert make an item, and an item's workgroups read the expert's rows past the registers
-// into LDS, 128 or 256 columns a step and two or three steps ahead; from there a wave takes
+// into LDS, 128 or 256 columns a step and one or two steps ahead; from there a wave takes
 // them as rows of the matrix instruction, turned into BF16 (exactly: E4M3 has four bits), with
 // the pairs as its columns.  Outputs of the pairs are added up per token in the order of its
 // choices, so that a result does not hang on which workgroup was first.

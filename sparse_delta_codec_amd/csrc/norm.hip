@@ -7,8 +7,8 @@
 //   s = bf16(x + residual), or x         (what later layers and the backward pass read)
 //   r = 1 / sqrt(mean(s^2) + eps),  y = s r w
 //   dx = r (dy w - s r mean(dy w s r)) + dres,  dw = sum over rows of dy s r
-// Every byte is read and written once, so the large calls are bound by HBM (5.5 TB/s where a
-// copy has 5.1: more is read than written) and the small ones by the launch and the chain
+// Every byte is read and written once, so the large calls are bound by HBM (5.2 to 5.5 TB/s where
+// a copy has 5.1: more is read than written) and the small ones by the launch and the chain
 // load - sum - barrier - store.  A row stays in the registers of one workgroup between its sum
 // and its output: 8 columns (16 bytes) a lane, so that 16 lanes hold a quantisation group and
 // 64 lanes read 1024 contiguous bytes.
@@ -295,9 +295,9 @@ __global__ __launch_bounds__(256) void k_group_quant(GroupQuantArgs g) {
 }
 
 // Waves of a row's workgroup and pieces of a wave: with many rows few waves, of which more rows
-// are under way at once, with few rows many.  With codes and a residual, up to 4 and 16 waves:
-// 512 x 5120 7.1 and 7.3 us (the launch's own time), 1024 x 5120 9.4 and 10.6, 8192 x 5120 53.0 and
-// 57.0 (5.5 TB/s), 8192 x 16384 170 and 165.
+// are under way at once, with few rows many.  With codes and a residual, new rows for each call, up to 4 and
+// 16 waves: 512 x 5120 8.2 and 8.1 us (the call's own time), 1024 x 5120 11.8 and 13.0, 4099 x 4096 24.8
+// and 26.8, 8192 x 5120 56.9 and 57.1 (5.2 TB/s), 8192 x 16384 172 and 168.
 struct NormShape {
     int waves, pieces;
 };
