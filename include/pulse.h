@@ -835,7 +835,7 @@ int pulse_moe_route(const float *logits, int64_t ld, int64_t n_tokens, int64_t e
 /* y[t] = sum over a token's choices j, e = ids[t][j], of weights[t][j] down_e h,
  * h = silu(gate_e x[t]) * (up_e x[t]), for a few tokens: the time is that of reading the
  * chosen experts' weights.  x enters as BF16, h as the sum of two BF16 (2^-16 of itself is
- * left out), weights as code times scale; sums are held in float32 and y is rounded once.
+ * left out, or 2^-134 where that is more), weights as code times scale; sums are held in float32 and y is rounded once.
  *   x       [T][ldx] BF16, ldx up to 2^20.   hidden and inter multiples of 16 up to 65536.
  *   ids     [T][top_k] int32, top_k <= experts (any expert any number of times; -1 for none): y of
  *           a token without an expert is zero.  weights [T][top_k] float32.
