@@ -406,6 +406,8 @@ __global__ __launch_bounds__((MoeStage<UP, NX, FEW>::MW * kWave), 2) void k_moe_
         if (place >= np) continue;
         const int pair = pair_of(place);
         if constexpr (UP) {
+            // two BF16 hold 16 bits of h, 2^-8 of what y's rounding leaves; one would be as coarse as y itself, and
+            // a third would take down's matrix instructions and x's place in LDS half as often again
             float h[4], rest[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
