@@ -128,3 +128,20 @@ def test_a_stride_of_2_20():
     y, st = torch.empty((3, 272), dtype=torch.bfloat16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
     pulse.pulse_moe_forward(wide[:, :272], *map(dev, args[1:]), y, st, pulse.moe_workspace(3, 272, 144, 4, 2))
     np.testing.assert_array_equal(y.double().cpu().numpy(), clean)
+
+
+@pytest.mark.parametrize("h,i", [(65536, 16), (16, 65536)])
+def test_all_pairs_at_the_widest(h, i):
+    """1024 tokens with 8 of 16 experts: the first and the last tokens' results are those of them alone."""
+    t, e, k = 1024, 16, 8
+    args = list(layer(8, h, i, e, k, 24))
+    g = np.random.default_rng(25)
+    args[0] = ref.bf16(g.standard_normal((t, h), dtype=np.float32))
+    args[1] = np.stack([g.permutation(e)[:k] for _ in range(t)]).astype(np.int32)
+    args[2] = g.uniform(0.1, 1, (t, k)).astype(np.float32)
+    got = forward(*args)
+    for rows in (slice(0, 4), slice(t - 4, t)):
+        some = [a[rows] for a in args[:3]] + args[3:]
+        alone = forward(*some)
+        np.testing.assert_array_equal(got[rows], alone)
+        check(alone, *ref.moe(*some))
